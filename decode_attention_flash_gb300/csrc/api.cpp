@@ -204,6 +204,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   const bool fp8 = p.kv_dtype != DA_DTYPE_BF16;
   const bool token_scale = p.kv_dtype == DA_DTYPE_FP8_E4M3_TOKEN_SCALE;
   const bool int4 = p.kv_dtype == DA_DTYPE_INT4_GROUPS;  // takes the f16 (fp8) kernel path
+  const bool fp4 = p.kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS;  // fp4_split.cu: no tensor maps
   const bool paged = p.kv_layout == DA_KV_PAGED;
   const bool sparse = p.sparse_block_size > 0;
   if (!a->q || !a->k || !a->v || !a->seq_lens || !a->out) return DA_ERR_INVALID_ARG;
@@ -225,7 +226,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   // R = G x Q consecutive rows of q viewed as [B * HQ * Q][D]
   const int Q = p.q_len > 1 ? p.q_len : 1;
   const int R = p.num_q_heads / p.num_kv_heads * Q;
-  if (ctx->map_k_base != a->k || ctx->map_v_base != a->v || ctx->map_q_base != a->q) {
+  if (!fp4 && (ctx->map_k_base != a->k || ctx->map_v_base != a->v || ctx->map_q_base != a->q)) {
     ctx->map_k_base = ctx->map_v_base = ctx->map_q_base = nullptr;
     da_status st;
     if (int4) {
@@ -306,6 +307,14 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   gp.fp8_mma = p.fp8_mma;
   gp.test_stall_ns = ctx->test_stall_ns;
   ctx->test_stall_ns = 0;  // one call only
+  if (fp4) {
+    da::Fp4Params f;
+    f.g = gp;
+    f.k = reinterpret_cast<const uint8_t *>(a->k);
+    f.v = reinterpret_cast<const uint8_t *>(a->v);
+    f.o_head = reinterpret_cast<float *>(ws + da::fp4_head_offset(pl));
+    return da::launch_fp4(f, pl.grid_x, stream) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  }
   if (da::launch_gqa(fp8, gp.group, ctx->kmap, ctx->vmap, ctx->qmap,
                      token_scale ? ctx->kssmap : ctx->kmap, token_scale ? ctx->vssmap : ctx->vmap,
                      gp, pl.grid_x, stream) !=
@@ -387,7 +396,9 @@ da_status decode_attn_create(const da_problem *problem, int device, da_ctx **out
   int prev = 0;
   if (cudaGetDevice(&prev) != cudaSuccess) return DA_ERR_CUDA;
   if (cudaSetDevice(device) != cudaSuccess) return DA_ERR_CUDA;
-  cudaError_t e = problem->is_mla ? da::mla_prepare(device) : da::gqa_prepare(device);
+  cudaError_t e = problem->is_mla ? da::mla_prepare(device)
+                  : problem->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS ? da::fp4_prepare()
+                                                                  : da::gqa_prepare(device);
   cudaSetDevice(prev);
   if (e != cudaSuccess && e != cudaErrorNotSupported) return DA_ERR_CUDA;
   da_ctx *ctx = new (std::nothrow) da_ctx;

@@ -59,6 +59,23 @@ struct GqaParams {
                                // that nothing arrives on, given up after this long
 };
 
+// Decode over the 4-bit float cache (fp4_split.cu): granules of 16 rows, 1152
+// bytes each, read through their addresses; o_head holds, per CTA and warp, the
+// piece of a unit that ended inside that warp's range.
+struct Fp4Params {
+  GqaParams g;
+  const uint8_t *k, *v;
+  float *o_head;               // [ctas][warps][G][128]
+};
+
+// Which instantiation a call's score and mask modifications need: 0 none; 1
+// several query tokens, a draft-tree mask, a soft cap; 2 the flex-style mods too.
+inline int gqa_mod(const GqaParams &p) {
+  return (p.mask_window != nullptr || p.alibi_slopes != nullptr)
+             ? 2
+             : (p.q_len > 1 || p.spec_mask != nullptr || p.softcap_l2 > 0.f) ? 1 : 0;
+}
+
 // Group counters per GQA unit for the two-level merge of a unit cut into many
 // pieces (groups of ceil(sqrt(pieces)) pieces; pieces <= CTAs): shared by the
 // planner, which sizes the workspace, and the kernel.
@@ -108,6 +125,11 @@ cudaError_t launch_gqa(bool fp8, int group, const CUtensorMap &kmap, const CUten
                        cudaStream_t stream);
 int gqa_box_tokens(const da_problem &p);
 
+cudaError_t fp4_prepare();
+int fp4_tile();                // tokens per stage
+int fp4_warps(int group);      // warps of a CTA for `group` rows per unit
+cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream);
+
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream);
 
 cudaError_t mla_prepare(int device);
@@ -122,5 +144,7 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
                        const int32_t *seq_lens_host, const int32_t *kv_num_blks_host,
                        int32_t num_splits_override, da_plan_info *info);
 da_status validate_problem(const da_problem *p);
+// Byte offset of Fp4Params::o_head in the workspace (after the partial LSEs).
+int64_t fp4_head_offset(const da_plan_info &info);
 
 }  // namespace da

@@ -35,7 +35,8 @@ da_status validate_problem(const da_problem *p) {
   if (p->fp8_mma && (p->is_mla || p->kv_dtype != DA_DTYPE_FP8_E4M3)) return DA_ERR_UNSUPPORTED;
   if (p->kv_layout != DA_KV_CONTIGUOUS && p->kv_layout != DA_KV_PAGED) return DA_ERR_INVALID_ARG;
   if (p->kv_dtype != DA_DTYPE_BF16 && p->kv_dtype != DA_DTYPE_FP8_E4M3 &&
-      p->kv_dtype != DA_DTYPE_FP8_E4M3_TOKEN_SCALE && p->kv_dtype != DA_DTYPE_INT4_GROUPS)
+      p->kv_dtype != DA_DTYPE_FP8_E4M3_TOKEN_SCALE && p->kv_dtype != DA_DTYPE_INT4_GROUPS &&
+      p->kv_dtype != DA_DTYPE_FP4_E2M1_BLOCKS)
     return DA_ERR_INVALID_ARG;
   if (p->kv_dtype == DA_DTYPE_INT4_GROUPS) {
     if (!(p->kv_groups == 1 || p->kv_groups == 2 || p->kv_groups == 4 || p->kv_groups == 8))
@@ -85,6 +86,18 @@ da_status validate_problem(const da_problem *p) {
     if (p->kv_layout != DA_KV_CONTIGUOUS) return DA_ERR_UNSUPPORTED;
     if (p->max_sparse_blocks <= 0) return DA_ERR_INVALID_ARG;
   }
+  if (p->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS) {
+    // granules of 16 rows, read through 64-bit addresses; positions and the
+    // tiles of all units are counted in 32 bits
+    if (p->kv_layout == DA_KV_CONTIGUOUS && p->max_seq_len % 16 != 0) return DA_ERR_UNSUPPORTED;
+    const int64_t cap = p->kv_layout == DA_KV_PAGED ? (int64_t)p->max_pages_per_seq * p->page_size
+                                                    : (int64_t)p->max_seq_len;
+    const int64_t list = (int64_t)p->sparse_block_size * p->max_sparse_blocks * 2;
+    if (cap >= (1ll << 31) || list >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+    const int64_t tiles = (int64_t)p->batch * p->num_kv_heads * ((std::max(cap, list) + 31) / 32);
+    if ((int64_t)p->batch * p->num_kv_heads >= (1ll << 31) || tiles >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+    return DA_OK;
+  }
   // TMA row coordinates are 32-bit: (cache rows) x (rows per token) must fit
   const int64_t rows = p->kv_layout == DA_KV_PAGED
                            ? (int64_t)p->num_pages * p->num_kv_heads * p->page_size
@@ -93,9 +106,14 @@ da_status validate_problem(const da_problem *p) {
   return DA_OK;
 }
 
+int64_t fp4_head_offset(const da_plan_info &i) {
+  return align256(i.partial_lse_offset + ((int64_t)i.num_units + i.grid_x) * i.rows_per_unit * 4);
+}
+
 // Resident CTAs of the split kernel per SM, from its shared-memory footprint.
 static int ctas_per_sm(const da_problem *p, int32_t smem_per_sm) {
   const bool mla = p->is_mla != 0;
+  if (p->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS) return 1;  // its rings fill an SM
   const int per_cta = (mla ? mla_smem_bytes()
                            : gqa_smem_bytes(p->kv_dtype != DA_DTYPE_BF16,
                                             p->num_q_heads / p->num_kv_heads *
@@ -118,7 +136,8 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
   const bool mla = p->is_mla != 0;
   const bool sparse = !mla && p->sparse_block_size > 0;
   const bool paged = p->kv_layout == DA_KV_PAGED;
-  const int tile = mla ? kMlaTile : kGqaTile;
+  const bool fp4 = p->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS;
+  const int tile = mla ? kMlaTile : fp4 ? fp4_tile() : kGqaTile;
   const int align = sparse ? p->sparse_block_size : tile;
   // units: GQA (row, kv head); MLA (row, query token), whose heads share the latent cache
   const int Q = p->q_len > 1 ? p->q_len : 1;
@@ -183,6 +202,7 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
     off = align256(off + (units + ctas) * rows * (int64_t)dv * 4);
     info->partial_lse_offset = off;
     off = align256(off + (units + ctas) * rows * 4);
+    if (fp4) off = fp4_head_offset(*info) + align256(ctas * fp4_warps(rows) * rows * (int64_t)dv * 4);
     info->workspace_bytes = off;
     return DA_OK;
   }

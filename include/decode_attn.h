@@ -75,12 +75,20 @@ typedef enum { DA_KV_CONTIGUOUS = 0, DA_KV_PAGED = 1 } da_kv_layout;
  * of k / v is int32 words, first kv_groups coefficient words (fp16 scale in
  * the low half, fp16 shift in the high half), then D / 8 words of eight
  * unsigned 4-bit codes, element 8w + i in bits 4i..4i+3 of data word w;
- * element d has value code * scale + shift of group d / (D / kv_groups). */
+ * element d has value code * scale + shift of group d / (D / kv_groups); or
+ * 4-bit floating point in granules of 16 rows: a cache is bytes
+ * [B][HKV][L / 16][1152] or [num_pages][HKV][page_size / 16][1152] (L a multiple
+ * of 16). Byte 64 r + j (j < 64) of a granule holds the e2m1 codes of elements
+ * 2 j (low four bits) and 2 j + 1 of row r, byte 1024 + 8 r + i the e4m3 scale of
+ * the row's elements 16 i .. 16 i + 15; with one fp32 scale per kv head (k_scale /
+ * v_scale) an element is code * block scale * head scale. An e4m3 NaN scale makes
+ * its block NaN. */
 typedef enum {
   DA_DTYPE_BF16 = 0,
   DA_DTYPE_FP8_E4M3 = 1,
   DA_DTYPE_FP8_E4M3_TOKEN_SCALE = 2,
-  DA_DTYPE_INT4_GROUPS = 3
+  DA_DTYPE_INT4_GROUPS = 3,
+  DA_DTYPE_FP4_E2M1_BLOCKS = 4
 } da_dtype;
 
 /* Bits of the device error word (sticky until decode_attn_get_error clears it). */
@@ -154,8 +162,10 @@ typedef struct {
  *              MLA: k = ckv [num_pages][page_size][512], v = kpe [num_pages][page_size][64].
  *              Element type bf16, or e4m3 bytes when kv_dtype is an e4m3 type;
  *              DA_DTYPE_INT4_GROUPS: int32 rows of kv_groups + D / 8 words.
+ *              DA_DTYPE_FP4_E2M1_BLOCKS: granules of 1152 bytes (see da_dtype).
  *              Base addresses 16-byte aligned.
- *   k_scale, v_scale  DA_DTYPE_FP8_E4M3 only: fp32 [HKV]; dequantised value = e4m3 * scale
+ *   k_scale, v_scale  DA_DTYPE_FP8_E4M3 and DA_DTYPE_FP4_E2M1_BLOCKS only: fp32 [HKV];
+ *              dequantised value = e4m3 * scale, or e2m1 * block scale * scale
  *   k_scale_shift, v_scale_shift  DA_DTYPE_FP8_E4M3_TOKEN_SCALE only: int32, one word per
  *              cache row of k / v (contiguous [B][HKV][L], paged [num_pages][HKV][page_size]):
  *              fp16 scale in the low half, fp16 shift in the high half; dequantised
