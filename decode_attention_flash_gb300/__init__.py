@@ -24,7 +24,9 @@ __all__ = [
     "decode_attn_get_error_noalloc", "decode_attn_destroy",
     "decode_attn_status_string", "DecodeAttention", "DA_KV_CONTIGUOUS", "DA_KV_PAGED",
     "DA_DTYPE_BF16", "DA_DTYPE_FP8_E4M3", "DA_DTYPE_FP8_E4M3_TOKEN_SCALE", "DA_DTYPE_INT4_GROUPS",
-    "DA_DTYPE_FP4_E2M1_BLOCKS",
+    "DA_DTYPE_FP4_E2M1_BLOCKS", "TableArgs", "AppendArgs", "GatherArgs", "make_args",
+    "make_table_args", "make_append_args", "make_gather_args", "decode_attn_build_tables",
+    "decode_attn_append", "decode_attn_gather",
 ]
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_CUDA = 0, 1, 2, 3
@@ -33,6 +35,7 @@ DA_KV_CONTIGUOUS, DA_KV_PAGED = 0, 1
 DA_DTYPE_BF16, DA_DTYPE_FP8_E4M3, DA_DTYPE_FP8_E4M3_TOKEN_SCALE, DA_DTYPE_INT4_GROUPS = 0, 1, 2, 3
 DA_DTYPE_FP4_E2M1_BLOCKS = 4
 DA_DEVERR_PAGE_INDEX, DA_DEVERR_SPARSE_INDEX, DA_DEVERR_SEQ_LEN, DA_DEVERR_TIMEOUT = 1, 2, 4, 8
+DA_DEVERR_NO_PAGES, DA_DEVERR_SLOT, DA_DEVERR_POSITION = 16, 32, 64
 
 
 class DecodeAttnError(RuntimeError):
@@ -69,6 +72,34 @@ class Args(ctypes.Structure):
         ("mask_sink", ctypes.c_void_p), ("mask_window", ctypes.c_void_p),
         ("alibi_slopes", ctypes.c_void_p),
     ]
+
+
+class TableArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "seq_lens", "new_lens", "free_pages", "num_free", "block_table", "seq_lens_out",
+        "num_free_out", "slot_map", "positions", "token_row", "cu_new")] + [
+        ("free_capacity", ctypes.c_int32), ("slot_capacity", ctypes.c_int32)]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("q", ctypes.c_void_p), ("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64), ("v_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("slot_map", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+        ("position_stride", ctypes.c_int64), ("cos_sin", ctypes.c_void_p),
+        ("pair_axis", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("k_scale_shift", ctypes.c_void_p), ("v_scale_shift", ctypes.c_void_p),
+        ("num_tokens", ctypes.c_int32), ("q_len", ctypes.c_int32), ("rope_axes", ctypes.c_int32),
+        ("rope_dim", ctypes.c_int32), ("rope_adjacent", ctypes.c_int32),
+        ("max_position", ctypes.c_int32),
+    ]
+
+
+class GatherArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "k", "v", "k_scale", "v_scale", "k_scale_shift", "v_scale_shift", "slot_map", "k_out",
+        "v_out")] + [("num_tokens", ctypes.c_int32)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -110,6 +141,9 @@ def load(build_if_missing: bool = False):
         "decode_attn_run_noalloc": (st, [vp, ctypes.POINTER(Args), vp]),
         "decode_attn_get_error": (st, [vp, vp, vp, ctypes.POINTER(ctypes.c_uint32)]),
         "decode_attn_get_error_noalloc": (st, [vp, vp, ctypes.POINTER(ctypes.c_uint32)]),
+        "decode_attn_build_tables": (st, [vp, ctypes.POINTER(TableArgs), vp, ctypes.c_size_t, vp]),
+        "decode_attn_append": (st, [vp, ctypes.POINTER(AppendArgs), vp, ctypes.c_size_t, vp]),
+        "decode_attn_gather": (st, [vp, ctypes.POINTER(GatherArgs), vp, ctypes.c_size_t, vp]),
         "decode_attn_destroy": (None, [vp]),
         "decode_attn_status_string": (ctypes.c_char_p, [st]),
         # test hooks (include/decode_attn_testing.h)
@@ -250,6 +284,123 @@ def decode_attn_merge(ctx, o_part, lse_part, num_splits: int, rows: int, dv: int
            "decode_attn_merge")
 
 
+def _typed_ptr(tensors: dict, name: str, dtype, numel=None):
+    """Device pointer of an argument the kernels index by element: its type and
+    its number of elements are checked here."""
+    t = tensors.get(name)
+    if isinstance(t, torch.Tensor):
+        if t.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+        if numel is not None and t.numel() != numel:
+            raise ValueError(f"{name} must have {numel} elements, got {t.numel()}")
+    return _ptr(t)
+
+
+def make_table_args(tensors: dict) -> TableArgs:
+    """Arguments of ``decode_attn_build_tables`` from a dict with the names of the C struct.
+    ``slot_capacity`` and ``free_capacity`` are the sizes of ``slot_map`` and ``free_pages``."""
+    rows, slots = tensors["seq_lens"].numel(), tensors["slot_map"].numel()
+    a = TableArgs()
+    for name, n in (("seq_lens", rows), ("new_lens", rows), ("seq_lens_out", rows), ("cu_new", rows + 1),
+                    ("free_pages", None), ("num_free", 1), ("num_free_out", 1), ("block_table", None),
+                    ("positions", slots), ("token_row", slots)):
+        setattr(a, name, _typed_ptr(tensors, name, torch.int32, n))
+    a.slot_map = _typed_ptr(tensors, "slot_map", torch.int64)
+    a.slot_capacity = slots
+    a.free_capacity = tensors["free_pages"].numel() if tensors.get("free_pages") is not None else 0
+    return a
+
+
+def _token_rows(t, name: str, tokens: int):
+    """Pointer and token stride of [tokens, ...] rows whose inner axes are contiguous (a view
+    of a wider projection is fine)."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be in device memory (got a host tensor)")
+    if t.dtype != torch.bfloat16 or t.dim() < 2 or t.shape[0] != tokens:
+        raise ValueError(f"{name} must be bf16 with {tokens} rows")
+    inner = 1
+    for size, stride in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and stride != inner:
+            raise ValueError(f"the rows of {name} must be contiguous")
+        inner *= size
+    return ctypes.c_void_p(t.data_ptr()), (t.stride(0) if tokens > 1 else inner)
+
+
+def make_append_args(tensors: dict, pair_axis=None, rope_adjacent: bool = False, q_len: int = 1) -> AppendArgs:
+    """Arguments of ``decode_attn_append`` from a dict with the names of the C struct. The number
+    of tokens is that of ``slot_map`` (or of ``q``, for queries alone), the rotated dimensions are
+    ``cos_sin``'s width, the axes ``positions``' rows; ``pair_axis`` is a sequence of ints."""
+    first = tensors.get("slot_map") if tensors.get("slot_map") is not None else tensors["q"]
+    n = first.shape[0]
+    a = AppendArgs()
+    for name, stride in (("q", "q_stride"), ("k_new", "k_stride"), ("v_new", "v_stride")):
+        ptr, st = _token_rows(tensors.get(name), name, n)
+        setattr(a, name, ptr)
+        setattr(a, stride, st)
+    q = tensors.get("q")
+    a.q_out = _typed_ptr(tensors, "q_out", torch.bfloat16, q.numel() if q is not None else None)
+    a.slot_map = _typed_ptr(tensors, "slot_map", torch.int64, n)
+    for name in ("k_scale", "v_scale"):
+        setattr(a, name, _typed_ptr(tensors, name, torch.float32))
+    for name in ("k_scale_shift", "v_scale_shift"):
+        setattr(a, name, _typed_ptr(tensors, name, torch.int32))
+    a.k, a.v = _ptr(tensors.get("k")), _ptr(tensors.get("v"))
+    a.num_tokens, a.q_len, a.rope_adjacent = n, int(q_len), int(rope_adjacent)
+    table, pos = tensors.get("cos_sin"), tensors.get("positions")
+    if table is not None:
+        if table.dim() != 2 or pos is None or pos.shape[-1] != n or pos.dim() > 2:
+            raise ValueError("cos_sin must be [positions, rope_dim] and positions [tokens] or [axes, tokens]")
+        a.cos_sin = _typed_ptr(tensors, "cos_sin", torch.float32)
+        a.positions = _typed_ptr(tensors, "positions", torch.int32)
+        a.max_position, a.rope_dim = table.shape
+        a.rope_axes, a.position_stride = (pos.shape[0] if pos.dim() == 2 else 1), n
+        if pair_axis is not None:
+            if len(pair_axis) != a.rope_dim // 2:
+                raise ValueError(f"pair_axis must have {a.rope_dim // 2} entries")
+            a._pairs = (ctypes.c_uint8 * len(pair_axis))(*[int(x) for x in pair_axis])
+            a.pair_axis = ctypes.cast(a._pairs, ctypes.c_void_p)
+    return a
+
+
+def make_gather_args(tensors: dict) -> GatherArgs:
+    """Arguments of ``decode_attn_gather`` from a dict with the names of the C struct."""
+    a = GatherArgs()
+    n = tensors["slot_map"].numel()
+    for name in ("k_out", "v_out"):
+        if tensors[name].shape[0] != n:
+            raise ValueError(f"{name} must have {n} rows")
+        setattr(a, name, _typed_ptr(tensors, name, torch.bfloat16))
+    a.slot_map = _typed_ptr(tensors, "slot_map", torch.int64)
+    for name in ("k_scale", "v_scale"):
+        setattr(a, name, _typed_ptr(tensors, name, torch.float32))
+    for name in ("k_scale_shift", "v_scale_shift"):
+        setattr(a, name, _typed_ptr(tensors, name, torch.int32))
+    a.k, a.v, a.num_tokens = _ptr(tensors.get("k")), _ptr(tensors.get("v")), n
+    return a
+
+
+def _workspace_call(name: str, ctx, args, workspace, stream):
+    _check(getattr(load(), name)(ctx, ctypes.byref(args), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream)), name)
+
+
+def decode_attn_build_tables(ctx, args: TableArgs, workspace: torch.Tensor, stream=None):
+    """Block table, slots and lengths of the tokens that the rows get now (one kernel)."""
+    _workspace_call("decode_attn_build_tables", ctx, args, workspace, stream)
+
+
+def decode_attn_append(ctx, args: AppendArgs, workspace: torch.Tensor, stream=None):
+    """Rotates queries and new keys, and writes keys and values into the cache (one kernel)."""
+    _workspace_call("decode_attn_append", ctx, args, workspace, stream)
+
+
+def decode_attn_gather(ctx, args: GatherArgs, workspace: torch.Tensor, stream=None):
+    """Reads cache rows back as bf16 (one kernel)."""
+    _workspace_call("decode_attn_gather", ctx, args, workspace, stream)
+
+
 def decode_attn_get_error(ctx, workspace: torch.Tensor, stream=None) -> int:
     flags = ctypes.c_uint32()
     st = load().decode_attn_get_error(ctx, _ptr(workspace), _stream(stream), ctypes.byref(flags))
@@ -306,6 +457,68 @@ class DecodeAttention:
             raise ValueError(f"lse must be float32 with {lead} elements")
         decode_attn_run(self.ctx, make_args(tensors, scale, out, lse, softcap), self.workspace, stream)
         return out
+
+    def _cache_sizes(self):
+        """Bytes of a cache tensor (K, V) and its number of positions."""
+        p = self.problem
+        paged = p.kv_layout == DA_KV_PAGED
+        slots = (p.num_pages * p.page_size) if paged else p.batch * p.max_seq_len
+        if p.is_mla:
+            return slots * 1024, slots * 128, slots
+        row = {DA_DTYPE_BF16: 256, DA_DTYPE_INT4_GROUPS: 4 * (p.kv_groups + 16),
+               DA_DTYPE_FP4_E2M1_BLOCKS: 72}.get(p.kv_dtype, 128)
+        return slots * p.num_kv_heads * row, slots * p.num_kv_heads * row, slots
+
+    def _check_cache(self, tensors: dict):
+        p = self.problem
+        k, v, slots = self._cache_sizes()
+        for name, want in (("k", k), ("v", v)):
+            t = tensors[name]
+            if t.numel() * t.element_size() != want:
+                raise ValueError(f"{name} must be a cache of {want} bytes, got {t.numel() * t.element_size()}")
+        per_head = p.kv_dtype in (DA_DTYPE_FP8_E4M3, DA_DTYPE_FP4_E2M1_BLOCKS)
+        for name, on, want in (("k_scale", per_head, p.num_kv_heads), ("v_scale", per_head, p.num_kv_heads),
+                               ("k_scale_shift", p.kv_dtype == DA_DTYPE_FP8_E4M3_TOKEN_SCALE, slots * p.num_kv_heads),
+                               ("v_scale_shift", p.kv_dtype == DA_DTYPE_FP8_E4M3_TOKEN_SCALE, slots * p.num_kv_heads)):
+            if on and (tensors.get(name) is None or tensors[name].numel() != want):
+                raise ValueError(f"{name} must have {want} elements")
+
+    def build_tables(self, tensors: dict, stream=None):
+        """``decode_attn_build_tables`` with the sizes checked against the problem."""
+        p = self.problem
+        if tensors["seq_lens"].numel() != p.batch:
+            raise ValueError(f"seq_lens must have {p.batch} elements")
+        table = tensors.get("block_table")
+        if table is not None and table.numel() != p.batch * p.max_pages_per_seq:
+            raise ValueError(f"block_table must be [{p.batch}, {p.max_pages_per_seq}]")
+        decode_attn_build_tables(self.ctx, make_table_args(tensors), self.workspace, stream)
+
+    def append(self, tensors: dict, pair_axis=None, rope_adjacent=False, q_len=1, stream=None):
+        """``decode_attn_append`` with the sizes checked against the problem."""
+        p = self.problem
+        d = 64 if p.is_mla else 128
+        if tensors.get("k_new") is not None:
+            self._check_cache(tensors)
+        for name, row in (("q", p.num_q_heads * d), ("k_new", 512 if p.is_mla else p.num_kv_heads * d),
+                          ("v_new", 64 if p.is_mla else p.num_kv_heads * d)):
+            t = tensors.get(name)
+            if t is not None and math.prod(t.shape[1:]) != row:
+                raise ValueError(f"the rows of {name} must have {row} elements")
+        decode_attn_append(self.ctx, make_append_args(tensors, pair_axis, rope_adjacent, q_len),
+                           self.workspace, stream)
+        return tensors.get("q_out")
+
+    def gather(self, tensors: dict, stream=None):
+        """``decode_attn_gather`` with the sizes checked against the problem."""
+        p = self.problem
+        self._check_cache(tensors)
+        n = tensors["slot_map"].numel()
+        for name, row in (("k_out", 512 if p.is_mla else p.num_kv_heads * 128),
+                          ("v_out", 64 if p.is_mla else p.num_kv_heads * 128)):
+            if tensors[name].numel() != n * row:
+                raise ValueError(f"{name} must have {n * row} elements")
+        decode_attn_gather(self.ctx, make_gather_args(tensors), self.workspace, stream)
+        return tensors["k_out"], tensors["v_out"]
 
     def errors(self, stream=None) -> int:
         return decode_attn_get_error(self.ctx, self.workspace, stream)

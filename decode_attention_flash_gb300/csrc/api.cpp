@@ -41,6 +41,10 @@ namespace da {
 int ctx_device(const da_ctx *ctx) { return ctx->device; }
 // Arms the test stall of the context's next GQA run (decode_attn_testing.h).
 void ctx_set_test_stall(da_ctx *ctx, uint32_t ns) { ctx->test_stall_ns = ns; }
+// What the cache calls (cache_api.cpp) read of a context.
+int ctx_num_sms(const da_ctx *ctx) { return ctx->num_sms; }
+bool ctx_planned(const da_ctx *ctx) { return ctx->planned; }
+const da_problem &ctx_problem(const da_ctx *ctx) { return ctx->prob; }
 bool ctx_is_mla(const da_ctx *ctx) { return ctx->prob.is_mla != 0; }
 }  // namespace da
 

@@ -15,6 +15,7 @@ constexpr uint64_t kWaitLimitNs = 1500ull * 1000ull * 1000ull;
 
 // Workspace: [error word | pad to 256 B][unit counters u32][partial O fp32][partial LSE fp32]
 constexpr int64_t kWorkspaceHeader = 256;
+constexpr int64_t kTicketOffset = 64;  // in the header: block counter of build_tables, zero between calls
 // Page / block ids one split CTA stages in shared memory (caps the split length).
 constexpr int kGqaMaxIds = 512;
 // Splits per unit the fused merge handles (its weights live in shared memory).
@@ -115,6 +116,45 @@ struct MlaParams {
   int32_t q_len;                // Q >= 1
 };
 
+// Rows of the cache written (append) or read back (gather), cache_rows.cu. A
+// slot is page * rows_per_page + offset (contiguous: batch row * cache length +
+// position, rows_per_page the cache length).
+struct CacheRowParams {
+  const __nv_bfloat16 *q, *k_new, *v_new;  // rows of a token, strides in elements
+  int64_t q_stride, k_stride, v_stride;
+  __nv_bfloat16 *q_out;        // [T][HQ][D], or [B][HQ][q_len][D] when q_len > 1
+  void *k, *v;                 // the cache
+  const float *k_scale, *v_scale;
+  int32_t *k_scale_shift, *v_scale_shift;
+  const int64_t *slot_map;     // [T]; -1 is padding; null: queries only
+  int64_t num_slots;
+  const int32_t *positions;    // [axes][T], rows position_stride apart
+  int64_t position_stride;
+  const float *cos_sin;        // [max_position][2 * rope_pairs]: cosines, then sines
+  __nv_bfloat16 *k_out, *v_out;  // gather: [T][HKV][D] each (latent: [T][512], [T][64])
+  uint32_t *err;
+  int32_t num_tokens, num_q_heads, num_kv_heads, rows_per_page, kv_groups, q_len;
+  int32_t max_position, rope_pairs;
+  int32_t rope_adjacent;       // pairs are elements 2i, 2i + 1 (else i, i + n)
+  int32_t rope_whole;          // a lane's pairs share an axis (vector loads of the table)
+  int32_t parts;               // warps a token's heads are spread over (the launcher's)
+  uint8_t pair_axis[64];
+};
+
+// decode_attn_build_tables, tables.cu.
+struct TableParams {
+  const int32_t *seq_lens, *new_lens;  // [B]
+  const int32_t *free_pages, *num_free;  // null: the table already holds every page
+  int32_t *block_table;        // [B][max_pages]
+  int32_t *seq_lens_out, *num_free_out;
+  int64_t *slot_map;           // [slot_capacity]
+  int32_t *positions, *token_row, *cu_new;  // optional
+  uint32_t *err, *ticket;
+  int64_t capacity;            // positions a row can hold
+  int32_t batch, page_size, max_pages, num_pages, free_capacity, slot_capacity;
+  int32_t paged, in_place;     // in_place: an output overlaps an input that every block reads
+};
+
 // Kernel launchers (return the launch error).
 cudaError_t gqa_prepare(int device);  // sets shared-memory attributes once per device
 int gqa_smem_bytes(bool fp8, int group, bool token_scale, bool int4);
@@ -129,6 +169,10 @@ cudaError_t fp4_prepare();
 int fp4_tile();                // tokens per stage
 int fp4_warps(int group);      // warps of a CTA for `group` rows per unit
 cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream);
+
+cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
+cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
+cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_merge(const MergeParams &p, cudaStream_t stream);
 

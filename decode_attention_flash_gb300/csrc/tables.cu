@@ -1,0 +1,235 @@
+// tables.cu -- block tables and slot maps from request lengths (decode_attn_build_tables).
+//
+// The mathematics. Row b holds old tokens and takes nw new ones: it needs
+// need_b = ceil((old + nw) / P) - ceil(old / P) pages, the ones after the
+// a_b = sum_{b' < b} need_b' pages that earlier rows take from the top of the
+// free stack F[0 .. n): its k-th new page is F[n - 1 - (a_b + k)]. New token i of
+// row b stands at position old + i, in slot page(pos / P) * P + pos % P, where the
+// page is the table's for the pages that the row had and the stack's for the others
+// (so no token waits for the table to be written).
+//
+// What bounds it. A decode step moves a few KB: latency. So it is one launch,
+// and no block waits for another: every block scans all rows' lengths again (two
+// block scans of a few thousand integers from L2) and then writes its own share of
+// the tokens, of the new table entries and (block 0) of the per-row results;
+// a token finds its row by bisecting the scan, kept per thread in shared memory.
+// Results written over the lengths they came from wait for the block that is last
+// to have read them (a counter in the workspace, back at zero afterwards).
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace da {
+namespace {
+
+constexpr int kThreads = 512;
+
+struct Row {
+  int64_t old, nw, asked;   // cached positions, new ones that fit, new tokens asked for
+  int64_t first, need;      // pages it has, pages it needs
+};
+
+__device__ __forceinline__ Row row_of(const TableParams &p, int b, uint32_t &err) {
+  Row r;
+  int64_t o = p.seq_lens[b], a = p.new_lens[b];
+  if (o < 0 || o > p.capacity) {
+    err |= DA_DEVERR_SEQ_LEN;
+    o = o < 0 ? 0 : p.capacity;
+  }
+  if (a < 0) {
+    err |= DA_DEVERR_SEQ_LEN;
+    a = 0;
+  }
+  r.old = o;
+  r.asked = a;
+  r.nw = a;
+  if (o + a > p.capacity) {
+    err |= DA_DEVERR_SEQ_LEN;
+    r.nw = p.capacity - o;
+  }
+  r.first = r.need = 0;
+  if (p.paged) {
+    const uint32_t P = (uint32_t)p.page_size;
+    r.first = (uint32_t)(o + P - 1) / P;
+    r.need = p.free_pages ? (uint32_t)(o + r.nw + P - 1) / P - r.first : 0;
+  }
+  return r;
+}
+
+__global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
+  __shared__ int64_t s_tok[kThreads + 1], s_pg[kThreads + 1];
+  __shared__ int64_t w_tok[kThreads / 32], w_pg[kThreads / 32];
+  __shared__ int64_t s_used;
+  __shared__ int s_last;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  uint32_t err = 0;
+  int64_t nf = 0;
+  if (p.free_pages) {
+    nf = *p.num_free;
+    if (nf < 0 || nf > p.free_capacity) {
+      err |= DA_DEVERR_NO_PAGES;
+      nf = nf < 0 ? 0 : p.free_capacity;
+    }
+  }
+  if (tid == 0) {
+    s_used = 0;
+    s_last = 1;
+  }
+  int64_t tok = 0, pg = 0;
+  for (int b = b0; b < b1; ++b) {
+    const Row r = row_of(p, b, err);
+    tok += r.asked;
+    pg += r.need;
+  }
+  int64_t it = tok, ip = pg;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, it, o), y = __shfl_up_sync(0xffffffffu, ip, o);
+    if (lane >= o) {
+      it += x;
+      ip += y;
+    }
+  }
+  if (lane == 31) {
+    w_tok[warp] = it;
+    w_pg[warp] = ip;
+  }
+  __syncthreads();
+  for (int w = 0; w < warp; ++w) {
+    it += w_tok[w];
+    ip += w_pg[w];
+  }
+  s_tok[tid + 1] = it;
+  s_pg[tid + 1] = ip;
+  if (tid == 0) s_tok[0] = s_pg[0] = 0;
+  __syncthreads();
+  const int64_t total = s_tok[kThreads], pages = s_pg[kThreads];
+
+  auto served = [&](int64_t ahead, int64_t need) { return need == 0 || ahead + need <= nf; };
+  auto free_id = [&](int64_t a) -> int {  // the a-th page taken
+    const int id = __ldg(p.free_pages + (nf - 1 - a));
+    if (id < 0 || id >= p.num_pages) {
+      err |= DA_DEVERR_PAGE_INDEX;
+      return -1;
+    }
+    return id;
+  };
+  // the thread whose rows hold item i of a prefix array
+  auto find = [&](const int64_t *s, int64_t i) {
+    int lo = 0, hi = kThreads;
+    while (hi - lo > 1) {
+      const int m = (lo + hi) >> 1;
+      if (s[m] <= i) lo = m;
+      else hi = m;
+    }
+    return lo;
+  };
+
+  const int64_t stride = (int64_t)gridDim.x * kThreads, start = (int64_t)blockIdx.x * kThreads + tid;
+  // ---- tokens
+  for (int64_t i = start; i < p.slot_capacity; i += stride) {
+    int64_t slot = -1, pos = 0;
+    int row = -1;
+    if (i < total) {
+      const int c = find(s_tok, i);
+      int64_t at = s_tok[c], ahead = s_pg[c];
+      int b = c * per;
+      uint32_t ignored = 0;
+      Row r = row_of(p, b, ignored);
+      while (i >= at + r.asked) {
+        at += r.asked;
+        ahead += r.need;
+        r = row_of(p, ++b, ignored);
+      }
+      row = b;
+      const int64_t k = i - at;
+      pos = r.old + k;
+      if (k < r.nw && served(ahead, r.need)) {
+        if (!p.paged) {
+          slot = (int64_t)b * p.capacity + pos;
+        } else {
+          const uint32_t P = (uint32_t)p.page_size, pi = (uint32_t)pos / P;
+          int id;
+          if (pi < r.first || !p.free_pages) {
+            id = p.block_table[(int64_t)b * p.max_pages + pi];
+            if (id < 0 || id >= p.num_pages) {
+              err |= DA_DEVERR_PAGE_INDEX;
+              id = -1;
+            }
+          } else {
+            id = free_id(ahead + pi - r.first);
+          }
+          if (id >= 0) slot = (int64_t)id * P + ((uint32_t)pos - pi * P);
+        }
+      }
+    }
+    p.slot_map[i] = slot;
+    if (p.positions) p.positions[i] = (int32_t)min(pos, (int64_t)INT32_MAX);
+    if (p.token_row) p.token_row[i] = row;
+  }
+  // ---- new table entries
+  for (int64_t a = start; a < pages; a += stride) {
+    const int c = find(s_pg, a);
+    int64_t ahead = s_pg[c];
+    int b = c * per;
+    uint32_t ignored = 0;
+    Row r = row_of(p, b, ignored);
+    while (a >= ahead + r.need) {
+      ahead += r.need;
+      r = row_of(p, ++b, ignored);
+    }
+    if (served(ahead, r.need)) {
+      const int id = free_id(a);
+      if (id >= 0) p.block_table[(int64_t)b * p.max_pages + r.first + (a - ahead)] = id;
+    }
+  }
+  // ---- per-row results: block 0, or the last block to have read the lengths
+  bool mine = blockIdx.x == 0;
+  if (p.in_place && gridDim.x > 1) {
+    __syncthreads();
+    if (tid == 0) {
+      s_last = atomic_add_acq_rel_gpu(p.ticket, 1u) == gridDim.x - 1;
+      if (s_last) *p.ticket = 0u;
+    }
+    __syncthreads();
+    mine = s_last != 0;
+  } else {
+    __syncthreads();  // this block's reads of the lengths
+  }
+  if (mine) {
+    int64_t at = s_tok[tid], ahead = s_pg[tid], used = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Row r = row_of(p, b, err);
+      const bool ok = served(ahead, r.need);
+      if (!ok) err |= DA_DEVERR_NO_PAGES;
+      else if (r.need > 0) used = ahead + r.need;  // (rows served without a page may stand after one refused)
+      if (p.cu_new) p.cu_new[b] = (int32_t)min(at, (int64_t)INT32_MAX);
+      p.seq_lens_out[b] = (int32_t)(ok ? r.old + r.nw : r.old);
+      at += r.asked;
+      ahead += r.need;
+    }
+    if (p.free_pages) atomicMax(reinterpret_cast<unsigned long long *>(&s_used), (unsigned long long)used);
+    __syncthreads();
+    if (tid == 0) {
+      if (p.cu_new) p.cu_new[p.batch] = (int32_t)min(total, (int64_t)INT32_MAX);
+      if (p.free_pages) *p.num_free_out = (int32_t)(nf - s_used);
+      if (total > p.slot_capacity) err |= DA_DEVERR_SLOT;
+    }
+  }
+  if (err) atomicOr(p.err, err);
+}
+
+}  // namespace
+
+cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream) {
+  // one block up to 2048 tokens (a decode step), then 4 tokens a thread, at most
+  // one block for each SM
+  int64_t blocks = (p.slot_capacity + 4 * kThreads - 1) / (4 * kThreads);
+  if (blocks < 1) blocks = 1;
+  if (blocks > num_sms) blocks = num_sms;
+  tables_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace da

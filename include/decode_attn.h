@@ -97,7 +97,12 @@ enum {
   DA_DEVERR_SPARSE_INDEX = 2u, /* kv_idx outside the cache or kv_num_blks outside
                                   [0, max_sparse_blocks]: block skipped / count clamped   */
   DA_DEVERR_SEQ_LEN = 4u,      /* seq_lens[b] < 0 or over the cache capacity: clamped      */
-  DA_DEVERR_TIMEOUT = 8u       /* a pipeline wait gave up after its time limit             */
+  DA_DEVERR_TIMEOUT = 8u,      /* a pipeline wait gave up after its time limit             */
+  DA_DEVERR_NO_PAGES = 16u,    /* the free pages do not cover a row's new tokens, or num_free
+                                  is outside [0, free_capacity]                            */
+  DA_DEVERR_SLOT = 32u,        /* a slot outside the cache (token skipped), or more new
+                                  tokens than slot_map holds                               */
+  DA_DEVERR_POSITION = 64u     /* a position outside the cosine table: token skipped       */
 };
 
 /*
@@ -366,6 +371,161 @@ da_status decode_attn_run_noalloc(da_ctx *ctx, const da_args *args, da_stream_t 
  * CUDA.
  */
 da_status decode_attn_get_error_noalloc(da_ctx *ctx, da_stream_t stream, uint32_t *flags);
+
+/*
+ * The cache around the decode: tables from request lengths, rows written, rows
+ * read back. The three calls below take a planned context for the cache's layout
+ * and element kind, and its workspace (its first 256 bytes: the error word that
+ * decode_attn_get_error reads, and a counter). They only enqueue one kernel on
+ * `stream`. A slot is one position of the cache: page * page_size + offset, or
+ * batch row * max_seq_len + position in a contiguous cache.
+ */
+
+/*
+ * Arguments of decode_attn_build_tables: device pointers, caller-owned.
+ *
+ *   seq_lens     int32 [B], positions each row has cached
+ *   new_lens     int32 [B], tokens each row gets now (0 allowed)
+ *   free_pages   int32 [free_capacity], ids of unused pages, a stack of num_free[0]
+ *                entries whose end is its top; NULL: nothing is allocated, the
+ *                table already holds the pages (contiguous caches: NULL)
+ *   num_free     int32 [1]; NULL without free_pages
+ *   block_table  int32 [B][max_pages_per_seq], read for the pages a row has, written
+ *                for the ones it gets; no other entry is touched. Contiguous: NULL
+ *   seq_lens_out int32 [B], may be seq_lens: the lengths with the new tokens
+ *   num_free_out int32 [1], may be num_free; NULL without free_pages
+ *   slot_map     int64 [slot_capacity]: the slot of each new token, row after row in
+ *                order of position; -1 for tokens that got none and past the last token
+ *   positions    int32 [slot_capacity], optional: each token's position (0 past the last)
+ *   token_row    int32 [slot_capacity], optional: each token's batch row (-1 past the last)
+ *   cu_new       int32 [B + 1], optional: tokens of the rows before each row
+ */
+typedef struct {
+  const int32_t *seq_lens;
+  const int32_t *new_lens;
+  const int32_t *free_pages;
+  const int32_t *num_free;
+  int32_t *block_table;
+  int32_t *seq_lens_out;
+  int32_t *num_free_out;
+  int64_t *slot_map;
+  int32_t *positions;
+  int32_t *token_row;
+  int32_t *cu_new;
+  int32_t free_capacity;
+  int32_t slot_capacity;
+} da_table_args;
+
+/*
+ * Builds the block table and the slots of the tokens that B requests get now,
+ * from their lengths alone. Rows take pages from the top of the stack in order of
+ * b, each row's pages in order of position. A row whose pages are not all there
+ * gets no token (its length, its table row and its slots say so, -1) and neither
+ * does a later row that needs a page: DA_DEVERR_NO_PAGES. Tokens past the row's
+ * capacity get no slot (DA_DEVERR_SEQ_LEN), and a page id outside the pool gives -1
+ * (DA_DEVERR_PAGE_INDEX). No output may overlap an input except where said.
+ * Errors: INVALID_ARG, UNSUPPORTED (a capacity of 2^31 positions), WORKSPACE,
+ * NOT_PLANNED, CUDA.
+ */
+da_status decode_attn_build_tables(da_ctx *ctx, const da_table_args *args, void *workspace,
+                                   size_t workspace_bytes, da_stream_t stream);
+
+/*
+ * Arguments of decode_attn_append: device pointers unless said, caller-owned.
+ *
+ *   q, k_new, v_new  bf16 rows of num_tokens tokens, [HQ][D], [HKV][D], [HKV][D] each, the
+ *                next token's row *_stride elements on (views of one fused projection);
+ *                16-byte aligned, strides multiples of 8 of at least a row. q NULL:
+ *                no queries; k_new and v_new NULL: queries only (slot_map may be NULL).
+ *                MLA: q = the rope part of the queries [HQ][64], k_new = the latent row
+ *                [512] (stored as it is), v_new = the rope part of the key [64]
+ *   q_out        bf16 [T][HQ][D] (MLA [T][HQ][64]), the rotated queries; with q_len
+ *                Q > 1 the layout that decode_attn_run reads, [B][HQ][Q][D], token
+ *                t = b Q + i (num_tokens must be B Q). May be q itself when q_stride
+ *                is HQ D and q_len is 0 or 1; no other overlap
+ *   slot_map     int64 [T]; -1: padding, nothing of the token is read into an output. Two
+ *                tokens of one call may not have the same slot
+ *   positions    int32 [rope_axes][T], axis a at positions + a * position_stride
+ *   cos_sin      fp32 [max_position][rope_dim]: rope_dim / 2 cosines, then as many sines;
+ *                16-byte aligned. decode_attn_run's caller keeps it as it keeps weights
+ *   pair_axis    HOST memory, uint8 [rope_dim / 2], the axis whose position turns each
+ *                pair (time, height, width in any arrangement); NULL: axis 0 turns all
+ *   rope_dim     elements of a head that are turned: 0 (none), or a multiple of 16 up to
+ *                D (MLA 64). Pair i is (i, i + rope_dim / 2), or (2 i, 2 i + 1) with
+ *                rope_adjacent
+ *   k, v, k_scale, v_scale, k_scale_shift, v_scale_shift  the cache, as in da_args (the
+ *                scale words are written; the per-head scales are read)
+ */
+typedef struct {
+  const void *q;
+  const void *k_new;
+  const void *v_new;
+  int64_t q_stride, k_stride, v_stride;
+  void *q_out;
+  const int64_t *slot_map;
+  const int32_t *positions;
+  int64_t position_stride;
+  const float *cos_sin;
+  const uint8_t *pair_axis;
+  void *k;
+  void *v;
+  const float *k_scale;
+  const float *v_scale;
+  int32_t *k_scale_shift;
+  int32_t *v_scale_shift;
+  int32_t num_tokens;
+  int32_t q_len;
+  int32_t rope_axes;
+  int32_t rope_dim;
+  int32_t rope_adjacent;
+  int32_t max_position;
+} da_append_args;
+
+/*
+ * Turns the queries and the new keys by their positions and writes keys and
+ * values into the cache's rows `slot_map`, in its element kind. With cos and sin
+ * c, s of pair (a, b): (a c - b s, b c + a s), each product and sum rounded to fp32,
+ * then to bf16; that bf16 key is what a quantised cache quantises:
+ *   e4m3         e4m3(x / scale[h]), round to nearest even, saturating
+ *   e4m3, token  shift = f16((max + min) / 2), scale = f16((max - min) / 2 / 448) of the
+ *                row, 1 when that is 0; e4m3((x - shift) / scale)
+ *   int4 groups  shift = f16(min), scale = f16((max - min) / 15) of the group, 1 when that
+ *                is 0; round((x - shift) / scale) within 0..15
+ *   4-bit float  block scale = e4m3(max |x| / (6 scale[h])) of 16 elements; the e2m1 nearest
+ *                to x / (block scale * scale[h]), ties to even; zeros when that product is
+ *                below 2^-126. A NaN makes its block NaN, an infinity saturates
+ * (rows outside f16's range make an infinite scale or shift). A slot outside the
+ * cache (DA_DEVERR_SLOT) or a position outside the table (DA_DEVERR_POSITION) skips
+ * its token whole. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, NOT_PLANNED, CUDA.
+ */
+da_status decode_attn_append(da_ctx *ctx, const da_append_args *args, void *workspace,
+                             size_t workspace_bytes, da_stream_t stream);
+
+/*
+ * Arguments of decode_attn_gather: the cache (as in da_args), slot_map int64 [T],
+ * k_out and v_out bf16 [T][HKV][D] (MLA: [T][512] and [T][64]), 16-byte aligned.
+ */
+typedef struct {
+  const void *k;
+  const void *v;
+  const float *k_scale;
+  const float *v_scale;
+  const int32_t *k_scale_shift;
+  const int32_t *v_scale_shift;
+  const int64_t *slot_map;
+  void *k_out;
+  void *v_out;
+  int32_t num_tokens;
+} da_gather_args;
+
+/*
+ * Reads the cache rows `slot_map` back as bf16 (for a dense prefill over a cached
+ * prefix): the value that the element kind stands for, in fp32, rounded once to
+ * bf16. A slot of -1 leaves its output row as it was; one outside the cache does too
+ * (DA_DEVERR_SLOT). Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, NOT_PLANNED, CUDA.
+ */
+da_status decode_attn_gather(da_ctx *ctx, const da_gather_args *args, void *workspace,
+                             size_t workspace_bytes, da_stream_t stream);
 
 /* Releases the context (NULL is allowed). */
 void decode_attn_destroy(da_ctx *ctx);
