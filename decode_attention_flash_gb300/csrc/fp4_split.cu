@@ -15,9 +15,12 @@
 // pair takes a multiply by its block's scale: about 320 issue cycles per 16
 // tokens and scheduler, against 392 that the measured copy bandwidth leaves. So
 // the kernel is laid out to add as little as possible to that:
-//  - every warp streams alone: its own ring of 32-token stages, filled by
-//    untiled bulk copies of whole granules (16 rows, 1152 bytes; no tensor map),
-//    its own barriers, no producer warp and no barrier between warps until the end;
+//  - every warp streams alone: its own ring of 32-token stages, filled by its own
+//    16-byte asynchronous copies of whole granules (16 rows, 1152 bytes), and no
+//    barrier between warps until the end. (Bulk copies, one lane each, cost about 12
+//    instructions a copy: their operands are warp-uniform.) What a tile is -- its pages,
+//    its valid tokens, its addresses -- one further warp works out for all of them, a
+//    lane for each;
 //  - K: lane (r, q) of a quad takes bytes 16q..16q+15 of row r as one 16-byte load:
 //    the contraction's order is free, so these are its A fragments of all eight
 //    k-steps (Q is read in the same order), within two blocks, two scales;
@@ -43,41 +46,52 @@ constexpr int kT = 32;               // tokens per stage
 constexpr int kGran = 16;            // rows of a granule
 constexpr int kGranBytes = 1152;     // 16 x 64 code bytes, then 16 x 8 scale bytes
 constexpr int kScaleOff = 1024;
+constexpr int kQueue = 8;             // described tiles a warp may have waiting or in its ring
 constexpr int kStageBytes = 2 * (kT / kGran) * kGranBytes;  // K granules, then V granules
-constexpr float kRaise = 8.f;        // log2 headroom of the running maximum
+constexpr float kRaise = 1024.f;     // a sum of weights past this raises their reference
 
 template <int NT>
 struct F4 {
-  static constexpr int kWarps = NT == 1 ? 16 : 12;
-  static constexpr int kThreads = kWarps * 32;
+  static constexpr int kWarps = NT == 1 ? 15 : 11;                // consumers: with the producer four (three) a scheduler
+  static constexpr int kThreads = (kWarps + 1) * 32;             // and the producer warp
   static constexpr int kStages = NT == 1 ? 3 : 4;
   static constexpr int kRingBytes = kStages * kStageBytes;       // one warp's ring
-  static constexpr int oFull = kWarps * kRingBytes;
-  static constexpr int oMeta = oFull + 8 * kWarps * kStages + 16;  // + the test stall's barrier
-  static constexpr int oStat = oMeta + 32 * kWarps * kStages;    // [warp][tail|head][m|l][16]
+  static constexpr int oStall = kWarps * kRingBytes;             // the test stall's barrier
+  static constexpr int oCount = oStall + 16;                     // [16] tiles described, [16] tiles read, per warp
+  static constexpr int oDesc = oCount + 128;                     // [warp][kQueue] F4Tile
+  static constexpr int oStat = oDesc + kWarps * kQueue * 48;     // [warp][tail|head][m|l][16]
   static constexpr int oScan = oStat + kWarps * 64 * 4;
   static constexpr int oFlags = oScan + 16 * 4;                  // 40 ints, as in gqa_split.cuh
-  static constexpr int oStart = oFlags + 40 * 4;                 // [warp] int64 first tile of the start unit
-  static constexpr int oStartU = oStart + kWarps * 8;            // [warp] start unit
-  static constexpr int oLead = oStartU + kWarps * 4;             // [warp + 1] groups (see below)
-  static constexpr int kTotal = oLead + (kWarps + 1) * 16 + 128;
+  static constexpr int oStart = oFlags + 40 * 4;                 // [warp] F4Start
+  static constexpr int oLead = oStart + kWarps * 32;             // [warp + 1] groups (see below)
+  static constexpr int oSum = oLead + (kWarps + 1) * 16;         // [warp + 1][16] 1 / L, [..][16] LSE
+  static constexpr int kTotal = oSum + (kWarps + 1) * 32 * 4 + 128;
   static_assert(kRingBytes >= NT * 8 * kD * 4, "a warp's ring holds its piece after the stream");
-  static_assert(kRingBytes % 128 == 0 && oFull % 16 == 0 && oMeta % 16 == 0 && oStart % 8 == 0, "alignment");
+  static_assert(kRingBytes % 128 == 0 && oDesc % 16 == 0 && oStart % 16 == 0 && oLead % 16 == 0,
+                "alignment");
+  static_assert(kTotal <= 232448, "shared memory of a CTA");
 };
 
-struct __align__(16) F4Meta {
-  uint32_t valid;   // bit t: token t of the stage is a valid position
-  int32_t unit;
-  int32_t flags;    // kFirst, kLast, kFull; kUnitStart / kUnitEnd: the unit's first / last tile
-  int32_t nval;     // the row's length minus the stage's first position
-  int32_t pos0;     // the stage's first position in the row
-  int32_t warps;    // first and last warp of this CTA holding the unit (bits 0-7, 8-15),
-                    // whether the last one goes on to another unit (bit 16), and
-                    // whether the unit reaches other CTAs (bit 17)
-  int32_t c_first, n_seg;
+// A tile as the walker describes it to the warp that reads it: the valid tokens
+// (bit t: token t of the stage), flags (kFirst, kLast, kFull; kUnitStart / kUnitEnd:
+// the unit's first / last tile), for the masks the row's length minus the tile's
+// first position and that position; the byte offsets of its two halves' granules (in
+// K and V alike; a half without a valid token is not read); the unit, its number of
+// tiles and its first tile.
+struct __align__(16) F4Tile {
+  uint32_t valid;
+  int32_t flags, nval, pos0;
+  int64_t off0, off1;
+  int32_t unit, tiles;
+  int64_t P;
 };
-static_assert(sizeof(F4Meta) == 32, "layout");
 constexpr int32_t kUnitStart = 8, kUnitEnd = 16;
+// Where a warp's range starts: its unit, that unit's first tile and its UnitInfo.
+struct __align__(16) F4Start {
+  int64_t P;
+  int32_t unit, n_valid, tiles, nbp, trow, pad;
+};
+static_assert(sizeof(F4Tile) == 48 && sizeof(F4Start) == 32, "layout");
 
 __device__ __forceinline__ UnitInfo f4_unit_info(const GqaParams &p, int u, uint32_t &err) {
   UnitInfo x = unit_info(p, u, err);
@@ -100,6 +114,79 @@ __device__ __forceinline__ uint32_t f4_mul2(uint32_t x, uint32_t y) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
   return *reinterpret_cast<const uint32_t *>(&r);
 }
+// A pair times the low or the high half of `s`.
+__device__ __forceinline__ uint32_t f4_scale(uint32_t x, uint32_t s, int high) {
+  const __half2 h = *reinterpret_cast<const __half2 *>(&s);
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), high ? __high2half2(h) : __low2half2(h));
+  return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// All threads merge the n <= 32 pieces of `unit` that CTAs c_first .. c_first + n - 1
+// left (slots unit + cta) into the final output: warp g takes row g's LSEs, one
+// piece a lane, for the weights; the threads' loads of the pieces' O, kLoads at a
+// time, are in flight meanwhile. `scr`: shared memory, free.
+template <int THREADS>
+__device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first, int n, int G, float *scr) {
+  constexpr int kLoads = 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int nout = G * (kD / 4);
+  const int64_t slot0 = (int64_t)unit + c_first;
+  float *w = scr;                                          // [G][32] weights over their sum
+  float4 *acc = reinterpret_cast<float4 *>(scr + G * 32);  // [parts][nout]
+  const int parts = max(1, min(THREADS / nout, n));        // threads that share an output
+  const float4 *src = reinterpret_cast<const float4 *>(p.o_part + slot0 * G * kD);
+  const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
+  const int64_t row0 = (int64_t)b * p.num_q_heads + h * G;
+  for (int g = warp; g < G; g += THREADS / 32) {
+    const float l = lane < n ? __ldcg(p.lse_part + (slot0 + lane) * G + g) : neg_inf();
+    float M = l;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float e = l == neg_inf() ? 0.f : ex2((l - M) * 1.4426950408889634f);
+    float sum = e;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    w[g * 32 + lane] = sum == 0.f ? 0.f : e / sum;
+    if (lane == 0 && p.lse) p.lse[row0 + g] = sum == 0.f ? neg_inf() : M + __log2f(sum) * 0.69314718055994531f;
+  }
+  for (int item = tid; item < nout * parts; item += THREADS) {
+    const int o = item % nout, s0 = item / nout, g = o / (kD / 4);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s = s0; s < n; s += parts * kLoads) {
+      float4 v[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        v[k] = s + k * parts < n ? __ldcg(src + (int64_t)(s + k * parts) * nout + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+      if (item == tid && s == s0) __syncthreads();  // (every thread comes here once) the weights are in w
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) {
+        const float e = s + k * parts < n ? w[g * 32 + s + k * parts] : 0.f;
+        if (e != 0.f) {  // a piece of weight 0 may hold anything
+          a.x += e * v[k].x;
+          a.y += e * v[k].y;
+          a.z += e * v[k].z;
+          a.w += e * v[k].w;
+        }
+      }
+    }
+    acc[item] = a;
+  }
+  if (tid >= nout * parts) __syncthreads();  // (threads without an item: the barrier above)
+  __syncthreads();
+  for (int o = tid; o < nout; o += THREADS) {
+    float4 a = acc[o];
+    for (int k = 1; k < parts; ++k) {
+      const float4 v = acc[k * nout + o];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    *reinterpret_cast<uint2 *>(p.out + row0 * kD + 4 * o) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+  }
+  __syncthreads();
+}
+constexpr int kOneLevel = 32;  // pieces that f4_merge takes; a unit of more is merged in two levels
 
 template <int NT, int MOD>
 __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
@@ -112,10 +199,9 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   float *stat_all = reinterpret_cast<float *>(smem + C::oStat);
   int *scan = reinterpret_cast<int *>(smem + C::oScan);
   volatile int *flags = reinterpret_cast<volatile int *>(smem + C::oFlags);
-  // flags: [0] a wait gave up; [12] merges owed, [13] scratch, [24..31] those
-  // merges (record_merge of gqa_split.cuh)
-  int64_t *wstart = reinterpret_cast<int64_t *>(smem + C::oStart);
-  int *wunit = reinterpret_cast<int *>(smem + C::oStartU);
+  // flags: [0] a wait gave up; [13] scratch, [24..31] the merges owed (two: unit,
+  // c_first, n_seg, group; unit -1: none)
+  F4Start *start = reinterpret_cast<F4Start *>(smem + C::oStart);
   // Groups: the pieces of one unit inside this CTA, warps a..b. Entry a, written
   // by warp a (entry W when the piece is warp 0's head alone): unit (-1: none); b,
   // with bit 8 when warp b goes on to another unit; c_first; n_seg (0: the whole
@@ -131,7 +217,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   if (threadIdx.x == 0) {
     if (p.paged) prefetch_share_l2(p.block_table, (int64_t)p.batch * p.max_pages * 4);
     flags[0] = 0;
-    flags[12] = 0;
+    flags[24] = flags[28] = -1;
   }
   if (threadIdx.x <= W) lead[threadIdx.x] = make_int4(-1, 0, 0, 0);
 
@@ -161,8 +247,14 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           const int64_t s = lo + (int64_t)w * n_cta / W;
           if (s >= Pu + t_u) break;
           if (s >= Pu) {
-            wstart[w] = Pu;
-            wunit[w] = u;
+            F4Start f;
+            f.P = Pu;
+            f.unit = u;
+            f.n_valid = x.n_valid;
+            f.tiles = x.tiles;
+            f.nbp = x.nbp;
+            f.trow = x.trow;
+            start[w] = f;
           }
         }
       }
@@ -179,39 +271,40 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     if (dev_err) atomicOr(p.err, dev_err);
     return;
   }
-  uint8_t *ring = smem + (size_t)warp * C::kRingBytes;
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::oFull) + warp * S;
-  uint64_t *stall_bar = reinterpret_cast<uint64_t *>(smem + C::oFull) + W * S;  // nothing arrives on it
-  F4Meta *meta = reinterpret_cast<F4Meta *>(smem + C::oMeta) + warp * S;
-  if (lane == 0) {
-    for (int s = 0; s < S; ++s) mbar_init(&full[s], 1);
-    if (warp == 0) mbar_init(stall_bar, 1);
+  uint64_t *stall_bar = reinterpret_cast<uint64_t *>(smem + C::oStall);  // nothing arrives on it
+  uint32_t *ready_all = reinterpret_cast<uint32_t *>(smem + C::oCount);  // tiles described, per warp
+  uint32_t *done_all = ready_all + 16;                                   // and tiles read
+  F4Tile *tiles_all = reinterpret_cast<F4Tile *>(smem + C::oDesc);
+  if (threadIdx.x == 0) {
+    mbar_init(stall_bar, 1);
     fence_mbar_init();
   }
+  if (threadIdx.x < 32) ready_all[threadIdx.x] = 0u;
   __syncthreads();
 
-  const int64_t wlo = lo + (int64_t)warp * n_cta / W, whi = lo + (int64_t)(warp + 1) * n_cta / W;
-  const int ntiles = (int)(whi - wlo);
   bool ok = true;
-  int issued = 0;
-
-  if (ntiles == 0) stat_all[warp * 64 + lane] = 0.f;  // no piece: weight 0 in the sums below
-  if (ntiles > 0) {
-    // ------------------------------------------------------------ the walker of this warp's tiles
-    const int q4 = lane & 3, r8 = lane >> 2;
+  if (warp == W) {
+    // ============================================================ the walker
+    // Lane w walks the tiles of warp w's range, a few tiles ahead of it: which pages or
+    // blocks, which tokens are valid, where the bytes are. One pass of the loop serves
+    // every warp, so the walk costs a fraction of what it would in each of them.
+    const int w = lane < W ? lane : 0;
+    const int64_t wlo = lo + (int64_t)w * n_cta / W, whi = lo + (int64_t)(w + 1) * n_cta / W;
+    const int ntiles = lane < W ? (int)(whi - wlo) : 0;
+    F4Tile *queue = tiles_all + w * kQueue;
     const int P = p.page_size;
     const bool sparse = p.sparse_block_size > 0;
     // entries (pages or listed blocks) of `tpe` tiles each; pages of 16 tokens: two per tile
     const int tpe = sparse ? p.sparse_block_size / kT : (p.paged ? (P >= kT ? P / kT : 1) : 1);
     const bool two_pages = p.paged && P < kT;
     const bool has_ids = p.paged || sparse;
-    const int64_t gran_unit = p.paged ? P / kGran : p.cache_len / kGran;  // granules per (page | row, head)
-    int u = wunit[warp], j = (int)(wlo - wstart[warp]);
-    int64_t Pu = wstart[warp];
+    const int gran_unit = p.paged ? P / kGran : p.cache_len / kGran;  // granules per (page | row, head)
+    int u = 0, j = 0, ent = 0, sub = 0, nent = 0;  // unit, its tile, current entry, tile inside it, entries
+    int id0 = -1, id1 = -1;                        // the current tile's ids
+    int64_t Pu = 0;
     UnitInfo x;
-    int ent = 0, sub = 0, nent = 0;     // current entry, tile inside it, entries of the unit
-    int wbase = 0, wid = -1, wnext = -1;  // 32 entry ids from wbase (one per lane), and the next 32
-    int winfo = 0, c_first = 0, n_seg = 0;
+    x.b = x.h = x.n_valid = x.nbp = x.trow = 0;
+    x.tiles = 1;
     auto load_id = [&](int e) -> int {
       if (e >= nent) return -1;
       if (sparse)
@@ -219,128 +312,182 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
                          : __ldg(p.kv_full_idx + (int64_t)x.trow * p.max_sparse_blocks + e - x.nbp);
       return __ldg(p.block_table + (int64_t)x.b * p.max_pages + e);
     };
+    auto load_ids = [&]() {
+      id0 = load_id(ent);
+      if (two_pages) id1 = load_id(ent + 1);
+    };
     auto enter_unit = [&]() {  // x holds unit u's info; tile j of it comes next
       if (has_ids) {
-        if (two_pages) {
-          ent = 2 * j;
-          sub = 0;
-        } else {
-          ent = j / tpe;
-          sub = j - ent * tpe;
-        }
+        ent = two_pages ? 2 * j : j / tpe;
+        sub = two_pages ? 0 : j - ent * tpe;
         nent = sparse ? x.tiles / tpe : (x.n_valid + P - 1) / P;
-        wbase = ent;
-        wid = load_id(ent + lane);
-        wnext = load_id(ent + 32 + lane);
+        load_ids();
       }
-      const int64_t a = Pu < lo ? lo : Pu, b = Pu + x.tiles > hi ? hi : Pu + x.tiles;
-      const bool outside = Pu < lo || Pu + x.tiles > hi;
-      const int bw = cta_of(b - 1 - lo, n_cta, W);
-      const bool goes_on = b < lo + (int64_t)(bw + 1) * n_cta / W;
-      winfo = cta_of(a - lo, n_cta, W) | (bw << 8) | (goes_on ? 1 << 16 : 0) | (outside ? 1 << 17 : 0);
-      c_first = outside ? cta_of(Pu, T, CTAS) : cta;
-      n_seg = outside ? cta_of(Pu + x.tiles - 1, T, CTAS) - c_first + 1 : 0;
+      prefetch_l2(p.q + ((int64_t)x.b * p.num_q_heads + x.h * G) * kD, (uint32_t)(G * kD * 2));
     };
-    x = f4_unit_info(p, u, dev_err);
-    enter_unit();
-
-    auto issue = [&](int i) {
-      const int st = i % S;
-      const int tok0 = j * kT;
-      int pos0 = tok0;
-      int64_t gr0 = -1, gr1 = -1;  // granules of the stage's two halves
-      uint32_t valid = 0;
-      bool full_blk = false;
-      if (!has_ids) {
-        gr0 = (int64_t)u * gran_unit + tok0 / kGran;
-        gr1 = gr0 + 1;
-        valid = (uint32_t)low_bits(min(x.n_valid - tok0, kT));
-      } else {
-        if (ent >= wbase + 32) {
-          wid = wnext;
-          wbase += 32;
-          wnext = load_id(wbase + 32 + lane);
-        }
-        if (two_pages) {
-          const int id0 = __shfl_sync(0xffffffffu, wid, ent - wbase);
-          const int id1 = __shfl_sync(0xffffffffu, wid, ent + 1 - wbase);  // wbase is even: same window
-          const bool in1 = tok0 + kGran < x.n_valid;
-          const bool ok0 = id0 >= 0 && id0 < p.num_pages, ok1 = in1 && id1 >= 0 && id1 < p.num_pages;
-          if (!ok0 || (in1 && !ok1)) dev_err |= DA_DEVERR_PAGE_INDEX;
-          const uint32_t v = (uint32_t)low_bits(min(x.n_valid - tok0, kT));
-          if (ok0) {
-            gr0 = (int64_t)id0 * p.num_kv_heads + x.h;
-            valid |= v & 0xFFFFu;
-          }
-          if (ok1) {
-            gr1 = (int64_t)id1 * p.num_kv_heads + x.h;
-            valid |= v & 0xFFFF0000u;
-          }
-          ent += 2;
-        } else {
-          const int id = __shfl_sync(0xffffffffu, wid, ent - wbase);
-          if (sparse) {
-            full_blk = ent >= x.nbp;
-            if (id < 0 || (int64_t)id * p.sparse_block_size >= p.cache_len) {
-              dev_err |= DA_DEVERR_SPARSE_INDEX;
-            } else {
-              pos0 = id * p.sparse_block_size + sub * kT;
-              valid = (uint32_t)low_bits(min(min(x.n_valid - pos0, kT), p.cache_len - pos0));
-              gr0 = (int64_t)u * gran_unit + pos0 / kGran;
-            }
-          } else if (id < 0 || id >= p.num_pages) {
-            dev_err |= DA_DEVERR_PAGE_INDEX;
+    if (ntiles > 0) {
+      const F4Start f0 = start[w];
+      u = f0.unit;
+      Pu = f0.P;
+      j = (int)(wlo - Pu);
+      x.b = u / p.num_kv_heads;
+      x.h = u - x.b * p.num_kv_heads;
+      x.n_valid = f0.n_valid;
+      x.tiles = f0.tiles;
+      x.nbp = f0.nbp;
+      x.trow = f0.trow;
+      enter_unit();
+    }
+    int i = 0;
+    uint64_t since = 0;
+    while (true) {
+      const bool go = i < ntiles && i < (int)ld_acquire_cta(&done_all[w]) + kQueue;
+      if (go) {
+        int pos0 = j * kT;
+        uint32_t valid = 0;
+        int64_t gr0, gr1;
+        bool full_blk = false;
+        if (sparse) {
+          full_blk = ent >= x.nbp;
+          if (id0 < 0 || (int64_t)id0 * p.sparse_block_size >= p.cache_len) {
+            dev_err |= DA_DEVERR_SPARSE_INDEX;
           } else {
-            valid = (uint32_t)low_bits(min(x.n_valid - tok0, kT));
-            gr0 = ((int64_t)id * p.num_kv_heads + x.h) * gran_unit + sub * (kT / kGran);
+            pos0 = id0 * p.sparse_block_size + sub * kT;
+            valid = (uint32_t)low_bits(min(min(x.n_valid - pos0, kT), p.cache_len - pos0));
           }
-          gr1 = gr0 >= 0 ? gr0 + 1 : -1;
-          if (++sub == tpe) {
+          gr0 = (int64_t)u * gran_unit + pos0 / kGran;
+          gr1 = gr0 + 1;
+        } else {
+          const int left = x.n_valid - pos0;  // at least 1
+          valid = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
+          if (!p.paged) {
+            gr0 = (int64_t)u * gran_unit + j * (kT / kGran);
+            gr1 = gr0 + 1;
+          } else if (two_pages) {
+            const bool ok0 = (uint32_t)id0 < (uint32_t)p.num_pages, ok1 = (uint32_t)id1 < (uint32_t)p.num_pages;
+            if (!ok0 || (left > kGran && !ok1)) dev_err |= DA_DEVERR_PAGE_INDEX;
+            valid &= (ok0 ? 0xFFFFu : 0u) | (ok1 ? 0xFFFF0000u : 0u);
+            gr0 = (int64_t)id0 * p.num_kv_heads + x.h;
+            gr1 = (int64_t)id1 * p.num_kv_heads + x.h;
+          } else {
+            if ((uint32_t)id0 >= (uint32_t)p.num_pages) {
+              dev_err |= DA_DEVERR_PAGE_INDEX;
+              valid = 0;
+            }
+            gr0 = ((int64_t)id0 * p.num_kv_heads + x.h) * gran_unit + sub * (kT / kGran);
+            gr1 = gr0 + 1;
+          }
+        }
+        const int fl = (i == 0 || j == 0 ? kFirst : 0) | (i + 1 == ntiles || j + 1 == x.tiles ? kLast : 0) |
+                       (full_blk ? kFull : 0) | (j == 0 ? kUnitStart : 0) | (j + 1 == x.tiles ? kUnitEnd : 0);
+        F4Tile t;
+        t.valid = valid;
+        t.flags = fl;
+        t.nval = x.n_valid - pos0;
+        t.pos0 = pos0;
+        t.off0 = gr0 * kGranBytes;
+        t.off1 = gr1 * kGranBytes;
+        t.unit = u;
+        t.tiles = x.tiles;
+        t.P = Pu;
+        queue[i % kQueue] = t;
+        ++i;
+        st_release_cta(&ready_all[w], (uint32_t)i);
+        // the next tile, its ids in flight until there is room for it
+        if (++j < x.tiles) {
+          if (two_pages) {
+            ent += 2;
+            load_ids();
+          } else if (has_ids && ++sub == tpe) {
             sub = 0;
             ++ent;
+            load_ids();
           }
+        } else if (i < ntiles) {
+          Pu += x.tiles;
+          do {
+            ++u;
+            x = f4_unit_info(p, u < U ? u : U - 1, dev_err);
+          } while (u < U && x.tiles == 0);
+          j = 0;
+          enter_unit();
         }
       }
-      const bool v0 = (valid & 0xFFFFu) != 0, v1 = (valid >> 16) != 0;  // halves with no token are not read
-      if (lane == 0) {
-        F4Meta m;
-        m.valid = valid;
-        m.unit = u;
-        m.flags = (i == 0 || j == 0 ? kFirst : 0) | (i + 1 == ntiles || j + 1 == x.tiles ? kLast : 0) |
-                  (full_blk ? kFull : 0) | (j == 0 ? kUnitStart : 0) | (j + 1 == x.tiles ? kUnitEnd : 0);
-        m.nval = x.n_valid - pos0;
-        m.pos0 = pos0;
-        m.warps = winfo;
-        m.c_first = c_first;
-        m.n_seg = n_seg;
-        meta[st] = m;
-        mbar_arrive_expect_tx(&full[st], (v0 ? 2u * kGranBytes : 0u) + (v1 ? 2u * kGranBytes : 0u));
+      if (!__any_sync(0xffffffffu, i < ntiles)) break;
+      if (__any_sync(0xffffffffu, go)) {
+        since = 0;
+      } else {
+        // every queue is full: wait a little (bounded, like every wait)
+        const uint64_t now = global_timer_ns();
+        if (since == 0) since = now;
+        if (flags[0] || now - since > kWaitLimitNs) {
+          ok = false;
+          break;
+        }
+        __nanosleep(100);
       }
-      __syncwarp();
-      // lane 0, 1: K and V of the first half; 2, 3: of the second
-      if (lane < 4) {
-        const int64_t gr = lane < 2 ? gr0 : gr1;
-        if (lane < 2 ? v0 : v1)
-          bulk_copy_g2s(ring + st * kStageBytes + ((lane & 1) * 2 + (lane >> 1)) * kGranBytes,
-                        (lane & 1 ? fp.v : fp.k) + gr * kGranBytes, kGranBytes, &full[st]);
-      }
-      issued = i + 1;
-      if (++j == x.tiles && i + 1 < ntiles) {
-        Pu += x.tiles;
-        do {
-          ++u;
-          x = f4_unit_info(p, u < U ? u : U - 1, dev_err);
-        } while (u < U && x.tiles == 0);
-        j = 0;
-        enter_unit();
-      }
+    }
+    if (!__all_sync(0xffffffffu, ok)) {
+      dev_err |= DA_DEVERR_TIMEOUT;
+      flags[0] = 1;
+    }
+    __syncthreads();
+    if (flags[0]) {
+      if (dev_err) atomicOr(p.err, dev_err);
+      return;
+    }
+  } else {
+    // ============================================================ consumers
+    const int q4 = lane & 3, r8 = lane >> 2;
+    const int64_t wlo = lo + (int64_t)warp * n_cta / W, whi = lo + (int64_t)(warp + 1) * n_cta / W;
+    const int ntiles = (int)(whi - wlo);
+    uint8_t *ring = smem + (size_t)warp * C::kRingBytes;
+    const F4Tile *queue = tiles_all + warp * kQueue;
+    if (ntiles == 0) stat_all[warp * 64 + lane] = 0.f;  // no piece: weight 0 in the sums below
+    // Tile i's copies into stage `to`: 16 bytes a lane, 72 lanes' worth a granule, one
+    // commit group. False when the walker stays away.
+    uint32_t ready = 0;
+    const uint8_t *k_lane = fp.k + lane * 16, *v_lane = fp.v + lane * 16;
+    const uint32_t ring_lane = smem_u32(ring) + lane * 16;
+    auto copy = [&](uint32_t dst, const uint8_t *src) {
+      cp_async_16(dst, src);
+      cp_async_16(dst + 512, src + 512);
+      if (lane < 8) cp_async_16(dst + 1024, src + 1024);
     };
-    for (int i = 0; i < S && i < ntiles; ++i) issue(i);
-
+    auto issue = [&](int i, int to) -> bool {
+      if ((int)ready <= i) {
+        ready = ld_acquire_cta(&ready_all[warp]);
+        if ((int)ready <= i) {
+          const uint64_t t0 = global_timer_ns();
+          while ((int)(ready = ld_acquire_cta(&ready_all[warp])) <= i)
+            if (flags[0] || global_timer_ns() - t0 > kWaitLimitNs) break;
+        }
+        ready = __reduce_min_sync(0xffffffffu, ready);
+        if ((int)ready <= i) return false;
+      }
+      const F4Tile *t = &queue[i % kQueue];
+      const uint32_t valid = t->valid;
+      const longlong2 off = *reinterpret_cast<const longlong2 *>(&t->off0);
+      const uint32_t dst = ring_lane + to * kStageBytes;
+      if (valid & 0xFFFFu) {
+        copy(dst, k_lane + off.x);
+        copy(dst + 2 * kGranBytes, v_lane + off.x);
+      }
+      if (valid >> 16) {
+        copy(dst + kGranBytes, k_lane + off.y);
+        copy(dst + 3 * kGranBytes, v_lane + off.y);
+      }
+      return true;
+    };
+    for (int i = 0; i < S; ++i) {
+      if (ok && i < ntiles) ok = issue(i, i);
+      cp_async_commit();
+    }
     // ------------------------------------------------------------ the stream
     uint32_t qf[NT][8][2];
     float oacc[NT][8][4];
-    float m_run[NT][2], l_part[NT][2];
+    float m_neg[NT][2], l_part[NT][2];  // minus the weights' reference (log2 units), and their sums
+    bool no_ref[NT][2];
     float sscale = p.score_scale, vmul = 1.f;
     const bool softcap = MOD >= 1 && p.softcap_l2 > 0.f;
     const bool mods = MOD == 2 && (p.mask_window != nullptr || p.alibi_slopes != nullptr);
@@ -354,20 +501,38 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         mword[nt][e] = (2u << trow[nt][e]) - 1u;
       }
     bool from_start = false;  // the segment holds its unit's first tile
+    bool fresh = false;       // no reference for the segment's weights yet
+    int unit = 0;
     // (the test stall of GqaParams, in the warp that always has a tile: the timeout path
     // runs as after a real failure)
     if (p.test_stall_ns != 0 && warp == W - 1) ok = warp_wait(stall_bar, 0u, p.test_stall_ns);
+    int st = -1;
+    const int k_off = r8 * 64 + q4 * 16, ks_off = kScaleOff + r8 * 8 + q4 * 2;          // this lane in a K granule
+    const int v_off = q4 * 128 + r8 * 8, vs_off = kScaleOff + q4 * 16 + r8;             // and in a V granule
     for (int i = 0; ok && i < ntiles; ++i) {
-      const int st = i % S;
-      if (!warp_wait(&full[st], (i / S) & 1, kWaitLimitNs)) {
-        ok = false;
-        break;
+      st = st + 1 == S ? 0 : st + 1;
+      cp_async_wait_group<S - 1>();  // this lane's copies of tile i have landed,
+      __syncwarp();                  // and so have the other lanes'
+      const F4Tile *tile = &queue[i % kQueue];
+      uint32_t valid;
+      int fl, nval = 0, pos0 = 0;
+      if (MOD == 0) {
+        const uint2 m = *reinterpret_cast<const uint2 *>(tile);
+        valid = m.x;
+        fl = (int)m.y;
+      } else {
+        const uint4 m = *reinterpret_cast<const uint4 *>(tile);
+        valid = m.x;
+        fl = (int)m.y;
+        nval = (int)m.z;
+        pos0 = (int)m.w;
       }
-      const F4Meta m = meta[st];
       const uint8_t *stage = ring + st * kStageBytes;
-      if (m.flags & kFirst) {
-        from_start = (m.flags & kUnitStart) != 0;
-        const int b = m.unit / p.num_kv_heads, h = m.unit - b * p.num_kv_heads;
+      if (fl & kFirst) {
+        from_start = (fl & kUnitStart) != 0;
+        fresh = true;
+        unit = tile->unit;
+        const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
         // Q^T fragments straight from global memory: k-step s of lane (r8, q4) is
         // dims 32 q4 + 4s .. + 3 of row r8 (the bytes a lane has of a K row). The
         // rows are scaled by one power of two into f16's range (gqa_split.cuh).
@@ -405,6 +570,9 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
             qf[nt][s][1] = bf16x2_to_f16x2(qw[nt][s].y, q2);
           }
         sscale = p.score_scale * p.k_scale[h] * pow2f(-qexp);
+        // a zero factor (uniform weights) as 2^-100: a finite score still weighs 1, and
+        // an infinite one (a masked token's) 0
+        if (sscale == 0.f) sscale = 0x1p-100f;
         vmul = p.v_scale[h];
         if (MOD >= 1 && p.spec_mask != nullptr) {
           const uint32_t *mrow = p.spec_mask + (size_t)b * p.q_len;
@@ -419,35 +587,34 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) oacc[nt][mt][e] = 0.f;
-          m_run[nt][0] = m_run[nt][1] = neg_inf();
+          m_neg[nt][0] = m_neg[nt][1] = 0.f;
+          no_ref[nt][0] = no_ref[nt][1] = true;
           l_part[nt][0] = l_part[nt][1] = 0.f;
         }
       }
-      if (m.valid != 0) {
+      if (valid != 0) {
         // ---------------- S^T = K Q^T, two granules of 16 tokens
         float s[NT][2][4];
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[nt][gi][0] = s[nt][gi][1] = s[nt][gi][2] = s[nt][gi][3] = 0.f;
-          if (((m.valid >> (16 * gi)) & 0xFFFFu) == 0) continue;
+          if (((valid >> (16 * gi)) & 0xFFFFu) == 0) continue;
           const uint8_t *gk = stage + gi * kGranBytes;
-          const uint4 ra = *reinterpret_cast<const uint4 *>(gk + r8 * 64 + q4 * 16);
-          const uint4 rb = *reinterpret_cast<const uint4 *>(gk + (r8 + 8) * 64 + q4 * 16);
-          const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + kScaleOff + r8 * 8 + q4 * 2));
-          const uint32_t sb =
-              e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + kScaleOff + (r8 + 8) * 8 + q4 * 2));
+          const uint4 ra = *reinterpret_cast<const uint4 *>(gk + k_off);
+          const uint4 rb = *reinterpret_cast<const uint4 *>(gk + k_off + 512);
+          const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + ks_off));
+          const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + ks_off + 64));
           const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
           for (int c = 0; c < 4; ++c) {  // word c: k-steps 2c and 2c + 1, block c / 2 of the lane's two
             uint32_t fa[4], fb[4];
             e2m1x8_to_f16(wa[c], fa);
             e2m1x8_to_f16(wb[c], fb);
-            const uint32_t xa = prmt(sa, 0, c < 2 ? 0x1010 : 0x3232), xb = prmt(sb, 0, c < 2 ? 0x1010 : 0x3232);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t a0 = f4_mul2(fa[2 * k], xa), a2 = f4_mul2(fa[2 * k + 1], xa);
-              const uint32_t a1 = f4_mul2(fb[2 * k], xb), a3 = f4_mul2(fb[2 * k + 1], xb);
+              const uint32_t a0 = f4_scale(fa[2 * k], sa, c >> 1), a2 = f4_scale(fa[2 * k + 1], sa, c >> 1);
+              const uint32_t a1 = f4_scale(fb[2 * k], sb, c >> 1), a3 = f4_scale(fb[2 * k + 1], sb, c >> 1);
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma_f16_16816(s[nt][gi], a0, a1, a2, a3, qf[nt][2 * c + k][0], qf[nt][2 * c + k][1]);
@@ -455,8 +622,12 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           }
         }
         // ---------------- masks and the online softmax (log2 units)
-        const bool part = m.valid != 0xFFFFFFFFu;
-        if (MOD >= 1) {  // scores become x = score * log2 e here; masked ones -inf
+        const bool part = valid != 0xFFFFFFFFu;
+        float f = sscale;  // log2 units of a score in s
+        // several query tokens: a stage of older positions only has nothing to mask
+        const bool masks = MOD == 2 || (MOD == 1 && (softcap || nval - p.q_len < kT));
+        if (MOD >= 1 && masks) {  // scores become x = score * log2 e here; masked ones -inf
+          f = 1.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -466,14 +637,14 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
                 const int t = r8 + 8 * k;  // token of the stage
                 float v = s[nt][k >> 1][(k & 1) * 2 + e] * sscale;
                 if (softcap) v = cap_tanh(v, p.softcap_l2, p.softcap_k);
-                const int jnew = t - (m.nval - p.q_len);
-                bool keep = (m.valid >> t) & 1u;
+                const int jnew = t - (nval - p.q_len);
+                bool keep = (valid >> t) & 1u;
                 keep = keep && (jnew < 0 || ((mword[nt][e] >> min(jnew, 31)) & 1u));
                 if (mods) {
                   const int row = min(nt * 8 + 2 * q4 + e, G - 1);
-                  const int hq = (m.unit % p.num_kv_heads) * (G / p.q_len) + row / p.q_len;
-                  const int kv = m.pos0 + t, qpos = m.nval + m.pos0 - p.q_len + trow[nt][e];
-                  if (p.mask_window && !(m.flags & kFull)) {
+                  const int hq = (unit % p.num_kv_heads) * (G / p.q_len) + row / p.q_len;
+                  const int kv = pos0 + t, qpos = nval + pos0 - p.q_len + trow[nt][e];
+                  if (p.mask_window && !(fl & kFull)) {
                     const int w = __ldg(p.mask_window + hq), sk = p.mask_sink ? __ldg(p.mask_sink + hq) : 0;
                     keep = keep && (kv < sk || w < 0 || kv > qpos - w);
                   }
@@ -482,46 +653,62 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
                 }
                 s[nt][k >> 1][(k & 1) * 2 + e] = keep ? v : neg_inf();
               }
+        } else if (part) {  // (dense rows of one query token; a page that was not there)
+          // a masked score takes the value whose weight is 0 whatever the scale's sign
+          const float none = sscale < 0.f ? -neg_inf() : neg_inf();
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (!((valid >> (r8 + 8 * k)) & 1u)) s[nt][k >> 1][(k & 1) * 2] = s[nt][k >> 1][(k & 1) * 2 + 1] = none;
         }
-        const float f = MOD >= 1 ? 1.f : sscale;
-        float y[NT][2][4];
-        bool raise = false;
+        // The weights 2^(x - m) against the held reference m, and their sums. The
+        // reference is raised only when a sum passes 2^10 (so no weight does, and
+        // f16 holds them all; the sums are fp32), or when there is none yet.
+        float y[NT][2][4], sum[NT][2];
+        bool raise = fresh;
+        auto weights = [&]() {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float mu = m_run[nt][e] == neg_inf() ? 0.f : m_run[nt][e];
-            raise = raise || m_run[nt][e] == neg_inf();
+            for (int e = 0; e < 2; ++e) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              float v = MOD >= 1 ? s[nt][k >> 1][(k & 1) * 2 + e] - mu
-                                 : fmaf(s[nt][k >> 1][(k & 1) * 2 + e], f, -mu);
-              if (MOD == 0 && part) v = (m.valid >> (r8 + 8 * k)) & 1u ? v : neg_inf();
-              y[nt][e][k] = v;
-              raise = raise || v > kRaise;
+              for (int k = 0; k < 4; ++k) {
+                const float v = s[nt][k >> 1][(k & 1) * 2 + e];
+                y[nt][e][k] = ex2(fmaf(v, f, m_neg[nt][e]));
+              }
+              sum[nt][e] = (y[nt][e][0] + y[nt][e][1]) + (y[nt][e][2] + y[nt][e][3]);
             }
-          }
+        };
+        weights();
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) raise = raise || sum[nt][0] > kRaise || sum[nt][1] > kRaise;
+        if (MOD >= 1)  // (a row may have had no kept token so far)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) raise = raise || no_ref[nt][0] || no_ref[nt][1];
         if (__any_sync(0xffffffffu, raise)) {
+          fresh = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float alpha[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const float mu = m_run[nt][e] == neg_inf() ? 0.f : m_run[nt][e];
-              float t = fmaxf(fmaxf(y[nt][e][0], y[nt][e][1]), fmaxf(y[nt][e][2], y[nt][e][3])) + mu;
+              float t = neg_inf();
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float v = s[nt][k >> 1][(k & 1) * 2 + e];
+                t = fmaxf(t, v * f);
+              }
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
-              const float m_new = fmaxf(m_run[nt][e], t);
+              // while no score of the row is valid the reference is 0, with nothing to rescale
+              const float m_new = no_ref[nt][e] ? t : fmaxf(-m_neg[nt][e], t);
               const float mn = m_new == neg_inf() ? 0.f : m_new;
-              alpha[e] = ex2(m_run[nt][e] - mn);
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {  // (masked scores stay -inf)
-                const float v = s[nt][k >> 1][(k & 1) * 2 + e];
-                y[nt][e][k] = y[nt][e][k] == neg_inf() ? neg_inf() : MOD >= 1 ? v - mn : fmaf(v, f, -mn);
-              }
+              alpha[e] = no_ref[nt][e] ? 1.f : ex2(-m_neg[nt][e] - mn);
+              no_ref[nt][e] = m_new == neg_inf();
+              m_neg[nt][e] = -mn;
               l_part[nt][e] *= alpha[e];
-              m_run[nt][e] = m_new;
             }
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
@@ -531,17 +718,14 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
               oacc[nt][mt][3] *= alpha[1];
             }
           }
+          weights();
         }
-        // P^T fragments: weights as f16 (at most 2^8), the row sum from the fp32 ones
+        // P^T fragments: weights as f16, the row sums from the fp32 ones
         uint32_t pb[NT][2][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) y[nt][e][k] = ex2(y[nt][e][k]);
-            l_part[nt][e] += (y[nt][e][0] + y[nt][e][1]) + (y[nt][e][2] + y[nt][e][3]);
-          }
+          l_part[nt][0] += sum[nt][0];
+          l_part[nt][1] += sum[nt][1];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             pb[nt][k >> 1][k & 1] = movmatrix_trans(pack_f16(y[nt][0][k], y[nt][1][k]));
@@ -549,7 +733,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         // ---------------- O^T += V^T P^T
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
-          const uint32_t vb = (m.valid >> (16 * gi)) & 0xFFFFu;
+          const uint32_t vb = (valid >> (16 * gi)) & 0xFFFFu;
           if (vb == 0) continue;
           const uint8_t *gv = stage + (2 + gi) * kGranBytes;
           // tokens 2 q4, 2 q4 + 1 and the same + 8: one block (8 bytes) of each, and its scale
@@ -557,12 +741,12 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           uint32_t sc[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int t = 2 * q4 + (k & 1) + 8 * (k >> 1);
-            w[k] = *reinterpret_cast<const uint2 *>(gv + t * 64 + r8 * 8);
-            sc[k] = gv[kScaleOff + t * 8 + r8];
+            const int t = (k & 1) + 8 * (k >> 1);
+            w[k] = *reinterpret_cast<const uint2 *>(gv + v_off + t * 64);
+            sc[k] = gv[vs_off + t * 8];
           }
-          uint32_t s01 = e4m3x2_to_f16x2((uint16_t)(sc[0] | (sc[1] << 8)));
-          uint32_t s89 = e4m3x2_to_f16x2((uint16_t)(sc[2] | (sc[3] << 8)));
+          uint32_t s01 = e4m3x2_to_f16x2((uint16_t)prmt(sc[0], sc[1], 0x0040));
+          uint32_t s89 = e4m3x2_to_f16x2((uint16_t)prmt(sc[2], sc[3], 0x0040));
           if (vb != 0xFFFFu) {  // a masked token's row may hold any scale (codes are finite)
             s01 &= lo16_mask((vb >> (2 * q4)) & 1u, (vb >> (2 * q4 + 1)) & 1u);
             s89 &= lo16_mask((vb >> (2 * q4 + 8)) & 1u, (vb >> (2 * q4 + 9)) & 1u);
@@ -588,23 +772,42 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           }
         }
       }
-      __syncwarp();  // every lane has read the stage
-      if (i + S < ntiles) issue(i + S);
-      if (!(m.flags & kLast)) continue;
+      int64_t seg_P = 0;
+      int seg_tiles = 0;
+      if (fl & kLast) {
+        seg_P = tile->P;
+        seg_tiles = tile->tiles;
+      }
+      __syncwarp();  // every lane has read the stage and its description
+      if (lane == 0) st_release_cta(&done_all[warp], (uint32_t)(i + 1));
+      if (i + S < ntiles) ok = issue(i + S, st);
+      cp_async_commit();  // (a group a tile, empty ones at the end)
+      if (!(fl & kLast)) continue;
       // ---------------- the segment ends. Row sums, then: a unit held by this
       // segment alone goes out from the registers; another segment's (m, l, O) to
       // this warp's ring when it is the warp's last, else to its global slot
-      const bool whole = from_start && (m.flags & kUnitEnd);
+      const bool whole = from_start && (fl & kUnitEnd);
       const bool tail = i + 1 == ntiles;
-      const int b = m.unit / p.num_kv_heads, h = m.unit - b * p.num_kv_heads;
+      const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
       float *piece = nullptr;
       if (!whole) {
         float *stat = stat_all + (warp * 2 + (tail ? 0 : 1)) * 32;
         piece = tail ? reinterpret_cast<float *>(ring)
                      : fp.o_head + ((int64_t)cta * W + warp) * G * kD;
         // the unit's first warp here names the group (a head alone is warp 0's)
-        if (lane == 0 && (m.warps & 255) == warp)
-          lead[tail ? warp : W] = make_int4(m.unit, (m.warps >> 8) & 0x1FF, m.c_first, (m.warps >> 17) ? m.n_seg : 0);
+        if (lane == 0) {
+          const int64_t first = seg_P < lo ? lo : seg_P, end = seg_P + seg_tiles > hi ? hi : seg_P + seg_tiles;
+          if (cta_of(first - lo, n_cta, W) == warp) {
+            const int bw = cta_of(end - 1 - lo, n_cta, W);
+            const bool goes_on = end < lo + (int64_t)(bw + 1) * n_cta / W;
+            int c_first = 0, n_seg = 0;
+            if (seg_P < lo || seg_P + seg_tiles > hi) {
+              c_first = cta_of(seg_P, T, CTAS);
+              n_seg = cta_of(seg_P + seg_tiles - 1, T, CTAS) - c_first + 1;
+            }
+            lead[tail ? warp : W] = make_int4(unit, bw | (goes_on ? 256 : 0), c_first, n_seg);
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -614,7 +817,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
             l += __shfl_xor_sync(0xffffffffu, l, 8);
             l += __shfl_xor_sync(0xffffffffu, l, 16);
             if (r8 == 0) {
-              stat[nt * 8 + 2 * q4 + e] = m_run[nt][e] == neg_inf() ? 0.f : m_run[nt][e];
+              stat[nt * 8 + 2 * q4 + e] = -m_neg[nt][e];
               stat[16 + nt * 8 + 2 * q4 + e] = l;
             }
           }
@@ -652,115 +855,137 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
                                     pack_bf16(oacc[nt][4 * k + 2][e] * mul, oacc[nt][4 * k + 2][2 + e] * mul),
                                     pack_bf16(oacc[nt][4 * k + 3][e] * mul, oacc[nt][4 * k + 3][2 + e] * mul));
               if (r8 == 0 && p.lse) {
-                const float mu = m_run[nt][e] == neg_inf() ? 0.f : m_run[nt][e];
-                p.lse[row] = l == 0.f ? neg_inf() : (mu + __log2f(l)) * 0.69314718055994531f;
+                p.lse[row] = l == 0.f ? neg_inf() : (__log2f(l) - m_neg[nt][e]) * 0.69314718055994531f;
               }
             }
           }
       }
     }
+    cp_async_wait_group<0>();  // no copy outlives the loop (one that gave up leaves early)
     if (!ok) {
-      // a wait gave up: wait (bounded) for the copies in flight before leaving
-      for (int st = 0; st < S && st < issued; ++st) {
-        const int last = (issued - 1) - ((issued - 1 - st) % S);
-        mbar_wait_bounded(&full[st], (last / S) & 1, kWaitLimitNs);
-      }
       dev_err |= DA_DEVERR_TIMEOUT;
       flags[0] = 1;
     }
-  }
-  __syncthreads();
-  if (flags[0]) {
-    if (dev_err) atomicOr(p.err, dev_err);
-    return;
+    __syncthreads();
+    if (flags[0]) {
+      if (dev_err) atomicOr(p.err, dev_err);
+      return;
+    }
   }
   // ---------------------------------------------------------------- pieces of this CTA, unit by unit
+  // First the weights: per group and row the reference M of its pieces, each piece's
+  // 2^(m - M) (in place of its m) and 1 / L; then the weighted sums.
   const int nout = G * (kD / 4);
-  int ngroups = 0;
-  for (int k = 0; k <= W; ++k) ngroups += lead[k].x >= 0 ? 1 : 0;
-  for (int item = threadIdx.x; item < ngroups * nout; item += C::kThreads) {
-    int k = 0;
-    for (int skip = item / nout;; ++k) {
-      if (lead[k].x < 0) continue;
-      if (skip-- == 0) break;
-    }
+  float *sums = reinterpret_cast<float *>(smem + C::oSum);
+  // the piece of group (k, b) in warp w: its head when w is the last and went on
+  auto stat_of = [&](const int4 &grp, int w) {
+    return stat_all + (w * 2 + (w == (grp.y & 255) && (grp.y & 256) ? 1 : 0)) * 32;
+  };
+  for (int i = threadIdx.x; i < (W + 1) * 16; i += C::kThreads) {
+    const int k = i >> 4, g = i & 15;
     const int4 grp = lead[k];
-    const int o = item % nout, g = o / (kD / 4);
+    if (grp.x < 0 || g >= G) continue;
     const int a = k == W ? 0 : k, bw = grp.y & 255;
-    // the last warp's piece is its head when that warp went on to another unit
-    auto stat_of = [&](int w) { return stat_all + (w * 2 + (w == bw && (grp.y & 256) ? 1 : 0)) * 32; };
     float M = neg_inf();
     for (int w = a; w <= bw; ++w) {
-      const float *st = stat_of(w);
+      const float *st = stat_of(grp, w);
       if (st[16 + g] != 0.f) M = fmaxf(M, st[g]);
     }
     float L = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int w = a; w <= bw; ++w) {
-      const float *st = stat_of(w);
-      const float l = st[16 + g];
-      if (l == 0.f) continue;
-      const float e = ex2(st[g] - M);
-      const bool head = w == bw && (grp.y & 256);
-      const float4 v = head ? __ldcg(reinterpret_cast<const float4 *>(fp.o_head + ((int64_t)cta * W + w) * G * kD) + o)
-                            : reinterpret_cast<const float4 *>(smem + (size_t)w * C::kRingBytes)[o];
-      L += e * l;
-      acc.x += e * v.x;
-      acc.y += e * v.y;
-      acc.z += e * v.z;
-      acc.w += e * v.w;
+      float *st = stat_of(grp, w);
+      const float l = st[16 + g], e = l == 0.f ? 0.f : ex2(st[g] - M);
+      st[g] = e;
+      if (l != 0.f) L += e * l;
     }
     const int b = grp.x / p.num_kv_heads, h = grp.x - b * p.num_kv_heads;
-    const float mul = L == 0.f ? 0.f : p.v_scale[h] / L;
+    sums[k * 32 + g] = L == 0.f ? 0.f : p.v_scale[h] / L;
+    const float lse = L == 0.f ? neg_inf() : (M + __log2f(L)) * 0.69314718055994531f;
+    if (grp.w > 0) p.lse_part[((int64_t)grp.x + cta) * G + g] = lse;
+    else if (p.lse) p.lse[(int64_t)b * p.num_q_heads + h * G + g] = lse;
+  }
+  __syncthreads();
+  uint32_t groups = 0;
+  for (int k = 0; k <= W; ++k) groups |= lead[k].x >= 0 ? 1u << k : 0u;
+  for (int item = threadIdx.x; item < __popc(groups) * nout; item += C::kThreads) {
+    uint32_t rest = groups;
+    for (int skip = item / nout; skip > 0; --skip) rest &= rest - 1;
+    const int k = __ffs(rest) - 1;
+    const int4 grp = lead[k];
+    const int o = item % nout, g = o / (kD / 4);
+    const int a = k == W ? 0 : k, bw = grp.y & 255;
+    const bool head = (grp.y & 256) != 0;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), last = acc;
+    if (head) last = __ldcg(reinterpret_cast<const float4 *>(fp.o_head + ((int64_t)cta * W + bw) * G * kD) + o);
+    auto add = [&](const float4 &v, float e) {
+      if (e != 0.f) {  // a piece of weight 0 may hold anything
+        acc.x += e * v.x;
+        acc.y += e * v.y;
+        acc.z += e * v.z;
+        acc.w += e * v.w;
+      }
+    };
+#pragma unroll 4
+    for (int w = a; w <= bw - (head ? 1 : 0); ++w)
+      add(reinterpret_cast<const float4 *>(smem + (size_t)w * C::kRingBytes)[o], stat_all[w * 64 + g]);
+    if (head) add(last, stat_all[bw * 64 + 32 + g]);
+    const float mul = sums[k * 32 + g];
     acc.x *= mul;
     acc.y *= mul;
     acc.z *= mul;
     acc.w *= mul;
-    const float lse = L == 0.f ? neg_inf() : (M + __log2f(L)) * 0.69314718055994531f;
     if (grp.w == 0) {
-      const int64_t row0 = (int64_t)b * p.num_q_heads + h * G;
-      *reinterpret_cast<uint2 *>(p.out + row0 * kD + 4 * o) =
+      const int b = grp.x / p.num_kv_heads, h = grp.x - b * p.num_kv_heads;
+      *reinterpret_cast<uint2 *>(p.out + ((int64_t)b * p.num_q_heads + h * G) * kD + 4 * o) =
           make_uint2(pack_bf16(acc.x, acc.y), pack_bf16(acc.z, acc.w));
-      if (o % (kD / 4) == 0 && p.lse) p.lse[row0 + g] = lse;
     } else {
-      const int64_t slot = (int64_t)grp.x + cta;
-      reinterpret_cast<float4 *>(p.o_part + slot * G * kD)[o] = acc;
-      if (o % (kD / 4) == 0) p.lse_part[slot * G + g] = lse;
+      reinterpret_cast<float4 *>(p.o_part + ((int64_t)grp.x + cta) * G * kD)[o] = acc;
     }
   }
   __syncthreads();
   // ---------------------------------------------------------------- units shared with other CTAs
-  if (threadIdx.x == 0)
-    for (int k = 0; k <= W; ++k) {
-      const int4 grp = lead[k];
-      if (grp.x >= 0 && grp.w > 0) count_piece(p, flags, grp.x, grp.z, grp.w, false);
+  // (at most two: the one that the range starts in and the one that it ends in),
+  // each counted by a thread of its own; the count that completes a unit, or a group
+  // of one merged in two levels, makes its merge this CTA's
+  if (threadIdx.x <= W && lead[threadIdx.x].x >= 0 && lead[threadIdx.x].w > 0) {
+    const int4 grp = lead[threadIdx.x];
+    const int unit = grp.x, cf = grp.z, ns = grp.w;
+    int q = -1, of = ns;
+    uint32_t *counter = p.counters + unit;
+    if (ns > kOneLevel) {
+      const int K = merge_group_size(ns);
+      q = (cta - cf) / K;
+      of = min(K, ns - q * K);
+      counter = p.counters + U + (int64_t)unit * max_merge_groups(gridDim.x) + q;
     }
+    if (atomic_add_acq_rel_gpu(counter, 1u) == (unsigned)(of - 1)) {
+      const int slot = cf < cta ? 24 : 28;  // the unit that the range starts in, or ends in
+      flags[slot + 1] = cf;
+      flags[slot + 2] = ns;
+      flags[slot + 3] = q;
+      flags[slot] = unit;
+    }
+  }
   __syncthreads();
-  const int npending = flags[12];
   float *scr = reinterpret_cast<float *>(smem);
   volatile int *last_group = flags + 13;
-  for (int k = 0; k < npending; ++k) {
-    const int unit = flags[24 + 4 * k], cf = flags[25 + 4 * k], ns = flags[26 + 4 * k];
-    const int q = flags[27 + 4 * k];
-    const int64_t slot0 = (int64_t)unit + cf;
+  for (int slot = 24; slot <= 28; slot += 4) {
+    const int unit = flags[slot], cf = flags[slot + 1], ns = flags[slot + 2], q = flags[slot + 3];
+    if (unit < 0) continue;
     if (q < 0) {
-      merge_slots_small(p, unit, G, slot0, 1, ns, true, 0, scr);  // at most kOneLevelSegs = kSmallMerge pieces
-      if (threadIdx.x == 0) p.counters[unit] = 0u;
-      __syncthreads();
+      f4_merge<C::kThreads>(p, unit, cf, ns, G, scr);
+      if (threadIdx.x == 0) p.counters[unit] = 0u;  // ready for the next call
       continue;
     }
+    const int64_t slot0 = (int64_t)unit + cf;
     const int K = merge_group_size(ns), ng = (ns + K - 1) / K, gs = min(K, ns - q * K);
-    if (gs <= kSmallMerge)
-      merge_slots_small(p, unit, G, slot0 + (int64_t)q * K, 1, gs, false, slot0 + (int64_t)q * K, scr);
-    else
-      merge_slots_cta(p, unit, G, slot0 + (int64_t)q * K, 1, gs, false, slot0 + (int64_t)q * K, scr);
+    merge_slots_cta(p, unit, G, slot0 + (int64_t)q * K, 1, gs, false, slot0 + (int64_t)q * K, scr);
     if (threadIdx.x == 0)
       *last_group = atomic_add_acq_rel_gpu(p.counters + unit, 1u) == (unsigned)(ng - 1) ? 1 : 0;
     __syncthreads();
     if (*last_group) {
-      if (ng <= kSmallMerge) merge_slots_small(p, unit, G, slot0, K, ng, true, 0, scr);
-      else merge_slots_cta(p, unit, G, slot0, K, ng, true, 0, scr);
-      uint32_t *gc = p.counters + p.batch * p.num_kv_heads + (int64_t)unit * max_merge_groups(gridDim.x);
+      merge_slots_cta(p, unit, G, slot0, K, ng, true, 0, scr);
+      uint32_t *gc = p.counters + U + (int64_t)unit * max_merge_groups(gridDim.x);
       for (int i = threadIdx.x; i < ng; i += C::kThreads) gc[i] = 0u;
       if (threadIdx.x == 0) p.counters[unit] = 0u;
     }
