@@ -220,7 +220,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   if (token_scale && (!a->k_scale_shift || !a->v_scale_shift || !aligned(a->k_scale_shift, 16) ||
                       !aligned(a->v_scale_shift, 16)))
     return DA_ERR_INVALID_ARG;
-  if (!aligned(a->k, 128) || !aligned(a->v, 128) || !aligned(a->q, 128) || !aligned(a->out, 8))
+  if (!aligned(a->k, 128) || !aligned(a->v, 128) || !aligned(a->q, 128) || !aligned(a->out, fp4 ? 16 : 8))
     return DA_ERR_INVALID_ARG;
 
   const uint64_t rows = paged ? (uint64_t)p.num_pages * p.num_kv_heads * p.page_size

@@ -61,13 +61,13 @@ struct F4 {
   static constexpr int oDesc = oCount + 128;                     // [warp][kQueue] F4Tile
   static constexpr int oStat = oDesc + kWarps * kQueue * 48;     // [warp][tail|head][m|l][16]
   static constexpr int oScan = oStat + kWarps * 64 * 4;
-  static constexpr int oFlags = oScan + 16 * 4;                  // 40 ints, as in gqa_split.cuh
-  static constexpr int oStart = oFlags + 40 * 4;                 // [warp] F4Start
-  static constexpr int oLead = oStart + kWarps * 32;             // [warp + 1] groups (see below)
+  static constexpr int oPre = oScan + 16 * 4;                    // [thread] tiles up to a thread's items
+  static constexpr int oFlags = oPre + kThreads * 4;             // 40 ints, as in gqa_split.cuh
+  static constexpr int oLead = oFlags + 40 * 4;                  // [warp + 1] groups (see below)
   static constexpr int oSum = oLead + (kWarps + 1) * 16;         // [warp + 1][16] 1 / L, [..][16] LSE
   static constexpr int kTotal = oSum + (kWarps + 1) * 32 * 4 + 128;
   static_assert(kRingBytes >= NT * 8 * kD * 4, "a warp's ring holds its piece after the stream");
-  static_assert(kRingBytes % 128 == 0 && oDesc % 16 == 0 && oStart % 16 == 0 && oLead % 16 == 0,
+  static_assert(kRingBytes % 128 == 0 && oDesc % 16 == 0 && oScan % 16 == 0 && oLead % 16 == 0,
                 "alignment");
   static_assert(kTotal <= 232448, "shared memory of a CTA");
 };
@@ -82,16 +82,22 @@ struct __align__(16) F4Tile {
   uint32_t valid;
   int32_t flags, nval, pos0;
   int64_t off0, off1;
-  int32_t unit, tiles;
-  int64_t P;
+  int32_t unit, tiles, P, pad;
 };
 constexpr int32_t kUnitStart = 8, kUnitEnd = 16;
-// Where a warp's range starts: its unit, that unit's first tile and its UnitInfo.
-struct __align__(16) F4Start {
-  int64_t P;
-  int32_t unit, n_valid, tiles, nbp, trow, pad;
+static_assert(sizeof(F4Tile) == 48, "layout");
+
+// n tiles cut into c consecutive ranges whose lengths differ by at most one (the
+// first n % c are the longer ones).
+struct Cut {
+  uint32_t base, rem;
+  __device__ __forceinline__ Cut(uint32_t n, uint32_t c) : base(n / c), rem(n % c) {}
+  __device__ __forceinline__ int start(uint32_t i) const { return (int)(i * base + min(i, rem)); }
+  __device__ __forceinline__ int owner(uint32_t t) const {
+    const uint32_t split = rem * (base + 1);
+    return (int)(t < split ? t / (base + 1) : rem + (t - split) / base);
+  }
 };
-static_assert(sizeof(F4Tile) == 48 && sizeof(F4Start) == 32, "layout");
 
 __device__ __forceinline__ UnitInfo f4_unit_info(const GqaParams &p, int u, uint32_t &err) {
   UnitInfo x = unit_info(p, u, err);
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   volatile int *flags = reinterpret_cast<volatile int *>(smem + C::oFlags);
   // flags: [0] a wait gave up; [13] scratch, [24..31] the merges owed (two: unit,
   // c_first, n_seg, group; unit -1: none)
-  F4Start *start = reinterpret_cast<F4Start *>(smem + C::oStart);
+  int *pre = reinterpret_cast<int *>(smem + C::oPre);
   // Groups: the pieces of one unit inside this CTA, warps a..b. Entry a, written
   // by warp a (entry W when the piece is warp 0's head alone): unit (-1: none); b,
   // with bit 8 when warp b goes on to another unit; c_first; n_seg (0: the whole
@@ -221,56 +227,59 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   }
   if (threadIdx.x <= W) lead[threadIdx.x] = make_int4(-1, 0, 0, 0);
 
-  // ---- the schedule (see gqa_split.cuh): this CTA's range, then this warp's
-  const int per = (U + C::kThreads - 1) / C::kThreads;
-  const int u_beg = min(U, (int)threadIdx.x * per), u_end = min(U, u_beg + per);
+  // ---- the schedule: the tiles of all units, end to end, one range per CTA. Thread t
+  // counts the items [t * per, t * per + per): rows (all heads of a dense row are alike)
+  // or, for listed blocks, units. The prefix sums stay in shared memory, where the
+  // walker finds the unit that each warp's range starts in.
+  const bool sparse = p.sparse_block_size > 0;
+  const int items = sparse ? U : p.batch, heads = sparse ? 1 : p.num_kv_heads;
+  const int per = (items + C::kThreads - 1) / C::kThreads;
+  auto item_tiles = [&](int it, uint32_t &err) -> int {  // of one unit of item `it`
+    return f4_unit_info(p, sparse ? it : it * heads, err).tiles;
+  };
   int local = 0;
-  for (int u = u_beg; u < u_end; ++u) local += f4_unit_info(p, u, dev_err).tiles;
-  int T32 = 0;
-  const int incl = block_inclusive_scan(local, scan, &T32);
-  const int64_t T = T32;
-  const int CTAS = (int)(T < (int64_t)gridDim.x ? T : (int64_t)gridDim.x);
-  const int64_t lo = cta < CTAS ? (int64_t)cta * T / CTAS : 0;
-  const int64_t hi = cta < CTAS ? (int64_t)(cta + 1) * T / CTAS : 0;
-  const int n_cta = (int)(hi - lo);
-  const int owner_of_tail = CTAS > 0 ? CTAS - 1 : 0;
-  {
-    int64_t Pu = incl - local;
-    uint32_t ignored = 0;
-    for (int u = u_beg; u < u_end; ++u) {
-      const UnitInfo x = f4_unit_info(p, u, ignored);
-      const int t_u = x.tiles;
-      if (t_u > 0 && Pu < hi && Pu + t_u > lo) {
-        // warps whose range starts in this unit
-        const int w0 = Pu <= lo ? 0 : cta_of(Pu - lo, n_cta, W);
-        for (int w = w0; w < W; ++w) {
-          const int64_t s = lo + (int64_t)w * n_cta / W;
-          if (s >= Pu + t_u) break;
-          if (s >= Pu) {
-            F4Start f;
-            f.P = Pu;
-            f.unit = u;
-            f.n_valid = x.n_valid;
-            f.tiles = x.tiles;
-            f.nbp = x.nbp;
-            f.trow = x.trow;
-            start[w] = f;
-          }
-        }
-      }
-      if (t_u == 0 && ((Pu >= lo && Pu < hi) || (Pu >= T && cta == owner_of_tail))) {
-        const int64_t row0 = (int64_t)x.b * p.num_q_heads + x.h * G;
-        for (int e = 0; e < G * kD; ++e) p.out[row0 * kD + e] = __float2bfloat16(0.f);
-        if (p.lse)
-          for (int g = 0; g < G; ++g) p.lse[row0 + g] = neg_inf();
-      }
-      Pu += t_u;
+  for (int k = 0; k < per; ++k) {
+    const int it = (int)threadIdx.x * per + k;
+    const int t = it < items ? item_tiles(it, dev_err) : 1;
+    if (it < items) local += t * heads;
+    // rows without a tile: zeros and -inf from the warp of the CTA that the item falls to
+    uint32_t none = __ballot_sync(0xffffffffu, t == 0 && it % (int)gridDim.x == cta);
+    for (; none != 0; none &= none - 1) {
+      const int e = __shfl_sync(0xffffffffu, it, __ffs(none) - 1);
+      const int rows = heads * G;
+      const int64_t row0 = sparse ? (int64_t)(e / p.num_kv_heads) * p.num_q_heads + e % p.num_kv_heads * G
+                                  : (int64_t)e * p.num_q_heads;
+      for (int i = lane; i < rows * (kD / 8); i += 32)
+        reinterpret_cast<uint4 *>(p.out + row0 * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (p.lse)
+        for (int i = lane; i < rows; i += 32) p.lse[row0 + i] = neg_inf();
     }
   }
-  if (n_cta <= 0) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, local, o);
+    if (lane >= o) local += v;
+  }
+  if (lane == 31) scan[warp] = local;
+  if (threadIdx.x < 16 && threadIdx.x > W) scan[threadIdx.x] = 0;  // (a vector of 16 sums is read)
+  __syncthreads();
+  int T = 0, before = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int4 v = reinterpret_cast<const int4 *>(scan)[k];
+    before += (4 * k < warp ? v.x : 0) + (4 * k + 1 < warp ? v.y : 0) + (4 * k + 2 < warp ? v.z : 0) +
+              (4 * k + 3 < warp ? v.w : 0);
+    T += v.x + v.y + v.z + v.w;
+  }
+  pre[threadIdx.x] = before + local;
+  const int CTAS = T < (int)gridDim.x ? T : (int)gridDim.x;  // never more ranges than tiles
+  if (cta >= CTAS) {
     if (dev_err) atomicOr(p.err, dev_err);
     return;
   }
+  const Cut cut((uint32_t)T, (uint32_t)CTAS);
+  const int lo = cut.start(cta), n_cta = cut.start(cta + 1) - lo, hi = lo + n_cta;
+  const Cut wcut((uint32_t)n_cta, W);
   uint64_t *stall_bar = reinterpret_cast<uint64_t *>(smem + C::oStall);  // nothing arrives on it
   uint32_t *ready_all = reinterpret_cast<uint32_t *>(smem + C::oCount);  // tiles described, per warp
   uint32_t *done_all = ready_all + 16;                                   // and tiles read
@@ -289,11 +298,10 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     // blocks, which tokens are valid, where the bytes are. One pass of the loop serves
     // every warp, so the walk costs a fraction of what it would in each of them.
     const int w = lane < W ? lane : 0;
-    const int64_t wlo = lo + (int64_t)w * n_cta / W, whi = lo + (int64_t)(w + 1) * n_cta / W;
-    const int ntiles = lane < W ? (int)(whi - wlo) : 0;
+    const int wlo = lo + wcut.start(w);
+    const int ntiles = lane < W ? lo + wcut.start(w + 1) - wlo : 0;
     F4Tile *queue = tiles_all + w * kQueue;
     const int P = p.page_size;
-    const bool sparse = p.sparse_block_size > 0;
     // entries (pages or listed blocks) of `tpe` tiles each; pages of 16 tokens: two per tile
     const int tpe = sparse ? p.sparse_block_size / kT : (p.paged ? (P >= kT ? P / kT : 1) : 1);
     const bool two_pages = p.paged && P < kT;
@@ -301,7 +309,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     const int gran_unit = p.paged ? P / kGran : p.cache_len / kGran;  // granules per (page | row, head)
     int u = 0, j = 0, ent = 0, sub = 0, nent = 0;  // unit, its tile, current entry, tile inside it, entries
     int id0 = -1, id1 = -1;                        // the current tile's ids
-    int64_t Pu = 0;
+    int Pu = 0;                                    // the unit's first tile
     UnitInfo x;
     x.b = x.h = x.n_valid = x.nbp = x.trow = 0;
     x.tiles = 1;
@@ -326,16 +334,31 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       prefetch_l2(p.q + ((int64_t)x.b * p.num_q_heads + x.h * G) * kD, (uint32_t)(G * kD * 2));
     };
     if (ntiles > 0) {
-      const F4Start f0 = start[w];
-      u = f0.unit;
-      Pu = f0.P;
-      j = (int)(wlo - Pu);
-      x.b = u / p.num_kv_heads;
-      x.h = u - x.b * p.num_kv_heads;
-      x.n_valid = f0.n_valid;
-      x.tiles = f0.tiles;
-      x.nbp = f0.nbp;
-      x.trow = f0.trow;
+      // the thread whose items hold tile wlo, then the item, then the head
+      int first = 0;
+      for (int n = C::kThreads; n > 0;) {  // the number of threads whose sum is at most wlo
+        const int half = n >> 1;
+        if (pre[first + half] <= wlo) {
+          first += half + 1;
+          n -= half + 1;
+        } else {
+          n = half;
+        }
+      }
+      Pu = first > 0 ? pre[first - 1] : 0;
+      uint32_t ignored = 0;
+      int it = first * per;
+      x = f4_unit_info(p, it * heads, ignored);
+      while (wlo >= Pu + x.tiles * heads) {
+        Pu += x.tiles * heads;
+        ++it;
+        x = f4_unit_info(p, it * heads, ignored);
+      }
+      const int h = sparse ? 0 : (wlo - Pu) / x.tiles;
+      u = it * heads + h;
+      x.h += h;
+      Pu += h * x.tiles;
+      j = wlo - Pu;
       enter_unit();
     }
     int i = 0;
@@ -405,10 +428,16 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           }
         } else if (i < ntiles) {
           Pu += x.tiles;
-          do {
-            ++u;
+          ++u;
+          if (!sparse && x.h + 1 < p.num_kv_heads) {
+            ++x.h;  // the next head of the row: the same lengths and pages
+          } else {
             x = f4_unit_info(p, u < U ? u : U - 1, dev_err);
-          } while (u < U && x.tiles == 0);
+            while (x.tiles == 0 && u + heads < U) {  // (rows without a tile were written above)
+              u += heads;
+              x = f4_unit_info(p, u, dev_err);
+            }
+          }
           j = 0;
           enter_unit();
         }
@@ -439,8 +468,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   } else {
     // ============================================================ consumers
     const int q4 = lane & 3, r8 = lane >> 2;
-    const int64_t wlo = lo + (int64_t)warp * n_cta / W, whi = lo + (int64_t)(warp + 1) * n_cta / W;
-    const int ntiles = (int)(whi - wlo);
+    const int ntiles = wcut.start(warp + 1) - wcut.start(warp);
     uint8_t *ring = smem + (size_t)warp * C::kRingBytes;
     const F4Tile *queue = tiles_all + warp * kQueue;
     if (ntiles == 0) stat_all[warp * 64 + lane] = 0.f;  // no piece: weight 0 in the sums below
@@ -505,14 +533,12 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     int unit = 0;
     // (the test stall of GqaParams, in the warp that always has a tile: the timeout path
     // runs as after a real failure)
-    if (p.test_stall_ns != 0 && warp == W - 1) ok = warp_wait(stall_bar, 0u, p.test_stall_ns);
+    if (p.test_stall_ns != 0 && warp == 0) ok = warp_wait(stall_bar, 0u, p.test_stall_ns);
     int st = -1;
     const int k_off = r8 * 64 + q4 * 16, ks_off = kScaleOff + r8 * 8 + q4 * 2;          // this lane in a K granule
     const int v_off = q4 * 128 + r8 * 8, vs_off = kScaleOff + q4 * 16 + r8;             // and in a V granule
     for (int i = 0; ok && i < ntiles; ++i) {
       st = st + 1 == S ? 0 : st + 1;
-      cp_async_wait_group<S - 1>();  // this lane's copies of tile i have landed,
-      __syncwarp();                  // and so have the other lanes'
       const F4Tile *tile = &queue[i % kQueue];
       uint32_t valid;
       int fl, nval = 0, pos0 = 0;
@@ -592,6 +618,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           l_part[nt][0] = l_part[nt][1] = 0.f;
         }
       }
+      cp_async_wait_group<S - 1>();  // this lane's copies of tile i have landed,
+      __syncwarp();                  // and so have the other lanes'
       if (valid != 0) {
         // ---------------- S^T = K Q^T, two granules of 16 tokens
         float s[NT][2][4];
@@ -772,8 +800,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           }
         }
       }
-      int64_t seg_P = 0;
-      int seg_tiles = 0;
+      int seg_P = 0, seg_tiles = 0;
       if (fl & kLast) {
         seg_P = tile->P;
         seg_tiles = tile->tiles;
@@ -796,14 +823,14 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
                      : fp.o_head + ((int64_t)cta * W + warp) * G * kD;
         // the unit's first warp here names the group (a head alone is warp 0's)
         if (lane == 0) {
-          const int64_t first = seg_P < lo ? lo : seg_P, end = seg_P + seg_tiles > hi ? hi : seg_P + seg_tiles;
-          if (cta_of(first - lo, n_cta, W) == warp) {
-            const int bw = cta_of(end - 1 - lo, n_cta, W);
-            const bool goes_on = end < lo + (int64_t)(bw + 1) * n_cta / W;
+          const int first = max(seg_P, lo), end = min(seg_P + seg_tiles, hi);
+          if (wcut.owner(first - lo) == warp) {
+            const int bw = wcut.owner(end - 1 - lo);
+            const bool goes_on = end < lo + wcut.start(bw + 1);
             int c_first = 0, n_seg = 0;
             if (seg_P < lo || seg_P + seg_tiles > hi) {
-              c_first = cta_of(seg_P, T, CTAS);
-              n_seg = cta_of(seg_P + seg_tiles - 1, T, CTAS) - c_first + 1;
+              c_first = cut.owner(seg_P);
+              n_seg = cut.owner(seg_P + seg_tiles - 1) - c_first + 1;
             }
             lead[tail ? warp : W] = make_int4(unit, bw | (goes_on ? 256 : 0), c_first, n_seg);
           }
@@ -881,36 +908,44 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   auto stat_of = [&](const int4 &grp, int w) {
     return stat_all + (w * 2 + (w == (grp.y & 255) && (grp.y & 256) ? 1 : 0)) * 32;
   };
-  for (int i = threadIdx.x; i < (W + 1) * 16; i += C::kThreads) {
-    const int k = i >> 4, g = i & 15;
-    const int4 grp = lead[k];
-    if (grp.x < 0 || g >= G) continue;
-    const int a = k == W ? 0 : k, bw = grp.y & 255;
-    float M = neg_inf();
-    for (int w = a; w <= bw; ++w) {
-      const float *st = stat_of(grp, w);
-      if (st[16 + g] != 0.f) M = fmaxf(M, st[g]);
-    }
-    float L = 0.f;
-    for (int w = a; w <= bw; ++w) {
-      float *st = stat_of(grp, w);
-      const float l = st[16 + g], e = l == 0.f ? 0.f : ex2(st[g] - M);
-      st[g] = e;
-      if (l != 0.f) L += e * l;
-    }
-    const int b = grp.x / p.num_kv_heads, h = grp.x - b * p.num_kv_heads;
-    sums[k * 32 + g] = L == 0.f ? 0.f : p.v_scale[h] / L;
-    const float lse = L == 0.f ? neg_inf() : (M + __log2f(L)) * 0.69314718055994531f;
-    if (grp.w > 0) p.lse_part[((int64_t)grp.x + cta) * G + g] = lse;
-    else if (p.lse) p.lse[(int64_t)b * p.num_q_heads + h * G + g] = lse;
-  }
-  __syncthreads();
   uint32_t groups = 0;
   for (int k = 0; k <= W; ++k) groups |= lead[k].x >= 0 ? 1u << k : 0u;
-  for (int item = threadIdx.x; item < __popc(groups) * nout; item += C::kThreads) {
+  const int ngroups = __popc(groups);
+  auto group_at = [&](int i) {  // the i-th group
     uint32_t rest = groups;
-    for (int skip = item / nout; skip > 0; --skip) rest &= rest - 1;
-    const int k = __ffs(rest) - 1;
+    for (; i > 0; --i) rest &= rest - 1;
+    return __ffs(rest) - 1;
+  };
+  // sixteen lanes a (group, row), one piece each
+  for (int t0 = warp * 2; t0 < ngroups * G; t0 += C::kThreads / 16) {
+    const int task = t0 + (lane >> 4), sub = lane & 15;
+    const bool on = task < ngroups * G;
+    const int gi = on ? task / G : 0, g = on ? task - gi * G : 0;
+    const int k = group_at(gi);
+    const int4 grp = lead[k];
+    const int w = (k == W ? 0 : k) + sub;
+    float *st = stat_of(grp, min(w, W - 1));
+    const float l = on && w <= (grp.y & 255) ? st[16 + g] : 0.f;
+    const float m = l != 0.f ? st[g] : neg_inf();
+    float M = m;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    const float e = l == 0.f ? 0.f : ex2(m - M);
+    float L = l == 0.f ? 0.f : e * l;
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+    if (on && w <= (grp.y & 255)) st[g] = e;
+    if (on && sub == 0) {
+      const int b = grp.x / p.num_kv_heads, h = grp.x - b * p.num_kv_heads;
+      sums[k * 32 + g] = L == 0.f ? 0.f : p.v_scale[h] / L;
+      const float lse = L == 0.f ? neg_inf() : (M + __log2f(L)) * 0.69314718055994531f;
+      if (grp.w > 0) p.lse_part[((int64_t)grp.x + cta) * G + g] = lse;
+      else if (p.lse) p.lse[(int64_t)b * p.num_q_heads + h * G + g] = lse;
+    }
+  }
+  __syncthreads();
+  for (int item = threadIdx.x; item < ngroups * nout; item += C::kThreads) {
+    const int k = group_at(item / nout);
     const int4 grp = lead[k];
     const int o = item % nout, g = o / (kD / 4);
     const int a = k == W ? 0 : k, bw = grp.y & 255;
