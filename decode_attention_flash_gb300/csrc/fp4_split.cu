@@ -553,8 +553,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         nval = (int)m.z;
         pos0 = (int)m.w;
       }
-      const uint8_t *stage = ring + st * kStageBytes;
-      if (fl & kFirst) {
+      uint8_t *stage = ring + st * kStageBytes;
+      if (__builtin_expect(fl & kFirst, 0)) {
         from_start = (fl & kUnitStart) != 0;
         fresh = true;
         unit = tile->unit;
@@ -620,14 +620,15 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       }
       cp_async_wait_group<S - 1>();  // this lane's copies of tile i have landed,
       __syncwarp();                  // and so have the other lanes'
-      if (valid != 0) {
-        // ---------------- S^T = K Q^T, two granules of 16 tokens
+      if (__builtin_expect(valid != 0, 1)) {
+        // ---------------- S^T = K Q^T, two granules of 16 tokens (both always: a branch
+        // between them would keep their instructions apart; what a half that was not
+        // copied holds is masked below)
         float s[NT][2][4];
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[nt][gi][0] = s[nt][gi][1] = s[nt][gi][2] = s[nt][gi][3] = 0.f;
-          if (((valid >> (16 * gi)) & 0xFFFFu) == 0) continue;
           const uint8_t *gk = stage + gi * kGranBytes;
           const uint4 ra = *reinterpret_cast<const uint4 *>(gk + k_off);
           const uint4 rb = *reinterpret_cast<const uint4 *>(gk + k_off + 512);
@@ -681,14 +682,22 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
                 }
                 s[nt][k >> 1][(k & 1) * 2 + e] = keep ? v : neg_inf();
               }
-        } else if (part) {  // (dense rows of one query token; a page that was not there)
-          // a masked score takes the value whose weight is 0 whatever the scale's sign
-          const float none = sscale < 0.f ? -neg_inf() : neg_inf();
+        }
+        if (__builtin_expect(part, 0)) {  // the row's end, or a page that was not there
+          if (MOD == 0 || !masks) {
+            // a masked score takes the value whose weight is 0 whatever the scale's sign
+            const float none = sscale < 0.f ? -neg_inf() : neg_inf();
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (!((valid >> (r8 + 8 * k)) & 1u)) s[nt][k >> 1][(k & 1) * 2] = s[nt][k >> 1][(k & 1) * 2 + 1] = none;
+              for (int k = 0; k < 4; ++k)
+                if (!((valid >> (r8 + 8 * k)) & 1u)) s[nt][k >> 1][(k & 1) * 2] = s[nt][k >> 1][(k & 1) * 2 + 1] = none;
+          }
+          // a masked token's value row may hold any scale (NaN; its codes are finite): zero them
+          if (!((valid >> lane) & 1u))
+            *reinterpret_cast<uint2 *>(stage + (2 + (lane >> 4)) * kGranBytes + kScaleOff + (lane & 15) * 8) =
+                make_uint2(0u, 0u);
+          __syncwarp();
         }
         // The weights 2^(x - m) against the held reference m, and their sums. The
         // reference is raised only when a sum passes 2^10 (so no weight does, and
@@ -714,7 +723,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         if (MOD >= 1)  // (a row may have had no kept token so far)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) raise = raise || no_ref[nt][0] || no_ref[nt][1];
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
           fresh = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -761,8 +770,6 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         // ---------------- O^T += V^T P^T
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
-          const uint32_t vb = (valid >> (16 * gi)) & 0xFFFFu;
-          if (vb == 0) continue;
           const uint8_t *gv = stage + (2 + gi) * kGranBytes;
           // tokens 2 q4, 2 q4 + 1 and the same + 8: one block (8 bytes) of each, and its scale
           uint2 w[4];
@@ -773,12 +780,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
             w[k] = *reinterpret_cast<const uint2 *>(gv + v_off + t * 64);
             sc[k] = gv[vs_off + t * 8];
           }
-          uint32_t s01 = e4m3x2_to_f16x2((uint16_t)prmt(sc[0], sc[1], 0x0040));
-          uint32_t s89 = e4m3x2_to_f16x2((uint16_t)prmt(sc[2], sc[3], 0x0040));
-          if (vb != 0xFFFFu) {  // a masked token's row may hold any scale (codes are finite)
-            s01 &= lo16_mask((vb >> (2 * q4)) & 1u, (vb >> (2 * q4 + 1)) & 1u);
-            s89 &= lo16_mask((vb >> (2 * q4 + 8)) & 1u, (vb >> (2 * q4 + 9)) & 1u);
-          }
+          const uint32_t s01 = e4m3x2_to_f16x2((uint16_t)prmt(sc[0], sc[1], 0x0040));
+          const uint32_t s89 = e4m3x2_to_f16x2((uint16_t)prmt(sc[2], sc[3], 0x0040));
           constexpr uint32_t kLow = 0x0F0F0F0Fu;
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
@@ -809,7 +812,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       if (lane == 0) st_release_cta(&done_all[warp], (uint32_t)(i + 1));
       if (i + S < ntiles) ok = issue(i + S, st);
       cp_async_commit();  // (a group a tile, empty ones at the end)
-      if (!(fl & kLast)) continue;
+      if (__builtin_expect(!(fl & kLast), 1)) continue;
       // ---------------- the segment ends. Row sums, then: a unit held by this
       // segment alone goes out from the registers; another segment's (m, l, O) to
       // this warp's ring when it is the warp's last, else to its global slot
