@@ -265,9 +265,7 @@ def make_args(tensors: dict, scale: float, out, lse=None, softcap: float = 0.0) 
 
 
 def decode_attn_run(ctx, args: Args, workspace: torch.Tensor, stream=None):
-    _check(load().decode_attn_run(ctx, ctypes.byref(args), _ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)),
-           "decode_attn_run")
+    _enqueue(load().decode_attn_run, "decode_attn_run", ctx, args, workspace, stream)
 
 
 def decode_attn_run_noalloc(ctx, args: Args, stream=None):
@@ -381,24 +379,33 @@ def make_gather_args(tensors: dict) -> GatherArgs:
     return a
 
 
-def _workspace_call(name: str, ctx, args, workspace, stream):
-    _check(getattr(load(), name)(ctx, ctypes.byref(args), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream)), name)
+def _enqueue(fn, name: str, ctx, args, workspace, stream):
+    """One call of an entry point that enqueues on a stream. Decode steps make a few of these a
+    token, so the arguments go over as plain integers (no ctypes objects are made here)."""
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        _ptr(workspace)  # raises
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(workspace.get_device())
+    else:
+        stream = _stream(stream)
+    status = fn(ctx, args, workspace.data_ptr(), workspace.nbytes, stream)
+    if status != DA_OK:
+        raise DecodeAttnError(status, name)
 
 
 def decode_attn_build_tables(ctx, args: TableArgs, workspace: torch.Tensor, stream=None):
     """Block table, slots and lengths of the tokens that the rows get now (one kernel)."""
-    _workspace_call("decode_attn_build_tables", ctx, args, workspace, stream)
+    _enqueue(load().decode_attn_build_tables, "decode_attn_build_tables", ctx, args, workspace, stream)
 
 
 def decode_attn_append(ctx, args: AppendArgs, workspace: torch.Tensor, stream=None):
     """Rotates queries and new keys, and writes keys and values into the cache (one kernel)."""
-    _workspace_call("decode_attn_append", ctx, args, workspace, stream)
+    _enqueue(load().decode_attn_append, "decode_attn_append", ctx, args, workspace, stream)
 
 
 def decode_attn_gather(ctx, args: GatherArgs, workspace: torch.Tensor, stream=None):
     """Reads cache rows back as bf16 (one kernel)."""
-    _workspace_call("decode_attn_gather", ctx, args, workspace, stream)
+    _enqueue(load().decode_attn_gather, "decode_attn_gather", ctx, args, workspace, stream)
 
 
 def decode_attn_get_error(ctx, workspace: torch.Tensor, stream=None) -> int:

@@ -444,10 +444,10 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
 
 int64_t blocks_for(int64_t items) { return (items + kWarps - 1) / kWarps; }
 
-// Parts a token's heads are cut into: as many warps as two for each scheduler of
-// every SM, when there are fewer tokens than that.
+// Parts a token's heads are cut into: about 48 warps for every SM, when there are
+// fewer tokens than that.
 int parts_for(int64_t tokens, int groups, int num_sms) {
-  const int64_t want = (int64_t)num_sms * 8;
+  const int64_t want = (int64_t)num_sms * 48;
   const int64_t parts = (want + tokens - 1) / tokens;
   return (int)(parts < 1 ? 1 : parts > groups ? groups : parts);
 }

@@ -99,6 +99,24 @@ struct Cut {
   }
 };
 
+// A CTA's n tiles cut into one range per consumer warp. The walker's scheduler has a
+// consumer less, so its warps (w % 4 == 3) run a little faster: they get kFast shares
+// where the others get kShare (equal shares left them 10 % ahead of the others).
+template <int W>
+struct WarpCut {
+  static constexpr uint32_t kShare = 10, kFast = W == 15 ? 11 : 12;
+  static constexpr uint32_t kAll = kShare * W + (kFast - kShare) * ((W + 1) / 4 - 1 + ((W + 1) % 4 == 0 ? 0 : 1));
+  int n;
+  __device__ __forceinline__ int start(int w) const {
+    return (int)((uint64_t)(uint32_t)n * (kShare * w + (kFast - kShare) * (w / 4)) / kAll);
+  }
+  __device__ __forceinline__ int owner(int t) const {
+    int w = 0;
+    while (w + 1 < W && start(w + 1) <= t) ++w;
+    return w;
+  }
+};
+
 __device__ __forceinline__ UnitInfo f4_unit_info(const GqaParams &p, int u, uint32_t &err) {
   UnitInfo x = unit_info(p, u, err);
   x.tiles = p.sparse_block_size > 0 ? x.tiles * (kTile / kT) : (x.n_valid + kT - 1) / kT;
@@ -127,23 +145,24 @@ __device__ __forceinline__ uint32_t f4_scale(uint32_t x, uint32_t s, int high) {
   return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// All threads merge the n <= 32 pieces of `unit` that CTAs c_first .. c_first + n - 1
-// left (slots unit + cta) into the final output: warp g takes row g's LSEs, one
+// `threads` threads (a whole number of warps, this one the `tid`-th, meeting at named
+// barrier `bar`) merge the n <= 32 pieces of `unit` that CTAs c_first .. c_first + n - 1
+// left (slots unit + cta) into the final output: a warp takes a row's LSEs, one
 // piece a lane, for the weights; the threads' loads of the pieces' O, kLoads at a
 // time, are in flight meanwhile. `scr`: shared memory, free.
-template <int THREADS>
-__device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first, int n, int G, float *scr) {
+__device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first, int n, int G, float *scr,
+                                      int tid, int threads, int bar) {
   constexpr int kLoads = 8;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = tid & 31, warp = tid >> 5;
   const int nout = G * (kD / 4);
   const int64_t slot0 = (int64_t)unit + c_first;
   float *w = scr;                                          // [G][32] weights over their sum
   float4 *acc = reinterpret_cast<float4 *>(scr + G * 32);  // [parts][nout]
-  const int parts = max(1, min(THREADS / nout, n));        // threads that share an output
+  const int parts = max(1, min(threads / nout, n));        // threads that share an output
   const float4 *src = reinterpret_cast<const float4 *>(p.o_part + slot0 * G * kD);
   const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
   const int64_t row0 = (int64_t)b * p.num_q_heads + h * G;
-  for (int g = warp; g < G; g += THREADS / 32) {
+  for (int g = warp; g < G; g += threads / 32) {
     const float l = lane < n ? __ldcg(p.lse_part + (slot0 + lane) * G + g) : neg_inf();
     float M = l;
 #pragma unroll
@@ -155,7 +174,9 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
     w[g * 32 + lane] = sum == 0.f ? 0.f : e / sum;
     if (lane == 0 && p.lse) p.lse[row0 + g] = sum == 0.f ? neg_inf() : M + __log2f(sum) * 0.69314718055994531f;
   }
-  for (int item = tid; item < nout * parts; item += THREADS) {
+  // (items are warp-uniform in number: nout * parts is a multiple of 32)
+  bool met = false;
+  for (int item = tid; item < nout * parts; item += threads) {
     const int o = item % nout, s0 = item / nout, g = o / (kD / 4);
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int s = s0; s < n; s += parts * kLoads) {
@@ -163,7 +184,8 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
         v[k] = s + k * parts < n ? __ldcg(src + (int64_t)(s + k * parts) * nout + o) : make_float4(0.f, 0.f, 0.f, 0.f);
-      if (item == tid && s == s0) __syncthreads();  // (every thread comes here once) the weights are in w
+      if (!met) named_barrier_sync(bar, threads);  // the weights are in w
+      met = true;
 #pragma unroll
       for (int k = 0; k < kLoads; ++k) {
         const float e = s + k * parts < n ? w[g * 32 + s + k * parts] : 0.f;
@@ -177,9 +199,9 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
     }
     acc[item] = a;
   }
-  if (tid >= nout * parts) __syncthreads();  // (threads without an item: the barrier above)
-  __syncthreads();
-  for (int o = tid; o < nout; o += THREADS) {
+  if (!met) named_barrier_sync(bar, threads);  // (a warp without an item)
+  named_barrier_sync(bar, threads);
+  for (int o = tid; o < nout; o += threads) {
     float4 a = acc[o];
     for (int k = 1; k < parts; ++k) {
       const float4 v = acc[k * nout + o];
@@ -190,7 +212,7 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
     }
     *reinterpret_cast<uint2 *>(p.out + row0 * kD + 4 * o) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
   }
-  __syncthreads();
+  if (tid == 0) p.counters[unit] = 0u;  // ready for the next call
 }
 constexpr int kOneLevel = 32;  // pieces that f4_merge takes; a unit of more is merged in two levels
 
@@ -279,7 +301,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   }
   const Cut cut((uint32_t)T, (uint32_t)CTAS);
   const int lo = cut.start(cta), n_cta = cut.start(cta + 1) - lo, hi = lo + n_cta;
-  const Cut wcut((uint32_t)n_cta, W);
+  const WarpCut<W> wcut{n_cta};
   uint64_t *stall_bar = reinterpret_cast<uint64_t *>(smem + C::oStall);  // nothing arrives on it
   uint32_t *ready_all = reinterpret_cast<uint32_t *>(smem + C::oCount);  // tiles described, per warp
   uint32_t *done_all = ready_all + 16;                                   // and tiles read
@@ -507,10 +529,10 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       }
       return true;
     };
-    for (int i = 0; i < S; ++i) {
-      if (ok && i < ntiles) ok = issue(i, i);
-      cp_async_commit();
-    }
+    // The first tile alone, so that no warp's first tile queues behind the others' second
+    // and third; those follow when the first has landed.
+    if (ntiles > 0) ok = issue(0, 0);
+    cp_async_commit();
     // ------------------------------------------------------------ the stream
     uint32_t qf[NT][8][2];
     float oacc[NT][8][4];
@@ -533,7 +555,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     int unit = 0;
     // (the test stall of GqaParams, in the warp that always has a tile: the timeout path
     // runs as after a real failure)
-    if (p.test_stall_ns != 0 && warp == 0) ok = warp_wait(stall_bar, 0u, p.test_stall_ns);
+    if (p.test_stall_ns != 0 && warp == W - 1) ok = warp_wait(stall_bar, 0u, p.test_stall_ns);
     int st = -1;
     const int k_off = r8 * 64 + q4 * 16, ks_off = kScaleOff + r8 * 8 + q4 * 2;          // this lane in a K granule
     const int v_off = q4 * 128 + r8 * 8, vs_off = kScaleOff + q4 * 16 + r8;             // and in a V granule
@@ -616,6 +638,14 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           m_neg[nt][0] = m_neg[nt][1] = 0.f;
           no_ref[nt][0] = no_ref[nt][1] = true;
           l_part[nt][0] = l_part[nt][1] = 0.f;
+        }
+      }
+      if (__builtin_expect(i == 0, 0)) {
+        cp_async_wait_group<0>();
+#pragma unroll
+        for (int k = 1; k < S; ++k) {
+          if (ok && k < ntiles) ok = issue(k, k);
+          cp_async_commit();
         }
       }
       cp_async_wait_group<S - 1>();  // this lane's copies of tile i have landed,
@@ -1007,14 +1037,19 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   __syncthreads();
   float *scr = reinterpret_cast<float *>(smem);
   volatile int *last_group = flags + 13;
+  // one-level merges: the whole block for one, a half each for two
+  const bool one0 = flags[24] >= 0 && flags[27] < 0, one1 = flags[28] >= 0 && flags[31] < 0;
+  if (one0 || one1) {
+    constexpr int kHalf = (W + 1) / 2 * 32;
+    const bool both = one0 && one1;
+    const int mine = both ? (int)threadIdx.x / kHalf : 0, slot = (both ? mine : one0 ? 0 : 1) ? 28 : 24;
+    f4_merge(p, flags[slot], flags[slot + 1], flags[slot + 2], G, scr + mine * 4096, (int)threadIdx.x - mine * kHalf,
+             both ? kHalf : C::kThreads, 1 + mine);
+    __syncthreads();
+  }
   for (int slot = 24; slot <= 28; slot += 4) {
     const int unit = flags[slot], cf = flags[slot + 1], ns = flags[slot + 2], q = flags[slot + 3];
-    if (unit < 0) continue;
-    if (q < 0) {
-      f4_merge<C::kThreads>(p, unit, cf, ns, G, scr);
-      if (threadIdx.x == 0) p.counters[unit] = 0u;  // ready for the next call
-      continue;
-    }
+    if (unit < 0 || q < 0) continue;
     const int64_t slot0 = (int64_t)unit + cf;
     const int K = merge_group_size(ns), ng = (ns + K - 1) / K, gs = min(K, ns - q * K);
     merge_slots_cta(p, unit, G, slot0 + (int64_t)q * K, 1, gs, false, slot0 + (int64_t)q * K, scr);

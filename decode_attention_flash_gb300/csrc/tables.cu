@@ -223,9 +223,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
 }  // namespace
 
 cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream) {
-  // one block up to 2048 tokens (a decode step), then 4 tokens a thread, at most
-  // one block for each SM
-  int64_t blocks = (p.slot_capacity + 4 * kThreads - 1) / (4 * kThreads);
+  // a token a thread, at most one block for each SM
+  int64_t blocks = (p.slot_capacity + kThreads - 1) / kThreads;
   if (blocks < 1) blocks = 1;
   if (blocks > num_sms) blocks = num_sms;
   tables_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
