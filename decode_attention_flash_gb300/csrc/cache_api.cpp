@@ -152,7 +152,7 @@ da_status decode_attn_append(da_ctx *ctx, const da_append_args *a, void *workspa
     if (!a->positions || !a->cos_sin || !aligned(a->cos_sin, 16) || a->max_position <= 0) return DA_ERR_INVALID_ARG;
     if (a->rope_axes < 1 || a->rope_axes > 255) return DA_ERR_INVALID_ARG;
     if (a->rope_axes > 1 && a->position_stride < a->num_tokens) return DA_ERR_INVALID_ARG;
-    const int group = a->rope_adjacent ? 4 : 8;  // pairs of a lane
+    const int group = 8;  // pairs of a lane
     c.rope_whole = 1;
     for (int i = 0; i < c.rope_pairs; ++i) {
       const int ax = a->pair_axis ? a->pair_axis[i] : 0;

@@ -8,13 +8,17 @@
 // fp32, the result to bf16. Keys and values then take the cache's element kind
 // (the rules stand at put_row); a quantised cache holds the quantised bf16 key.
 //
-// What bounds it. Every byte is read and written once, so HBM does for a
-// prefill and latency for a decode step. A warp owns a token (or, when there are
-// fewer tokens than the SMs take warps, a part of its heads): it loads the
-// token's cosines and sines once into registers and walks the heads, 16 lanes of
-// 8 elements a head (8 lanes for the 64-element rope heads of the latent cache),
-// kAhead loads in flight. A half-split pair sits in two lanes of the head and is
-// exchanged by shuffles; block maxima are shuffles of 2, 4 or 16 lanes.
+// What bounds it. Every byte is read and written once, so HBM does for a prefill
+// and latency for a decode step; the arithmetic has to stay out of the way (a first
+// form with every head as 16 lanes of 8 elements, partners exchanged by shuffles, was
+// bound by instruction issue). A warp owns a token, or a part of its heads when there
+// are fewer tokens than the SMs take warps. Queries: a lane takes both halves of
+// eight pairs (two 16-byte loads), so a head is 8 lanes (4 for the 64-element rope
+// heads of the latent cache), nothing is exchanged, and the cosines and sines of its
+// pairs stay in registers for all heads of the token. Keys and values: 16 lanes of 8
+// elements a head, as the element kinds want them (block maxima are shuffles of 2, 4
+// or 16 lanes), a key's halves exchanged by shuffles. Addresses advance by a head's
+// stride; kAhead loads are in flight.
 #include <cuda_fp16.h>
 
 #include "internal.h"
@@ -56,14 +60,53 @@ __device__ __forceinline__ float f16_value(uint32_t b) {
   return __half2float(__ushort_as_half((unsigned short)b));
 }
 
-// The cache row (in rows of one head) of slot `s`, kv head h: slots count the
-// positions of all pages (or of all batch rows of a contiguous cache).
-__device__ __forceinline__ int64_t cache_row(const CacheRowParams &p, int64_t page, int off, int h) {
-  return (page * p.num_kv_heads + h) * p.rows_per_page + off;
+// Where the rows of one slot are: lane l of 16 of kv head 0 in K and in V, the next
+// head `head` bytes on; the scale words (or, 4-bit float, the block scales) likewise.
+struct RowAt {
+  uint8_t *k, *v, *ks, *vs;
+  int64_t head, shead;
+};
+template <int KIND>
+__device__ __forceinline__ RowAt row_at(const CacheRowParams &p, int64_t slot, int l) {
+  const uint32_t P = (uint32_t)p.rows_per_page;
+  const int64_t page = (slot >> 32) == 0 ? (int64_t)((uint32_t)slot / P) : slot / P;
+  const int off = (int)(slot - page * P);
+  RowAt a;
+  a.ks = a.vs = nullptr;
+  a.shead = 0;
+  int64_t at;
+  if (KIND == kFp4) {
+    const int64_t gran = P / 16;
+    const int64_t g0 = (page * p.num_kv_heads * gran + off / 16) * 1152;
+    at = g0 + off % 16 * 64 + l * 4;
+    a.head = a.shead = gran * 1152;
+    const int64_t sc = g0 + 1024 + off % 16 * 8 + (l >> 1);
+    a.ks = reinterpret_cast<uint8_t *>(p.k) + sc;
+    a.vs = reinterpret_cast<uint8_t *>(p.v) + sc;
+  } else {
+    const int64_t row0 = page * p.num_kv_heads * P + off;
+    const int row_bytes = KIND == kBf16 ? 256 : KIND == kInt4 ? 4 * (p.kv_groups + 16) : 128;
+    at = row0 * row_bytes + (KIND == kBf16 ? l * 16 : KIND == kInt4 ? (p.kv_groups + l) * 4 : l * 8);
+    a.head = (int64_t)P * row_bytes;
+    if (KIND == kInt4) {  // the coefficient word of the lane's group
+      const int64_t sc = row0 * row_bytes + l * p.kv_groups / 16 * 4;
+      a.ks = reinterpret_cast<uint8_t *>(p.k) + sc;
+      a.vs = reinterpret_cast<uint8_t *>(p.v) + sc;
+      a.shead = a.head;
+    }
+    if (KIND == kE4m3Token) {
+      a.ks = reinterpret_cast<uint8_t *>(p.k_scale_shift + row0);
+      a.vs = reinterpret_cast<uint8_t *>(p.v_scale_shift + row0);
+      a.shead = (int64_t)P * 4;
+    }
+  }
+  a.k = reinterpret_cast<uint8_t *>(p.k) + at;
+  a.v = reinterpret_cast<uint8_t *>(p.v) + at;
+  return a;
 }
 
-// One row of 128 elements, 8 per lane (lane l of 16: elements 8l .. 8l + 7, bf16
-// values in fp32), into row `row` of the cache in its element kind:
+// One row of 128 elements, 8 per lane (lane l of 16: elements 8l .. 8l + 7, as bf16
+// pairs in `raw`), to `dst` (and its scale to `sdst`) in the cache's element kind:
 //   e4m3        code = e4m3(x / scale[h]), to nearest even, saturating
 //   e4m3, token shift = f16((max + min) / 2), scale = f16((max - min) / 2 / 448) (1
 //               when that is 0), code = e4m3((x - shift) / scale)
@@ -73,20 +116,20 @@ __device__ __forceinline__ int64_t cache_row(const CacheRowParams &p, int64_t pa
 //               e2m1(x * (1 / (block scale * scale[h]))), zeros when that product is 0
 // Every lane of the warp calls it (shuffles); lanes with !on store nothing.
 template <int KIND>
-__device__ __forceinline__ void put_row(const CacheRowParams &p, bool is_v, bool on, int64_t row, int h,
-                                        int l, const float (&x)[8], const uint4 &raw) {
-  void *cache = is_v ? p.v : p.k;
+__device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_t *dst, uint8_t *sdst, float head_scale,
+                                        int l, const uint4 &raw) {
   if (KIND == kBf16) {
-    if (on) *(reinterpret_cast<uint4 *>(cache) + row * 16 + l) = raw;
+    if (on) *reinterpret_cast<uint4 *>(dst) = raw;
     return;
   }
+  const float x[8] = {bf_lo(raw.x), bf_hi(raw.x), bf_lo(raw.y), bf_hi(raw.y),
+                      bf_lo(raw.z), bf_hi(raw.z), bf_lo(raw.w), bf_hi(raw.w)};
   if (KIND == kE4m3) {
-    const float s = on ? __ldg((is_v ? p.v_scale : p.k_scale) + h) : 1.f;
+    const float s = head_scale;
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
-    if (on)
-      *(reinterpret_cast<uint2 *>(cache) + row * 16 + l) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    if (on) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     return;
   }
   if (KIND == kFp4) {
@@ -94,7 +137,7 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool is_v, bool
 #pragma unroll
     for (int i = 1; i < 8; ++i) a = max_nan(a, fabsf(x[i]));
     a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
-    const float g = on ? __ldg((is_v ? p.v_scale : p.k_scale) + h) : 1.f;
+    const float g = head_scale;
     const uint32_t sb = f32x2_to_e4m3x2(__fdiv_rn(a, __fmul_rn(6.f, g)), 0.f) & 0xFFu;
     const uint32_t half2 = e4m3x2_to_f16x2((uint16_t)sb);
     const float eff = __fmul_rn(f16_value(half2 & 0xFFFFu), g);
@@ -103,10 +146,8 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool is_v, bool
 #pragma unroll
     for (int i = 0; i < 4; ++i) w |= e2m1x2(__fmul_rn(x[2 * i], inv), __fmul_rn(x[2 * i + 1], inv)) << (8 * i);
     if (on) {
-      uint8_t *gran = reinterpret_cast<uint8_t *>(cache) + (row >> 4) * 1152;
-      const int r = (int)(row & 15);
-      *reinterpret_cast<uint32_t *>(gran + r * 64 + l * 4) = w;
-      if ((l & 1) == 0) gran[1024 + r * 8 + (l >> 1)] = (uint8_t)sb;
+      *reinterpret_cast<uint32_t *>(dst) = w;
+      if ((l & 1) == 0) *sdst = (uint8_t)sb;
     }
     return;
   }
@@ -134,8 +175,8 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool is_v, bool
     for (int i = 0; i < 4; ++i)
       w[i] = f32x2_to_e4m3x2(__fdiv_rn(__fsub_rn(x[2 * i], sh), sc), __fdiv_rn(__fsub_rn(x[2 * i + 1], sh), sc));
     if (on) {
-      *(reinterpret_cast<uint2 *>(cache) + row * 16 + l) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
-      if (l == 0) (is_v ? p.v_scale_shift : p.k_scale_shift)[row] = word;
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+      if (l == 0) *reinterpret_cast<int32_t *>(sdst) = word;
     }
   } else {
     uint32_t w = 0;
@@ -145,9 +186,8 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool is_v, bool
       w |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
     }
     if (on) {
-      int32_t *dst = reinterpret_cast<int32_t *>(cache) + row * (p.kv_groups + 16);
-      dst[p.kv_groups + l] = (int32_t)w;
-      if (l % lanes == 0) dst[l / lanes] = word;
+      *reinterpret_cast<uint32_t *>(dst) = w;
+      if (l % lanes == 0) *reinterpret_cast<int32_t *>(sdst) = word;
     }
   }
 }
@@ -163,192 +203,247 @@ __device__ __forceinline__ int64_t load_slot(const CacheRowParams &p, int64_t t,
   return s;
 }
 
-// LPH lanes of 8 elements a rotated head: 16 (heads of 128) or 8 (the latent cache's 64).
-template <int KIND, int LPH>
-__global__ void __launch_bounds__(kWarps * 32) append_kernel(const __grid_constant__ CacheRowParams p) {
-  constexpr int kPer = 32 / LPH;  // heads a warp takes at once
-  constexpr int kHead = LPH * 8;
+// The cosines and sines of pairs pair0 .. pair0 + 7 (or + 3: kPairs) of token t;
+// false when a position is outside the table.
+template <int kPairs>
+__device__ __forceinline__ bool load_turn(const CacheRowParams &p, int64_t t, int pair0, float (&c)[8], float (&s)[8]) {
+  const int n = p.rope_pairs;
+  if (p.rope_whole) {  // they share an axis: vector loads
+    const int pos = __ldg(p.positions + (int64_t)p.pair_axis[pair0] * p.position_stride + t);
+    if (pos < 0 || pos >= p.max_position) return false;
+    const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + pair0);
+    const float4 *row2 = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + n + pair0);
+#pragma unroll
+    for (int j = 0; j < kPairs / 4; ++j) {
+      const float4 a = __ldg(row + j), b = __ldg(row2 + j);
+      c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
+      s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
+    }
+    return true;
+  }
+  bool ok = true;
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    const int pos = __ldg(p.positions + (int64_t)p.pair_axis[pair0 + i] * p.position_stride + t);
+    const bool in = pos >= 0 && pos < p.max_position;
+    ok = ok && in;
+    c[i] = in ? __ldg(p.cos_sin + (int64_t)pos * 2 * n + pair0 + i) : 1.f;
+    s[i] = in ? __ldg(p.cos_sin + (int64_t)pos * 2 * n + n + pair0 + i) : 0.f;
+  }
+  return ok;
+}
+
+// (a c - b s, b c + a s), every product and sum rounded to fp32
+__device__ __forceinline__ void turn(float a, float b, float c, float s, float &x, float &y) {
+  x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+}
+// Pairs (element i of `lo`, element i of `hi`), i < 8.
+__device__ __forceinline__ void turn_halves(uint4 &lo, uint4 &hi, const float (&c)[8], const float (&s)[8]) {
+  uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x0, y0, x1, y1;
+    turn(bf_lo(a[i]), bf_lo(b[i]), c[2 * i], s[2 * i], x0, y0);
+    turn(bf_hi(a[i]), bf_hi(b[i]), c[2 * i + 1], s[2 * i + 1], x1, y1);
+    a[i] = pack_bf16(x0, x1);
+    b[i] = pack_bf16(y0, y1);
+  }
+  lo = make_uint4(a[0], a[1], a[2], a[3]);
+  hi = make_uint4(b[0], b[1], b[2], b[3]);
+}
+// Pairs of neighbours: elements 2i, 2i + 1 of `v`, i < 4, with cosines c[at + i].
+__device__ __forceinline__ void turn_adjacent(uint4 &v, const float (&c)[8], const float (&s)[8], int at) {
+  uint32_t a[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float x, y;
+    turn(bf_lo(a[i]), bf_hi(a[i]), c[at + i], s[at + i], x, y);
+    a[i] = pack_bf16(x, y);
+  }
+  v = make_uint4(a[0], a[1], a[2], a[3]);
+}
+
+// HEAD: elements of a rotated head, 128 (the latent cache: 64).
+template <int KIND, int HEAD>
+__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const __grid_constant__ CacheRowParams p) {
+  constexpr int kChunks = HEAD / 8;        // 16-byte chunks of a head
+  constexpr int kLanes = kChunks / 2;      // lanes of a head with both halves of its pairs
+  constexpr int kHeads = 32 / kLanes;      // query heads a warp takes at once
+  constexpr int kDeep = kAhead / 2;        // groups of them in flight
   const int lane = threadIdx.x & 31;
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = item / p.parts;
+  const int64_t t = p.parts == 1 ? item : (int64_t)((uint32_t)item / (uint32_t)p.parts);
   const int part = (int)(item - t * p.parts);
   if (t >= p.num_tokens) return;
-  const int l = lane % LPH, sub = lane / LPH;
-  const int HQ = p.q ? p.num_q_heads : 0;
-  const int HK = p.k_new ? (KIND == kLatent ? 1 : p.num_kv_heads) : 0;
-  const int heads = HQ + (KIND == kLatent ? HK : 2 * HK);  // rotated q, rotated k, then v
-  const int groups = (heads + kPer - 1) / kPer;
-  const int g0 = (int)((int64_t)part * groups / p.parts), g1 = (int)((int64_t)(part + 1) * groups / p.parts);
-  const __nv_bfloat16 *qrow = p.q + t * p.q_stride, *krow = p.k_new + t * p.k_stride, *vrow = p.v_new + t * p.v_stride;
-  auto src_of = [&](int hd) -> const uint4 * {
-    const __nv_bfloat16 *s = hd < HQ ? qrow + (int64_t)hd * kHead
-                             : KIND == kLatent ? vrow  // the rope part of the latent row
-                             : hd < HQ + HK ? krow + (hd - HQ) * kHead
-                                            : vrow + (hd - HQ - HK) * kHead;
-    return reinterpret_cast<const uint4 *>(s) + l;
-  };
-  uint4 w[kAhead];
-  auto load = [&](int g) {
+  const int HQ = p.q ? p.num_q_heads : 0, HK = p.k_new ? p.num_kv_heads : 0;
+  // groups: queries kHeads at a time, then (not the latent cache) keys and values two at a time
+  const int nq = (HQ + kHeads - 1) / kHeads, nk = KIND == kLatent ? 0 : (HK + 1) / 2;
+  const int groups = nq + 2 * nk;
+  const int g0 = (int)((uint32_t)(part * groups) / (uint32_t)p.parts);
+  const int g1 = (int)((uint32_t)((part + 1) * groups) / (uint32_t)p.parts);
+
+  // ---- queries: this lane's chunks of a head. Half-split pairs of r chunks: lane i < r
+  // has chunks i and i + r; neighbours as pairs: chunks 2i and 2i + 1; elements past
+  // the rotated ones stay, two chunks a lane.
+  const int l = lane % kLanes, sub = lane / kLanes, r = p.rope_pairs / 8;
+  const bool turned = l < r;
+  const bool split = turned && !p.rope_adjacent;
+  const int ca = split ? l : 2 * l, cb = split ? l + r : 2 * l + 1;
+  const int gq1 = min(g1, nq);
+  const uint4 *qsrc = reinterpret_cast<const uint4 *>(p.q + t * p.q_stride);
+  uint4 a[kDeep], b[kDeep];
+  auto load_q = [&](int g) {
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int hd = (g + k) * kPer + sub;
-      w[k] = make_uint4(0u, 0u, 0u, 0u);
-      if (g + k < g1 && hd < heads) w[k] = __ldg(src_of(hd));
+    for (int k = 0; k < kDeep; ++k) {
+      const int hd = (g + k) * kHeads + sub;
+      if (g + k < gq1 && hd < HQ) {
+        a[k] = __ldg(qsrc + hd * kChunks + ca);
+        b[k] = __ldg(qsrc + hd * kChunks + cb);
+      }
     }
   };
-  load(g0);  // in flight while the slot and the position are looked up
+  load_q(g0);  // in flight while the slot and the positions are looked up
   uint32_t err = 0;
   const int64_t slot = load_slot(p, t, err);
   const bool padding = p.slot_map != nullptr && slot < 0;
-  // this lane's pairs: half-split lanes l and l + n / 8 hold elements i and i + n
-  const int n = p.rope_pairs;
-  const int nl = n / 8;                       // lanes of a half (half-split)
-  const bool turned = n > 0 && l < 2 * nl;
-  const bool second = !p.rope_adjacent && l >= nl;
-  const int pair0 = p.rope_adjacent ? 4 * l : 8 * (second ? l - nl : l);
-  const int npairs = p.rope_adjacent ? 4 : 8;
   float c[8], s[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    c[i] = 1.f;
-    s[i] = 0.f;
-  }
   bool bad = false;
-  if (turned) {
-    if (p.rope_whole) {  // one axis per aligned group of this lane's pairs: vector loads
-      const int pos = __ldg(p.positions + (int64_t)p.pair_axis[pair0] * p.position_stride + t);
-      bad = pos < 0 || pos >= p.max_position;
-      if (!bad) {
-        const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + pair0);
-        const float4 *row2 = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + n + pair0);
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-          if (4 * j < npairs) {
-            const float4 a = __ldg(row + j), b = __ldg(row2 + j);
-            c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
-            s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
-          }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (i < npairs) {
-          const int pos = __ldg(p.positions + (int64_t)p.pair_axis[pair0 + i] * p.position_stride + t);
-          const bool b = pos < 0 || pos >= p.max_position;
-          bad = bad || b;
-          if (!b) {
-            c[i] = __ldg(p.cos_sin + (int64_t)pos * 2 * n + pair0 + i);
-            s[i] = __ldg(p.cos_sin + (int64_t)pos * 2 * n + n + pair0 + i);
-          }
-        }
-    }
-  }
+  if (turned) bad = !load_turn<8>(p, t, 8 * l, c, s);
   bad = __any_sync(0xffffffffu, bad);
   if (bad && !padding) err |= DA_DEVERR_POSITION;
   if (err && lane == 0) atomicOr(p.err, err);
   if (bad || padding) return;
-  const int64_t page = p.slot_map ? slot / p.rows_per_page : 0;
-  const int off = p.slot_map ? (int)(slot - page * p.rows_per_page) : 0;
-  const int64_t qbase = p.q_len > 1 ? (t / p.q_len * p.num_q_heads) * p.q_len + t % p.q_len : t * p.num_q_heads;
-  const int partner = lane - l + (second ? l - nl : l + nl);
-
-  for (int g = g0; g < g1; g += kAhead) {
-    if (g > g0) load(g);
+  {
+    const bool many = p.q_len > 1;
+    const int64_t row0 = many ? (t / p.q_len * p.num_q_heads) * p.q_len + t % p.q_len : t * p.num_q_heads;
+    const int step = (many ? p.q_len : 1) * kChunks;
+    uint4 *dst = reinterpret_cast<uint4 *>(p.q_out) + row0 * kChunks;
+    for (int g = g0; g < gq1; g += kDeep) {
+      if (g > g0) load_q(g);
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (g + k >= g1) break;
-      const int hd = (g + k) * kPer + sub;
-      const bool on = hd < heads;
-      const bool is_q = hd < HQ, is_v = KIND != kLatent && hd >= HQ + HK;
-      float x[8] = {bf_lo(w[k].x), bf_hi(w[k].x), bf_lo(w[k].y), bf_hi(w[k].y),
-                    bf_lo(w[k].z), bf_hi(w[k].z), bf_lo(w[k].w), bf_hi(w[k].w)};
-      if (n > 0 && __any_sync(0xffffffffu, !is_v)) {
-        uint4 o = w[k];
-        if (p.rope_adjacent) {
-          float y[8];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            y[2 * i] = __fsub_rn(__fmul_rn(x[2 * i], c[i]), __fmul_rn(x[2 * i + 1], s[i]));
-            y[2 * i + 1] = __fadd_rn(__fmul_rn(x[2 * i + 1], c[i]), __fmul_rn(x[2 * i], s[i]));
-          }
-          o = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
-        } else {
-          uint4 z;
-          z.x = __shfl_sync(0xffffffffu, w[k].x, partner);
-          z.y = __shfl_sync(0xffffffffu, w[k].y, partner);
-          z.z = __shfl_sync(0xffffffffu, w[k].z, partner);
-          z.w = __shfl_sync(0xffffffffu, w[k].w, partner);
-          const float u[8] = {bf_lo(z.x), bf_hi(z.x), bf_lo(z.y), bf_hi(z.y),
-                              bf_lo(z.z), bf_hi(z.z), bf_lo(z.w), bf_hi(z.w)};
-          float y[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float a = __fmul_rn(x[i], c[i]), b = __fmul_rn(u[i], s[i]);
-            y[i] = second ? __fadd_rn(a, b) : __fsub_rn(a, b);
-          }
-          o = make_uint4(pack_bf16(y[0], y[1]), pack_bf16(y[2], y[3]), pack_bf16(y[4], y[5]), pack_bf16(y[6], y[7]));
+      for (int k = 0; k < kDeep; ++k) {
+        const int hd = (g + k) * kHeads + sub;
+        if (g + k >= gq1 || hd >= HQ) continue;
+        if (split) {
+          turn_halves(a[k], b[k], c, s);
+        } else if (turned) {
+          turn_adjacent(a[k], c, s, 0);
+          turn_adjacent(b[k], c, s, 4);
         }
-        if (turned && !is_v) {
-          w[k] = o;
-          x[0] = bf_lo(o.x), x[1] = bf_hi(o.x), x[2] = bf_lo(o.y), x[3] = bf_hi(o.y);
-          x[4] = bf_lo(o.z), x[5] = bf_hi(o.z), x[6] = bf_lo(o.w), x[7] = bf_hi(o.w);
-        }
-      }
-      if (on && is_q) {
-        const int64_t row = p.q_len > 1 ? qbase + (int64_t)hd * p.q_len : qbase + hd;
-        *(reinterpret_cast<uint4 *>(p.q_out) + row * LPH + l) = w[k];
-      }
-      if (KIND == kLatent) {
-        if (on && !is_q) *(reinterpret_cast<uint4 *>(p.v) + slot * 8 + l) = w[k];
-      } else if (__any_sync(0xffffffffu, on && !is_q)) {
-        const int h = hd - HQ - (is_v ? HK : 0);
-        put_row<KIND>(p, is_v, on && !is_q, cache_row(p, page, off, h), h, l, x, w[k]);
+        dst[(int64_t)hd * step + ca] = a[k];
+        dst[(int64_t)hd * step + cb] = b[k];
       }
     }
   }
-  if (KIND == kLatent && HK && part == p.parts - 1) {  // the 512 latent elements, as they are
-    const uint4 *src = reinterpret_cast<const uint4 *>(krow) + lane;
+  if (HK == 0) return;
+  if constexpr (KIND == kLatent) {
+    // the row of the latent cache: 512 elements as they are, 64 turned, by the last part
+    if (part != p.parts - 1) return;
+    const uint4 *src = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + lane;
     uint4 *dst = reinterpret_cast<uint4 *>(p.k) + slot * 64 + lane;
-    const uint4 a = __ldg(src), b = __ldg(src + 32);
-    dst[0] = a;
-    dst[32] = b;
+    const uint4 x = __ldg(src), y = __ldg(src + 32);
+    dst[0] = x;
+    dst[32] = y;
+    if (lane < kLanes) {
+      const uint4 *rope = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride);
+      uint4 u = __ldg(rope + ca), v = __ldg(rope + cb);
+      if (split) {
+        turn_halves(u, v, c, s);
+      } else if (turned) {
+        turn_adjacent(u, c, s, 0);
+        turn_adjacent(v, c, s, 4);
+      }
+      uint4 *out = reinterpret_cast<uint4 *>(p.v) + slot * 8;
+      out[ca] = u;
+      out[cb] = v;
+    }
+    return;
+  } else {
+    if (g1 <= nq) return;
+    // ---- keys and values: 16 lanes a head, two heads at once
+    const int kl = lane & 15, ksub = lane >> 4;
+    const bool kturned = kl < 2 * r, second = kturned && !p.rope_adjacent && kl >= r;
+    const int partner = lane - kl + (kturned && !p.rope_adjacent ? (second ? kl - r : kl + r) : kl);
+    const RowAt at = row_at<KIND>(p, slot, kl);
+    const int first = max(g0, nq);
+    if (first < nq + nk && r > 0) {  // some key is this warp's
+      if (kturned) {
+        if (p.rope_adjacent) load_turn<4>(p, t, 4 * kl, c, s);
+        else load_turn<8>(p, t, 8 * (second ? kl - r : kl), c, s);
+      }
+      if (second)  // (b c + a s) is (x c - u s) with s of the other sign
+#pragma unroll
+        for (int i = 0; i < 8; ++i) s[i] = -s[i];
+    }
+    const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + kl;
+    const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride) + kl;
+    for (int g = first; g < g1; g += kAhead) {
+      uint4 w[kAhead];
+      float hs[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool is_v = g + k >= nq + nk;
+        const int h = (g + k - nq - (is_v ? nk : 0)) * 2 + ksub;
+        w[k] = make_uint4(0u, 0u, 0u, 0u);
+        hs[k] = 1.f;
+        if (g + k < g1 && h < HK) {
+          w[k] = __ldg((is_v ? vsrc : ksrc) + h * 16);
+          if (KIND == kE4m3 || KIND == kFp4) hs[k] = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        if (g + k >= g1) break;
+        const bool is_v = g + k >= nq + nk;
+        const int h = (g + k - nq - (is_v ? nk : 0)) * 2 + ksub;
+        if (!is_v && r > 0) {
+          if (p.rope_adjacent) {
+            if (kturned) turn_adjacent(w[k], c, s, 0);
+          } else {
+            const uint4 z = make_uint4(__shfl_sync(0xffffffffu, w[k].x, partner), __shfl_sync(0xffffffffu, w[k].y, partner),
+                                       __shfl_sync(0xffffffffu, w[k].z, partner), __shfl_sync(0xffffffffu, w[k].w, partner));
+            if (kturned) {
+              uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+              const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                x[i] = pack_bf16(__fsub_rn(__fmul_rn(bf_lo(x[i]), c[2 * i]), __fmul_rn(bf_lo(u[i]), s[2 * i])),
+                                 __fsub_rn(__fmul_rn(bf_hi(x[i]), c[2 * i + 1]), __fmul_rn(bf_hi(u[i]), s[2 * i + 1])));
+              w[k] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          }
+        }
+        put_row<KIND>(p, h < HK, (is_v ? at.v : at.k) + h * at.head, (is_v ? at.vs : at.ks) + h * at.shead, hs[k], kl, w[k]);
+      }
+    }
   }
 }
 
-// Eight elements (lane l of 16) of row `row` as bf16 pairs: each value is the
-// fp32 product (and sum) of its parts, rounded once more to bf16.
+// Eight elements (lane l of 16) of a row as bf16 pairs: each value is the fp32
+// product (and sum) of its parts, rounded once more to bf16.
 struct RowBits {
   uint4 a;      // the lane's codes (bf16: its values)
   uint32_t s;   // block scale byte, or scale and shift halves
 };
 template <int KIND>
-__device__ __forceinline__ RowBits get_row(const CacheRowParams &p, bool is_v, int64_t row, int l) {
-  const void *cache = is_v ? p.v : p.k;
+__device__ __forceinline__ RowBits get_row(const uint8_t *src, const uint8_t *ssrc) {
   RowBits r;
   r.a = make_uint4(0u, 0u, 0u, 0u);
   r.s = 0;
-  if (KIND == kBf16) r.a = __ldg(reinterpret_cast<const uint4 *>(cache) + row * 16 + l);
+  if (KIND == kBf16) r.a = __ldg(reinterpret_cast<const uint4 *>(src));
   if (KIND == kE4m3 || KIND == kE4m3Token) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(cache) + row * 16 + l);
+    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
     r.a.x = v.x;
     r.a.y = v.y;
-    if (KIND == kE4m3Token) r.s = (uint32_t)__ldg((is_v ? p.v_scale_shift : p.k_scale_shift) + row);
   }
-  if (KIND == kInt4) {
-    const uint32_t *src = reinterpret_cast<const uint32_t *>(cache) + row * (p.kv_groups + 16);
-    r.a.x = __ldg(src + p.kv_groups + l);
-    r.s = __ldg(src + l * p.kv_groups / 16);
-  }
-  if (KIND == kFp4) {
-    const uint8_t *gran = reinterpret_cast<const uint8_t *>(cache) + (row >> 4) * 1152;
-    const int i = (int)(row & 15);
-    r.a.x = __ldg(reinterpret_cast<const uint32_t *>(gran + i * 64 + l * 4));
-    r.s = __ldg(gran + 1024 + i * 8 + (l >> 1));
-  }
+  if (KIND == kInt4 || KIND == kFp4) r.a.x = __ldg(reinterpret_cast<const uint32_t *>(src));
+  if (KIND == kInt4 || KIND == kE4m3Token) r.s = __ldg(reinterpret_cast<const uint32_t *>(ssrc));
+  if (KIND == kFp4) r.s = __ldg(ssrc);
   return r;
 }
 template <int KIND>
-__device__ __forceinline__ uint4 row_values(const CacheRowParams &p, const RowBits &r, float head_scale) {
+__device__ __forceinline__ uint4 row_values(const RowBits &r, float head_scale) {
   if (KIND == kBf16) return r.a;
   float x[8];
   if (KIND == kE4m3 || KIND == kE4m3Token) {
@@ -411,33 +506,29 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
     return;
   }
   const int l = lane & 15, sub = lane >> 4;
-  const int64_t page = slot / p.rows_per_page;
-  const int off = (int)(slot - page * p.rows_per_page);
-  const int rows = 2 * p.num_kv_heads;  // K then V; two rows at once
-  const int groups = p.num_kv_heads;
-  const int g0 = (int)((int64_t)part * groups / p.parts), g1 = (int)((int64_t)(part + 1) * groups / p.parts);
+  const RowAt at = row_at<KIND>(p, slot, l);
+  // heads two at once, of K and then of V; kAhead loads in flight
+  const int HK = p.num_kv_heads, nk = (HK + 1) / 2;
+  const int g0 = (int)((uint32_t)(part * 2 * nk) / (uint32_t)p.parts);
+  const int g1 = (int)((uint32_t)((part + 1) * 2 * nk) / (uint32_t)p.parts);
+  uint4 *ko = reinterpret_cast<uint4 *>(p.k_out) + t * HK * 16 + l, *vo = reinterpret_cast<uint4 *>(p.v_out) + t * HK * 16 + l;
   for (int g = g0; g < g1; g += kAhead) {
     RowBits r[kAhead];
     float hs[kAhead];
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = (g + k) * 2 + sub;
-      if (g + k < g1 && i < rows) {
-        const bool is_v = i >= p.num_kv_heads;
-        const int h = is_v ? i - p.num_kv_heads : i;
-        r[k] = get_row<KIND>(p, is_v, cache_row(p, page, off, h), l);
+      const bool is_v = g + k >= nk;
+      const int h = (g + k - (is_v ? nk : 0)) * 2 + sub;
+      if (g + k < g1 && h < HK) {
+        r[k] = get_row<KIND>((is_v ? at.v : at.k) + h * at.head, (is_v ? at.vs : at.ks) + h * at.shead);
         if (KIND == kE4m3 || KIND == kFp4) hs[k] = __ldg((is_v ? p.v_scale : p.k_scale) + h);
       }
     }
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const int i = (g + k) * 2 + sub;
-      if (g + k < g1 && i < rows) {
-        const bool is_v = i >= p.num_kv_heads;
-        const int h = is_v ? i - p.num_kv_heads : i;
-        *(reinterpret_cast<uint4 *>(is_v ? p.v_out : p.k_out) + (t * p.num_kv_heads + h) * 16 + l) =
-            row_values<KIND>(p, r[k], hs[k]);
-      }
+      const bool is_v = g + k >= nk;
+      const int h = (g + k - (is_v ? nk : 0)) * 2 + sub;
+      if (g + k < g1 && h < HK) (is_v ? vo : ko)[h * 16] = row_values<KIND>(r[k], hs[k]);
     }
   }
 }
@@ -456,26 +547,27 @@ int parts_for(int64_t tokens, int groups, int num_sms) {
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  const int per = kind == kLatent ? 4 : 2;
-  const int heads = (p.q ? p.num_q_heads : 0) + (p.k_new ? (kind == kLatent ? 1 : 2 * p.num_kv_heads) : 0);
-  if (heads == 0) return cudaSuccess;
-  p.parts = parts_for(p.num_tokens, (heads + per - 1) / per, num_sms);
+  if (!p.q && !p.k_new) return cudaSuccess;
+  const int per = kind == kLatent ? 8 : 4;
+  const int groups = (p.q ? (p.num_q_heads + per - 1) / per : 0) +
+                     (p.k_new && kind != kLatent ? 2 * ((p.num_kv_heads + 1) / 2) : 0);
+  p.parts = parts_for(p.num_tokens, groups < 1 ? 1 : groups, num_sms);
   const int64_t blocks = blocks_for((int64_t)p.num_tokens * p.parts);
   const unsigned grid = (unsigned)blocks;
   switch (kind) {
-    case kBf16: append_kernel<kBf16, 16><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kE4m3: append_kernel<kE4m3, 16><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kE4m3Token: append_kernel<kE4m3Token, 16><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kInt4: append_kernel<kInt4, 16><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kFp4: append_kernel<kFp4, 16><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    default: append_kernel<kLatent, 8><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kBf16: append_kernel<kBf16, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kE4m3: append_kernel<kE4m3, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kE4m3Token: append_kernel<kE4m3Token, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kInt4: append_kernel<kInt4, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kFp4: append_kernel<kFp4, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    default: append_kernel<kLatent, 64><<<grid, kWarps * 32, 0, stream>>>(p); break;
   }
   return cudaGetLastError();
 }
 
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  p.parts = kind == kLatent ? 1 : parts_for(p.num_tokens, p.num_kv_heads, num_sms);
+  p.parts = kind == kLatent ? 1 : parts_for(p.num_tokens, 2 * ((p.num_kv_heads + 1) / 2), num_sms);
   const unsigned grid = (unsigned)blocks_for((int64_t)p.num_tokens * p.parts);
   switch (kind) {
     case kBf16: gather_kernel<kBf16><<<grid, kWarps * 32, 0, stream>>>(p); break;
