@@ -52,11 +52,17 @@ constexpr float kRaise = 1024.f;     // a sum of weights past this raises their 
 
 template <int NT>
 struct F4 {
-  static constexpr int kWarps = NT == 1 ? 15 : 11;                // consumers: with the producer four (three) a scheduler
+  static constexpr int kWarps = NT == 1 ? 15 : 11;               // consumers: with the walker four (three) a scheduler
   static constexpr int kThreads = (kWarps + 1) * 32;             // and the producer warp
-  static constexpr int kStages = NT == 1 ? 3 : 4;
+  static constexpr int kStages = 3;
+  // Q^T fragments: registers for up to eight rows; for sixteen, whose O takes 64
+  // registers a thread, shared memory (16 bytes a lane and k-step): 16 rows x 4 query
+  // tokens 89.6 -> 80.9 us (four warps a scheduler instead, in 128 registers: 118 us)
+  static constexpr bool kQShared = NT == 2;
+  static constexpr int kQBytes = kQShared ? 8 * 32 * 16 : 0;
   static constexpr int kRingBytes = kStages * kStageBytes;       // one warp's ring
-  static constexpr int oStall = kWarps * kRingBytes;             // the test stall's barrier
+  static constexpr int oQ = kWarps * kRingBytes;                 // [warp][k-step][lane]
+  static constexpr int oStall = oQ + kWarps * kQBytes;           // the test stall's barrier
   static constexpr int oCount = oStall + 16;                     // [16] tiles described, [16] tiles read, per warp
   static constexpr int oDesc = oCount + 128;                     // [warp][kQueue] F4Tile
   static constexpr int oStat = oDesc + kWarps * kQueue * 48;     // [warp][tail|head][m|l][16]
@@ -96,24 +102,6 @@ struct Cut {
   __device__ __forceinline__ int owner(uint32_t t) const {
     const uint32_t split = rem * (base + 1);
     return (int)(t < split ? t / (base + 1) : rem + (t - split) / base);
-  }
-};
-
-// A CTA's n tiles cut into one range per consumer warp. The walker's scheduler has a
-// consumer less, so its warps (w % 4 == 3) run a little faster: they get kFast shares
-// where the others get kShare (equal shares left them 10 % ahead of the others).
-template <int W>
-struct WarpCut {
-  static constexpr uint32_t kShare = 10, kFast = W == 15 ? 11 : 12;
-  static constexpr uint32_t kAll = kShare * W + (kFast - kShare) * ((W + 1) / 4 - 1 + ((W + 1) % 4 == 0 ? 0 : 1));
-  int n;
-  __device__ __forceinline__ int start(int w) const {
-    return (int)((uint64_t)(uint32_t)n * (kShare * w + (kFast - kShare) * (w / 4)) / kAll);
-  }
-  __device__ __forceinline__ int owner(int t) const {
-    int w = 0;
-    while (w + 1 < W && start(w + 1) <= t) ++w;
-    return w;
   }
 };
 
@@ -301,7 +289,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   }
   const Cut cut((uint32_t)T, (uint32_t)CTAS);
   const int lo = cut.start(cta), n_cta = cut.start(cta + 1) - lo, hi = lo + n_cta;
-  const WarpCut<W> wcut{n_cta};
+  const Cut wcut((uint32_t)n_cta, W);
   uint64_t *stall_bar = reinterpret_cast<uint64_t *>(smem + C::oStall);  // nothing arrives on it
   uint32_t *ready_all = reinterpret_cast<uint32_t *>(smem + C::oCount);  // tiles described, per warp
   uint32_t *done_all = ready_all + 16;                                   // and tiles read
@@ -535,6 +523,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     cp_async_commit();
     // ------------------------------------------------------------ the stream
     uint32_t qf[NT][8][2];
+    uint4 *qs = reinterpret_cast<uint4 *>(smem + C::oQ + warp * C::kQBytes) + lane;  // kQShared
     float oacc[NT][8][4];
     float m_neg[NT][2], l_part[NT][2];  // minus the weights' reference (log2 units), and their sums
     bool no_ref[NT][2];
@@ -611,12 +600,15 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         const int qexp = q_exponent(amax);
         const float q2 = pow2f(qexp);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int s = 0; s < 8; ++s) {
-            qf[nt][s][0] = bf16x2_to_f16x2(qw[nt][s].x, q2);
-            qf[nt][s][1] = bf16x2_to_f16x2(qw[nt][s].y, q2);
+        for (int s = 0; s < 8; ++s) {
+          if constexpr (C::kQShared) {  // (each lane reads back what it wrote)
+            qs[s * 32] = make_uint4(bf16x2_to_f16x2(qw[0][s].x, q2), bf16x2_to_f16x2(qw[0][s].y, q2),
+                                    bf16x2_to_f16x2(qw[NT - 1][s].x, q2), bf16x2_to_f16x2(qw[NT - 1][s].y, q2));
+          } else {
+            qf[0][s][0] = bf16x2_to_f16x2(qw[0][s].x, q2);
+            qf[0][s][1] = bf16x2_to_f16x2(qw[0][s].y, q2);
           }
+        }
         sscale = p.score_scale * p.k_scale[h] * pow2f(-qexp);
         // a zero factor (uniform weights) as 2^-100: a finite score still weighs 1, and
         // an infinite one (a masked token's) 0
@@ -655,28 +647,45 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         // between them would keep their instructions apart; what a half that was not
         // copied holds is masked below)
         float s[NT][2][4];
+        uint4 ra[2], rb[2];
+        uint32_t sa[2], sb[2];
 #pragma unroll
         for (int gi = 0; gi < 2; ++gi) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[nt][gi][0] = s[nt][gi][1] = s[nt][gi][2] = s[nt][gi][3] = 0.f;
           const uint8_t *gk = stage + gi * kGranBytes;
-          const uint4 ra = *reinterpret_cast<const uint4 *>(gk + k_off);
-          const uint4 rb = *reinterpret_cast<const uint4 *>(gk + k_off + 512);
-          const uint32_t sa = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + ks_off));
-          const uint32_t sb = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + ks_off + 64));
-          const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+          ra[gi] = *reinterpret_cast<const uint4 *>(gk + k_off);
+          rb[gi] = *reinterpret_cast<const uint4 *>(gk + k_off + 512);
+          sa[gi] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + ks_off));
+          sb[gi] = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(gk + ks_off + 64));
+        }
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {  // word c: k-steps 2c and 2c + 1, block c / 2 of the lane's two
+        for (int c = 0; c < 4; ++c) {  // word c: k-steps 2c and 2c + 1, block c / 2 of the lane's two
+          uint32_t q[2][NT][2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if constexpr (C::kQShared) {
+              const uint4 v = qs[(2 * c + k) * 32];
+              q[k][0][0] = v.x;
+              q[k][0][1] = v.y;
+              q[k][NT - 1][0] = v.z;
+              q[k][NT - 1][1] = v.w;
+            } else {
+              q[k][0][0] = qf[0][2 * c + k][0];
+              q[k][0][1] = qf[0][2 * c + k][1];
+            }
+          }
+#pragma unroll
+          for (int gi = 0; gi < 2; ++gi) {
             uint32_t fa[4], fb[4];
-            e2m1x8_to_f16(wa[c], fa);
-            e2m1x8_to_f16(wb[c], fb);
+            e2m1x8_to_f16(c == 0 ? ra[gi].x : c == 1 ? ra[gi].y : c == 2 ? ra[gi].z : ra[gi].w, fa);
+            e2m1x8_to_f16(c == 0 ? rb[gi].x : c == 1 ? rb[gi].y : c == 2 ? rb[gi].z : rb[gi].w, fb);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t a0 = f4_scale(fa[2 * k], sa, c >> 1), a2 = f4_scale(fa[2 * k + 1], sa, c >> 1);
-              const uint32_t a1 = f4_scale(fb[2 * k], sb, c >> 1), a3 = f4_scale(fb[2 * k + 1], sb, c >> 1);
+              const uint32_t a0 = f4_scale(fa[2 * k], sa[gi], c >> 1), a2 = f4_scale(fa[2 * k + 1], sa[gi], c >> 1);
+              const uint32_t a1 = f4_scale(fb[2 * k], sb[gi], c >> 1), a3 = f4_scale(fb[2 * k + 1], sb[gi], c >> 1);
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-                mma_f16_16816(s[nt][gi], a0, a1, a2, a3, qf[nt][2 * c + k][0], qf[nt][2 * c + k][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][gi], a0, a1, a2, a3, q[k][nt][0], q[k][nt][1]);
             }
           }
         }
