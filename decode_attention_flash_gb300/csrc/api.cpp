@@ -317,6 +317,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
     f.k = reinterpret_cast<const uint8_t *>(a->k);
     f.v = reinterpret_cast<const uint8_t *>(a->v);
     f.o_head = reinterpret_cast<float *>(ws + da::fp4_head_offset(pl));
+    f.whole = pl.writes_final;
     return da::launch_fp4(f, pl.grid_x, stream) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
   }
   if (da::launch_gqa(fp8, gp.group, ctx->kmap, ctx->vmap, ctx->qmap,

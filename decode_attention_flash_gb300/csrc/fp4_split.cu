@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   }
   if (threadIdx.x <= W) lead[threadIdx.x] = make_int4(-1, 0, 0, 0);
 
-  // ---- the schedule: the tiles of all units, end to end, one range per CTA. Thread t
+  // ---- the schedule. fp.whole: CTA c has unit c, whole (nothing to scan, no piece
+  // leaves the CTA). Else the tiles of all units, end to end, one range per CTA. Thread t
   // counts the items [t * per, t * per + per): rows (all heads of a dense row are alike)
   // or, for listed blocks, units. The prefix sums stay in shared memory, where the
   // walker finds the unit that each warp's range starts in.
@@ -247,48 +248,62 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   auto item_tiles = [&](int it, uint32_t &err) -> int {  // of one unit of item `it`
     return f4_unit_info(p, sparse ? it : it * heads, err).tiles;
   };
+  // rows without a tile: zeros and -inf from the warp of the CTA that the item falls to
+  auto write_empty = [&](int64_t row0, int rows) {
+    for (int i = lane; i < rows * (kD / 8); i += 32)
+      reinterpret_cast<uint4 *>(p.out + row0 * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (p.lse)
+      for (int i = lane; i < rows; i += 32) p.lse[row0 + i] = neg_inf();
+  };
+  int T = 0, CTAS = 1;
+  if (fp.whole) {
+    const UnitInfo x = f4_unit_info(p, cta, dev_err);
+    T = x.tiles;
+    if (T == 0) {
+      if (warp == 0) write_empty((int64_t)x.b * p.num_q_heads + x.h * G, G);
+      if (dev_err) atomicOr(p.err, dev_err);
+      return;
+    }
+  }
   int local = 0;
-  for (int k = 0; k < per; ++k) {
+  for (int k = 0; !fp.whole && k < per; ++k) {
     const int it = (int)threadIdx.x * per + k;
     const int t = it < items ? item_tiles(it, dev_err) : 1;
     if (it < items) local += t * heads;
-    // rows without a tile: zeros and -inf from the warp of the CTA that the item falls to
     uint32_t none = __ballot_sync(0xffffffffu, t == 0 && it % (int)gridDim.x == cta);
     for (; none != 0; none &= none - 1) {
       const int e = __shfl_sync(0xffffffffu, it, __ffs(none) - 1);
-      const int rows = heads * G;
-      const int64_t row0 = sparse ? (int64_t)(e / p.num_kv_heads) * p.num_q_heads + e % p.num_kv_heads * G
-                                  : (int64_t)e * p.num_q_heads;
-      for (int i = lane; i < rows * (kD / 8); i += 32)
-        reinterpret_cast<uint4 *>(p.out + row0 * kD)[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (p.lse)
-        for (int i = lane; i < rows; i += 32) p.lse[row0 + i] = neg_inf();
+      write_empty(sparse ? (int64_t)(e / p.num_kv_heads) * p.num_q_heads + e % p.num_kv_heads * G
+                         : (int64_t)e * p.num_q_heads,
+                  heads * G);
     }
   }
+  if (!fp.whole) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, local, o);
-    if (lane >= o) local += v;
-  }
-  if (lane == 31) scan[warp] = local;
-  if (threadIdx.x < 16 && threadIdx.x > W) scan[threadIdx.x] = 0;  // (a vector of 16 sums is read)
-  __syncthreads();
-  int T = 0, before = 0;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, local, o);
+      if (lane >= o) local += v;
+    }
+    if (lane == 31) scan[warp] = local;
+    if (threadIdx.x < 16 && threadIdx.x > W) scan[threadIdx.x] = 0;  // (a vector of 16 sums is read)
+    __syncthreads();
+    int before = 0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int4 v = reinterpret_cast<const int4 *>(scan)[k];
-    before += (4 * k < warp ? v.x : 0) + (4 * k + 1 < warp ? v.y : 0) + (4 * k + 2 < warp ? v.z : 0) +
-              (4 * k + 3 < warp ? v.w : 0);
-    T += v.x + v.y + v.z + v.w;
-  }
-  pre[threadIdx.x] = before + local;
-  const int CTAS = T < (int)gridDim.x ? T : (int)gridDim.x;  // never more ranges than tiles
-  if (cta >= CTAS) {
-    if (dev_err) atomicOr(p.err, dev_err);
-    return;
+    for (int k = 0; k < 4; ++k) {
+      const int4 v = reinterpret_cast<const int4 *>(scan)[k];
+      before += (4 * k < warp ? v.x : 0) + (4 * k + 1 < warp ? v.y : 0) + (4 * k + 2 < warp ? v.z : 0) +
+                (4 * k + 3 < warp ? v.w : 0);
+      T += v.x + v.y + v.z + v.w;
+    }
+    pre[threadIdx.x] = before + local;
+    CTAS = T < (int)gridDim.x ? T : (int)gridDim.x;  // never more ranges than tiles
+    if (cta >= CTAS) {
+      if (dev_err) atomicOr(p.err, dev_err);
+      return;
+    }
   }
   const Cut cut((uint32_t)T, (uint32_t)CTAS);
-  const int lo = cut.start(cta), n_cta = cut.start(cta + 1) - lo, hi = lo + n_cta;
+  const int lo = fp.whole ? 0 : cut.start(cta), n_cta = fp.whole ? T : cut.start(cta + 1) - lo, hi = lo + n_cta;
   const Cut wcut((uint32_t)n_cta, W);
   uint64_t *stall_bar = reinterpret_cast<uint64_t *>(smem + C::oStall);  // nothing arrives on it
   uint32_t *ready_all = reinterpret_cast<uint32_t *>(smem + C::oCount);  // tiles described, per warp
@@ -344,30 +359,35 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       prefetch_l2(p.q + ((int64_t)x.b * p.num_q_heads + x.h * G) * kD, (uint32_t)(G * kD * 2));
     };
     if (ntiles > 0) {
-      // the thread whose items hold tile wlo, then the item, then the head
-      int first = 0;
-      for (int n = C::kThreads; n > 0;) {  // the number of threads whose sum is at most wlo
-        const int half = n >> 1;
-        if (pre[first + half] <= wlo) {
-          first += half + 1;
-          n -= half + 1;
-        } else {
-          n = half;
-        }
-      }
-      Pu = first > 0 ? pre[first - 1] : 0;
       uint32_t ignored = 0;
-      int it = first * per;
-      x = f4_unit_info(p, it * heads, ignored);
-      while (wlo >= Pu + x.tiles * heads) {
-        Pu += x.tiles * heads;
-        ++it;
+      if (fp.whole) {
+        u = cta;
+        x = f4_unit_info(p, u, ignored);
+      } else {
+        // the thread whose items hold tile wlo, then the item, then the head
+        int first = 0;
+        for (int n = C::kThreads; n > 0;) {  // the number of threads whose sum is at most wlo
+          const int half = n >> 1;
+          if (pre[first + half] <= wlo) {
+            first += half + 1;
+            n -= half + 1;
+          } else {
+            n = half;
+          }
+        }
+        Pu = first > 0 ? pre[first - 1] : 0;
+        int it = first * per;
         x = f4_unit_info(p, it * heads, ignored);
+        while (wlo >= Pu + x.tiles * heads) {
+          Pu += x.tiles * heads;
+          ++it;
+          x = f4_unit_info(p, it * heads, ignored);
+        }
+        const int h = sparse ? 0 : (wlo - Pu) / x.tiles;
+        u = it * heads + h;
+        x.h += h;
+        Pu += h * x.tiles;
       }
-      const int h = sparse ? 0 : (wlo - Pu) / x.tiles;
-      u = it * heads + h;
-      x.h += h;
-      Pu += h * x.tiles;
       j = wlo - Pu;
       enter_unit();
     }

@@ -67,6 +67,7 @@ struct Fp4Params {
   GqaParams g;
   const uint8_t *k, *v;
   float *o_head;               // [ctas][warps][G][128]
+  int32_t whole;               // CTA c has unit c, whole (the grid is the units)
 };
 
 // Which instantiation a call's score and mask modifications need: 0 none; 1
