@@ -546,8 +546,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     uint4 *qs = reinterpret_cast<uint4 *>(smem + C::oQ + warp * C::kQBytes) + lane;  // kQShared
     float oacc[NT][8][4];
     float m_neg[NT][2], l_part[NT][2];  // minus the weights' reference (log2 units), and their sums
-    bool no_ref[NT][2];
-    float sscale = p.score_scale, vmul = 1.f;
+    bool no_ref[NT][2];                 // (MOD > 0) no kept token of the row so far
+    float sscale = p.score_scale;
     const bool softcap = MOD >= 1 && p.softcap_l2 > 0.f;
     const bool mods = MOD == 2 && (p.mask_window != nullptr || p.alibi_slopes != nullptr);
     int trow[NT][2];
@@ -633,7 +633,6 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
         // a zero factor (uniform weights) as 2^-100: a finite score still weighs 1, and
         // an infinite one (a masked token's) 0
         if (sscale == 0.f) sscale = 0x1p-100f;
-        vmul = p.v_scale[h];
         if (MOD >= 1 && p.spec_mask != nullptr) {
           const uint32_t *mrow = p.spec_mask + (size_t)b * p.q_len;
 #pragma unroll
@@ -783,6 +782,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) raise = raise || no_ref[nt][0] || no_ref[nt][1];
         if (__builtin_expect(__any_sync(0xffffffffu, raise), 0)) {
+          const bool first = fresh;
           fresh = false;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -799,10 +799,11 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
               // while no score of the row is valid the reference is 0, with nothing to rescale
-              const float m_new = no_ref[nt][e] ? t : fmaxf(-m_neg[nt][e], t);
+              const bool none = MOD == 0 ? first : no_ref[nt][e];
+              const float m_new = none ? t : fmaxf(-m_neg[nt][e], t);
               const float mn = m_new == neg_inf() ? 0.f : m_new;
-              alpha[e] = no_ref[nt][e] ? 1.f : ex2(-m_neg[nt][e] - mn);
-              no_ref[nt][e] = m_new == neg_inf();
+              alpha[e] = none ? 1.f : ex2(-m_neg[nt][e] - mn);
+              if (MOD >= 1) no_ref[nt][e] = m_new == neg_inf();
               m_neg[nt][e] = -mn;
               l_part[nt][e] *= alpha[e];
             }
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
             const int g = nt * 8 + 2 * q4 + e;
             if (g < G) {
               const int64_t row = (int64_t)b * p.num_q_heads + h * G + g;
-              const float mul = l == 0.f ? 0.f : vmul / l;  // no valid token: 0; NaN goes through
+              const float mul = l == 0.f ? 0.f : p.v_scale[h] / l;  // no valid token: 0; NaN goes through
               uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD + 16 * r8);
 #pragma unroll
               for (int k = 0; k < 2; ++k)
