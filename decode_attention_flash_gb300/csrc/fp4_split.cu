@@ -896,6 +896,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
               n_seg = cut.owner(seg_P + seg_tiles - 1) - c_first + 1;
             }
             lead[tail ? warp : W] = make_int4(unit, bw | (goes_on ? 256 : 0), c_first, n_seg);
+            reinterpret_cast<float *>(smem + C::oSum)[(tail ? warp : W) * 32 + 16] = p.v_scale[h];
           }
         }
 #pragma unroll
@@ -917,10 +918,11 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           for (int e = 0; e < 2; ++e) {
             const int g = nt * 8 + 2 * q4 + e;
             if (g < G) {
+              // (float4 f of a row stands at f ^ (f >> 3 & 3): no bank conflicts either way)
               float4 *dst = reinterpret_cast<float4 *>(piece + g * kD + 16 * r8);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                dst[k] = make_float4(oacc[nt][2 * k][e], oacc[nt][2 * k][2 + e], oacc[nt][2 * k + 1][e],
+                dst[k ^ (r8 >> 1)] = make_float4(oacc[nt][2 * k][e], oacc[nt][2 * k][2 + e], oacc[nt][2 * k + 1][e],
                                      oacc[nt][2 * k + 1][2 + e]);
             }
           }
@@ -971,8 +973,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   auto stat_of = [&](const int4 &grp, int w) {
     return stat_all + (w * 2 + (w == (grp.y & 255) && (grp.y & 256) ? 1 : 0)) * 32;
   };
-  uint32_t groups = 0;
-  for (int k = 0; k <= W; ++k) groups |= lead[k].x >= 0 ? 1u << k : 0u;
+  const uint32_t groups = __ballot_sync(0xffffffffu, lane <= W && lead[min(lane, W)].x >= 0);
   const int ngroups = __popc(groups);
   auto group_at = [&](int i) {  // the i-th group
     uint32_t rest = groups;
@@ -1000,21 +1001,25 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     if (on && w <= (grp.y & 255)) st[g] = e;
     if (on && sub == 0) {
       const int b = grp.x / p.num_kv_heads, h = grp.x - b * p.num_kv_heads;
-      sums[k * 32 + g] = L == 0.f ? 0.f : p.v_scale[h] / L;
+      sums[k * 32 + g] = L == 0.f ? 0.f : sums[k * 32 + 16] / L;
       const float lse = L == 0.f ? neg_inf() : (M + __log2f(L)) * 0.69314718055994531f;
       if (grp.w > 0) p.lse_part[((int64_t)grp.x + cta) * G + g] = lse;
       else if (p.lse) p.lse[(int64_t)b * p.num_q_heads + h * G + g] = lse;
     }
   }
   __syncthreads();
-  for (int item = threadIdx.x; item < ngroups * nout; item += C::kThreads) {
-    const int k = group_at(item / nout);
+  // items (group, float4 o of its rows), thread by thread
+  uint32_t rest = groups;
+  for (int o = threadIdx.x;; o += C::kThreads) {
+    for (; rest != 0 && o >= nout; o -= nout) rest &= rest - 1;
+    if (rest == 0) break;
+    const int k = __ffs(rest) - 1;
     const int4 grp = lead[k];
-    const int o = item % nout, g = o / (kD / 4);
+    const int g = o / (kD / 4), f = o % (kD / 4), at = g * (kD / 4) + (f ^ ((f >> 3) & 3));
     const int a = k == W ? 0 : k, bw = grp.y & 255;
     const bool head = (grp.y & 256) != 0;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f), last = acc;
-    if (head) last = __ldcg(reinterpret_cast<const float4 *>(fp.o_head + ((int64_t)cta * W + bw) * G * kD) + o);
+    if (head) last = __ldcg(reinterpret_cast<const float4 *>(fp.o_head + ((int64_t)cta * W + bw) * G * kD) + at);
     auto add = [&](const float4 &v, float e) {
       if (e != 0.f) {  // a piece of weight 0 may hold anything
         acc.x += e * v.x;
@@ -1025,7 +1030,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     };
 #pragma unroll 4
     for (int w = a; w <= bw - (head ? 1 : 0); ++w)
-      add(reinterpret_cast<const float4 *>(smem + (size_t)w * C::kRingBytes)[o], stat_all[w * 64 + g]);
+      add(reinterpret_cast<const float4 *>(smem + (size_t)w * C::kRingBytes)[at], stat_all[w * 64 + g]);
     if (head) add(last, stat_all[bw * 64 + 32 + g]);
     const float mul = sums[k * 32 + g];
     acc.x *= mul;
