@@ -107,6 +107,8 @@ __device__ __forceinline__ RowAt row_at(const CacheRowParams &p, int64_t slot, i
 
 // One row of 128 elements, 8 per lane (lane l of 16: elements 8l .. 8l + 7, as bf16
 // pairs in `raw`), to `dst` (and its scale to `sdst`) in the cache's element kind:
+// (quotients as products with one fp32 reciprocal: eight divisions a lane took
+// longer than the copies)
 //   e4m3        code = e4m3(x / scale[h]), to nearest even, saturating
 //   e4m3, token shift = f16((max + min) / 2), scale = f16((max - min) / 2 / 448) (1
 //               when that is 0), code = e4m3((x - shift) / scale)
@@ -125,10 +127,10 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_
   const float x[8] = {bf_lo(raw.x), bf_hi(raw.x), bf_lo(raw.y), bf_hi(raw.y),
                       bf_lo(raw.z), bf_hi(raw.z), bf_lo(raw.w), bf_hi(raw.w)};
   if (KIND == kE4m3) {
-    const float s = head_scale;
+    const float inv = __frcp_rn(head_scale);
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = f32x2_to_e4m3x2(__fdiv_rn(x[2 * i], s), __fdiv_rn(x[2 * i + 1], s));
+    for (int i = 0; i < 4; ++i) w[i] = f32x2_to_e4m3x2(__fmul_rn(x[2 * i], inv), __fmul_rn(x[2 * i + 1], inv));
     if (on) *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     return;
   }
@@ -167,13 +169,13 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_
   const uint32_t shift = f16_bits(KIND == kInt4 ? lo : __fmul_rn(__fadd_rn(hi, lo), 0.5f));
   uint32_t scale = f16_bits(KIND == kInt4 ? __fdiv_rn(span, 15.f) : __fdiv_rn(__fmul_rn(span, 0.5f), 448.f));
   if (scale == 0) scale = 0x3C00u;
-  const float sc = f16_value(scale), sh = f16_value(shift);
+  const float inv = __frcp_rn(f16_value(scale)), sh = f16_value(shift);
   const int32_t word = (int32_t)(scale | (shift << 16));
   if (KIND == kE4m3Token) {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      w[i] = f32x2_to_e4m3x2(__fdiv_rn(__fsub_rn(x[2 * i], sh), sc), __fdiv_rn(__fsub_rn(x[2 * i + 1], sh), sc));
+      w[i] = f32x2_to_e4m3x2(__fmul_rn(__fsub_rn(x[2 * i], sh), inv), __fmul_rn(__fsub_rn(x[2 * i + 1], sh), inv));
     if (on) {
       *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
       if (l == 0) *reinterpret_cast<int32_t *>(sdst) = word;
@@ -182,7 +184,7 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float c = rintf(__fdiv_rn(__fsub_rn(x[i], sh), sc));
+      const float c = rintf(__fmul_rn(__fsub_rn(x[i], sh), inv));
       w |= (uint32_t)fminf(fmaxf(c, 0.f), 15.f) << (4 * i);
     }
     if (on) {
