@@ -274,6 +274,8 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const __grid_con
   constexpr int kHeads = 32 / kLanes;      // query heads a warp takes at once
   constexpr int kDeep = kAhead / 2;        // groups of them in flight
   const int lane = threadIdx.x & 31;
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = p.parts == 1 ? item : (int64_t)((uint32_t)item / (uint32_t)p.parts);
   const int part = (int)(item - t * p.parts);
@@ -487,6 +489,8 @@ __device__ __forceinline__ uint4 row_values(const RowBits &r, float head_scale) 
 template <int KIND>
 __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_constant__ CacheRowParams p) {
   const int lane = threadIdx.x & 31;
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int64_t t = item / p.parts;
   const int part = (int)(item - t * p.parts);
@@ -557,14 +561,13 @@ cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t 
   const int64_t blocks = blocks_for((int64_t)p.num_tokens * p.parts);
   const unsigned grid = (unsigned)blocks;
   switch (kind) {
-    case kBf16: append_kernel<kBf16, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kE4m3: append_kernel<kE4m3, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kE4m3Token: append_kernel<kE4m3Token, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kInt4: append_kernel<kInt4, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kFp4: append_kernel<kFp4, 128><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    default: append_kernel<kLatent, 64><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kBf16: return launch_dependent(append_kernel<kBf16, 128>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3: return launch_dependent(append_kernel<kE4m3, 128>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3Token: return launch_dependent(append_kernel<kE4m3Token, 128>, grid, kWarps * 32, 0, stream, p);
+    case kInt4: return launch_dependent(append_kernel<kInt4, 128>, grid, kWarps * 32, 0, stream, p);
+    case kFp4: return launch_dependent(append_kernel<kFp4, 128>, grid, kWarps * 32, 0, stream, p);
+    default: return launch_dependent(append_kernel<kLatent, 64>, grid, kWarps * 32, 0, stream, p);
   }
-  return cudaGetLastError();
 }
 
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
@@ -572,14 +575,13 @@ cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t 
   p.parts = kind == kLatent ? 1 : parts_for(p.num_tokens, 2 * ((p.num_kv_heads + 1) / 2), num_sms);
   const unsigned grid = (unsigned)blocks_for((int64_t)p.num_tokens * p.parts);
   switch (kind) {
-    case kBf16: gather_kernel<kBf16><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kE4m3: gather_kernel<kE4m3><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kE4m3Token: gather_kernel<kE4m3Token><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kInt4: gather_kernel<kInt4><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    case kFp4: gather_kernel<kFp4><<<grid, kWarps * 32, 0, stream>>>(p); break;
-    default: gather_kernel<kLatent><<<grid, kWarps * 32, 0, stream>>>(p); break;
+    case kBf16: return launch_dependent(gather_kernel<kBf16>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3: return launch_dependent(gather_kernel<kE4m3>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3Token: return launch_dependent(gather_kernel<kE4m3Token>, grid, kWarps * 32, 0, stream, p);
+    case kInt4: return launch_dependent(gather_kernel<kInt4>, grid, kWarps * 32, 0, stream, p);
+    case kFp4: return launch_dependent(gather_kernel<kFp4>, grid, kWarps * 32, 0, stream, p);
+    default: return launch_dependent(gather_kernel<kLatent>, grid, kWarps * 32, 0, stream, p);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace da

@@ -230,6 +230,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
   const int cta = blockIdx.x;
   uint32_t dev_err = 0;
 
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   if (threadIdx.x == 0) {
     if (p.paged) prefetch_share_l2(p.block_table, (int64_t)p.batch * p.max_pages * 4);
     flags[0] = 0;
@@ -1125,7 +1127,8 @@ cudaError_t fp4_prepare() {
 
 cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream) {
   const int mod = gqa_mod(p.g);
-#define DA_F4(NT, M) fp4_split_kernel<NT, M><<<ctas, F4<NT>::kThreads, F4<NT>::kTotal, stream>>>(p)
+#define DA_F4(NT, M) \
+  return launch_dependent(fp4_split_kernel<NT, M>, (unsigned)ctas, F4<NT>::kThreads, F4<NT>::kTotal, stream, p)
   if (p.g.group <= 8) {
     if (mod == 0) DA_F4(1, 0);
     else if (mod == 1) DA_F4(1, 1);
@@ -1136,7 +1139,6 @@ cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream) {
     else DA_F4(2, 2);
   }
 #undef DA_F4
-  return cudaGetLastError();
 }
 
 }  // namespace da

@@ -156,6 +156,26 @@ struct TableParams {
   int32_t paged, in_place;     // in_place: an output overlaps an input that every block reads
 };
 
+// Launches a kernel that begins with wait_for_previous_kernel (ptx.cuh), so that its
+// blocks may take their places while the stream's previous kernel drains: a
+// launch after another one of ours costs about 1.5 us less. Ordering is that of the
+// stream, as for any launch, also in captured graphs.
+template <typename... Params, typename... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem,
+                             cudaStream_t stream, const Args &...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 // Kernel launchers (return the launch error).
 cudaError_t gqa_prepare(int device);  // sets shared-memory attributes once per device
 int gqa_smem_bytes(bool fp8, int group, bool token_scale, bool int4);

@@ -76,6 +76,14 @@ __device__ __forceinline__ uint32_t ld_acquire_cta(const uint32_t *p) {
   return v;
 }
 
+// ---------------------------------------------------------------- dependent launches
+// Kernels launched with launch_dependent (internal.h) may start while the previous
+// kernel of the stream is still running: nothing that it may have written is read,
+// and nothing at all is written, before this returns.
+__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream start its blocks (they wait as above).
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- cp.async
 
 // 4-byte asynchronous copy global -> shared (one table entry); each thread's

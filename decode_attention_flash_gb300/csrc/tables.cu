@@ -64,6 +64,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
   uint32_t err = 0;
+  wait_for_previous_kernel();
+  let_next_kernel_start();
   int64_t nf = 0;
   if (p.free_pages) {
     nf = *p.num_free;
@@ -227,8 +229,7 @@ cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream
   int64_t blocks = (p.slot_capacity + kThreads - 1) / kThreads;
   if (blocks < 1) blocks = 1;
   if (blocks > num_sms) blocks = num_sms;
-  tables_kernel<<<(unsigned)blocks, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(tables_kernel, (unsigned)blocks, kThreads, 0, stream, p);
 }
 
 }  // namespace da
