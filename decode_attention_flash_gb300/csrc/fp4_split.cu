@@ -232,8 +232,9 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
 
   wait_for_previous_kernel();
   let_next_kernel_start();
+  if (threadIdx.x == W * 32 && p.paged)  // (a warp that has no lengths to wait for)
+    prefetch_share_l2(p.block_table, (int64_t)p.batch * p.max_pages * 4);
   if (threadIdx.x == 0) {
-    if (p.paged) prefetch_share_l2(p.block_table, (int64_t)p.batch * p.max_pages * 4);
     flags[0] = 0;
     flags[24] = flags[28] = -1;
   }
