@@ -10,33 +10,46 @@
 // with the query group as the MMA's N dimension.
 //
 // What bounds it. 16 tokens of one kv head are 2304 bytes and 4096 elements to
-// turn into f16. The e2m1 conversion runs at half rate (2 cycles a warp for a
-// pair per lane, measured), an m16n8k16 takes 8.5 cycles of a scheduler, and every
-// pair takes a multiply by its block's scale: about 320 issue cycles per 16
-// tokens and scheduler, against 392 that the measured copy bandwidth leaves. So
-// the kernel is laid out to add as little as possible to that:
+// turn into f16. Measured per scheduler: an e2m1 conversion (a pair a lane) takes 2
+// cycles of the ALU, a multiply by the block's scale 2 of the FMA pipe, an m16n8k16
+// 8.2; 64 + 64 + 16 of them, with what they hold up of each other, take 322 cycles for
+// 16 tokens, against 412 that the measured copy bandwidth leaves. So the kernel is
+// laid out to add as little as possible to that (291 instructions for 16 tokens in
+// all, 211 of them the above):
 //  - every warp streams alone: its own ring of 32-token stages, filled by its own
 //    16-byte asynchronous copies of whole granules (16 rows, 1152 bytes), and no
 //    barrier between warps until the end. (Bulk copies, one lane each, cost about 12
 //    instructions a copy: their operands are warp-uniform.) What a tile is -- its pages,
-//    its valid tokens, its addresses -- one further warp works out for all of them, a
-//    lane for each;
+//    its valid tokens, its addresses -- one further warp, the walker, works out for all
+//    of them, a lane for each (in the streaming warps that was 45 instructions more);
 //  - K: lane (r, q) of a quad takes bytes 16q..16q+15 of row r as one 16-byte load:
 //    the contraction's order is free, so these are its A fragments of all eight
 //    k-steps (Q is read in the same order), within two blocks, two scales;
 //  - V: a lane takes bytes 8r..8r+7 (one block) of its four tokens; two shifts and
 //    two bit selects interleave the nibbles of a token pair so that one
 //    conversion gives the (token, token + 1) pair of a V^T fragment;
-//  - the running maximum is only raised when a score passes it by 2^8 (one
-//    warp vote per stage; P <= 2^8 in f16, sums in fp32), so a stage usually
-//    needs no shuffle and no rescaling of O.
+//  - the weights' reference is raised only when a sum of weights passes 2^10 (one
+//    warp vote per stage; the weights, at most 2^10, meet V as f16, which keeps 11 bits
+//    of each where V has 6; their sums are fp32), so a stage usually needs no shuffle
+//    and no rescaling of O;
+//  - no branch inside a stage: both granules are always computed, word by word in
+//    turn, and what a half that was not copied holds is masked (131 -> 119 us for 32
+//    rows of 16384 tokens).
+// Long rows stream at 90 % of the copy rate (32 rows of 16384 tokens, 8 kv heads:
+// 117 us, floor 89). A call of 32 rows of 1024..8192 takes 42 us, floor 22.7: 2 us
+// until the schedule stands, 2 until the first tile, 28 of stream, 4 in which the
+// warps end one after another, 2 for the pieces of a CTA and 4 for units that CTAs
+// share. Measured and not kept: 16 streaming warps with a register split (more
+// instructions: 42.0 -> 45.4 us), shares weighted by scheduler (115 -> 124 us), the walk
+// and the end as functions of their own (42.1 -> 45.5 us).
 //
 // The split. As in gqa_split.cuh the tiles of all (row, kv head) units are laid
 // end to end and cut into equal ranges, one per CTA; a CTA's range is cut again
 // into one range per warp. A unit inside one warp's range is written from its
 // registers; pieces of a unit shared by warps meet in shared memory after the
 // stream, and pieces shared by CTAs in global memory (counted and merged as in
-// gqa_split.cuh, without any CTA waiting for another).
+// gqa_split.cuh, without any CTA waiting for another). Small calls give a CTA to every
+// unit instead (plan.cpp): no scan, no merge between CTAs.
 #include "gqa_split.cuh"
 
 namespace da {
@@ -53,7 +66,7 @@ constexpr float kRaise = 1024.f;     // a sum of weights past this raises their 
 template <int NT>
 struct F4 {
   static constexpr int kWarps = NT == 1 ? 15 : 11;               // consumers: with the walker four (three) a scheduler
-  static constexpr int kThreads = (kWarps + 1) * 32;             // and the producer warp
+  static constexpr int kThreads = (kWarps + 1) * 32;             // and the walker
   static constexpr int kStages = 3;
   // Q^T fragments: registers for up to eight rows; for sixteen, whose O takes 64
   // registers a thread, shared memory (16 bytes a lane and k-step): 16 rows x 4 query
@@ -202,7 +215,8 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
   }
   if (tid == 0) p.counters[unit] = 0u;  // ready for the next call
 }
-constexpr int kOneLevel = 32;  // pieces that f4_merge takes; a unit of more is merged in two levels
+constexpr int kOneLevel = 32;  // pieces that f4_merge takes (a lane's worth); a unit of more is merged in
+                               // two levels, as in gqa_split.cuh
 
 template <int NT, int MOD>
 __global__ void __launch_bounds__(F4<NT>::kThreads, 1)

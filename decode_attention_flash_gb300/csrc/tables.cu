@@ -13,6 +13,8 @@
 // block scans of a few thousand integers from L2) and then writes its own share of
 // the tokens, of the new table entries and (block 0) of the per-row results;
 // a token finds its row by bisecting the scan, kept per thread in shared memory.
+// 256 rows of one token: 4.9 us, a launch and three dependent loads; 125 000 tokens of
+// 61 rows: 7.9 us (four tokens a thread in fewer blocks: 9.8).
 // Results written over the lengths they came from wait for the block that is last
 // to have read them (a counter in the workspace, back at zero afterwards).
 #include "internal.h"

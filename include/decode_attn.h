@@ -136,7 +136,7 @@ typedef struct {
   int32_t max_pages_per_seq;
   int32_t num_pages;
   da_dtype q_dtype;           /* DA_DTYPE_BF16 only */
-  da_dtype kv_dtype;          /* bf16, or (GQA) e4m3 with per-head or per-token scales */
+  da_dtype kv_dtype;          /* bf16; GQA also any other da_dtype */
   int32_t sparse_block_size;
   int32_t max_sparse_blocks;
   int32_t q_len;              /* query tokens per row; 0 or 1 = one */
@@ -376,8 +376,11 @@ da_status decode_attn_get_error_noalloc(da_ctx *ctx, da_stream_t stream, uint32_
  * The cache around the decode: tables from request lengths, rows written, rows
  * read back. The three calls below take a planned context for the cache's layout
  * and element kind, and its workspace (its first 256 bytes: the error word that
- * decode_attn_get_error reads, and a counter). They only enqueue one kernel on
- * `stream`. A slot is one position of the cache: page * page_size + offset, or
+ * decode_attn_get_error reads, and a counter of decode_attn_build_tables: two of
+ * those that overlap on the GPU need workspaces of their own; appends and gathers may
+ * share one with anything). They only enqueue one kernel on `stream`, which may take
+ * its place on the SMs while the stream's previous kernel drains, but reads and writes
+ * nothing before that has ended. A slot is one position of the cache: page * page_size + offset, or
  * batch row * max_seq_len + position in a contiguous cache.
  */
 
@@ -485,7 +488,8 @@ typedef struct {
  * Turns the queries and the new keys by their positions and writes keys and
  * values into the cache's rows `slot_map`, in its element kind. With cos and sin
  * c, s of pair (a, b): (a c - b s, b c + a s), each product and sum rounded to fp32,
- * then to bf16; that bf16 key is what a quantised cache quantises:
+ * then to bf16; that bf16 key is what a quantised cache quantises (quotients are fp32
+ * products with the fp32 reciprocal; per-head scales are positive):
  *   e4m3         e4m3(x / scale[h]), round to nearest even, saturating
  *   e4m3, token  shift = f16((max + min) / 2), scale = f16((max - min) / 2 / 448) of the
  *                row, 1 when that is 0; e4m3((x - shift) / scale)
