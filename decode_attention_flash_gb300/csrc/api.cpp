@@ -8,7 +8,7 @@
 #include <mutex>
 #include <new>
 
-#include "internal.h"
+#include "cache_ops.h"
 
 struct da_ctx {
   da_problem prob;

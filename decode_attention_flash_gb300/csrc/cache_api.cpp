@@ -4,7 +4,7 @@
 #include <algorithm>
 #include <cstring>
 
-#include "internal.h"
+#include "cache_ops.h"
 
 namespace da {
 // (defined beside the context in api.cpp)

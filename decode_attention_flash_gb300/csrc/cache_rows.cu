@@ -26,8 +26,8 @@
 // bound by instruction issue at 77 %).
 #include <cuda_fp16.h>
 
-#include "internal.h"
-#include "ptx.cuh"
+#include "cache_ops.h"
+#include "cache_ptx.cuh"
 
 namespace da {
 namespace {

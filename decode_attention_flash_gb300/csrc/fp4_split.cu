@@ -51,6 +51,8 @@
 // stream, and pieces shared by CTAs in global memory (counted and merged as in
 // gqa_split.cuh, without any CTA waiting for another). Small calls give a CTA to every
 // unit instead (plan.cpp): no scan, no merge between CTAs.
+#include "cache_ops.h"
+#include "cache_ptx.cuh"
 #include "gqa_split.cuh"
 
 namespace da {

@@ -13,7 +13,7 @@
 #include <cstring>
 #include <vector>
 
-#include "internal.h"
+#include "cache_ops.h"
 
 namespace da {
 

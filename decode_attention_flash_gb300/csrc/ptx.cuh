@@ -66,37 +66,12 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t *bar, uint32_t parity
   }
 }
 
-// A shared-memory word that one warp writes and another reads (release / acquire in the block).
-__device__ __forceinline__ void st_release_cta(uint32_t *p, uint32_t v) {
-  asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
-}
-__device__ __forceinline__ uint32_t ld_acquire_cta(const uint32_t *p) {
-  uint32_t v;
-  asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
-  return v;
-}
-
-// ---------------------------------------------------------------- dependent launches
-// Kernels launched with launch_dependent (internal.h) may start while the previous
-// kernel of the stream is still running: nothing that it may have written is read,
-// and nothing at all is written, before this returns.
-__device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel of the stream start its blocks (they wait as above).
-__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // ---------------------------------------------------------------- cp.async
 
 // 4-byte asynchronous copy global -> shared (one table entry); each thread's
 // copies are grouped by cp_async_commit and awaited by cp_async_wait_group<N>.
 __device__ __forceinline__ void cp_async_4(void *smem_dst, const void *gsrc) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(smem_dst)),
-               "l"(reinterpret_cast<uint64_t>(gsrc))
-               : "memory");
-}
-
-// 16 bytes to the shared address `smem_dst` (both sides 16-byte aligned), past L1.
-__device__ __forceinline__ void cp_async_16(uint32_t smem_dst, const void *gsrc) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_dst),
                "l"(reinterpret_cast<uint64_t>(gsrc))
                : "memory");
 }

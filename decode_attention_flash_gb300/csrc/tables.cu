@@ -17,8 +17,8 @@
 // 61 rows: 7.9 us (four tokens a thread in fewer blocks: 9.8).
 // Results written over the lengths they came from wait for the block that is last
 // to have read them (a counter in the workspace, back at zero afterwards).
-#include "internal.h"
-#include "ptx.cuh"
+#include "cache_ops.h"
+#include "cache_ptx.cuh"
 
 namespace da {
 namespace {
