@@ -22,8 +22,9 @@
 // instead kept fewer warps on an SM: 33.9 -> 43.5 us for the e4m3 rows below.)
 // Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 65 us, 93 % of the
 // copy rate; 4099 tokens of 64 + 16 heads into e4m3 with token scales: 31.6 us (75 %, two
-// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 61.5 us (83 %,
-// bound by instruction issue at 77 %).
+// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 56.2 us (90 %;
+// one row in flight of K and of V instead of two: 70.7, four: 56.6; K first and then V,
+// with a head's address worked out for each row: 61.3, bound by instruction issue).
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -33,7 +34,8 @@ namespace da {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kAhead = 4;
+constexpr int kAhead = 4;  // loads in flight a lane (append)
+constexpr int kSide = 2;   // rows of K, and as many of V (gather)
 
 enum Kind { kBf16 = 0, kE4m3 = 1, kE4m3Token = 2, kInt4 = 3, kFp4 = 4, kLatent = 5 };
 
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
   wait_for_previous_kernel();
   let_next_kernel_start();
   const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int64_t t = item / p.parts;
+  const int64_t t = p.parts == 1 ? item : (int64_t)((uint32_t)item / (uint32_t)p.parts);
   const int part = (int)(item - t * p.parts);
   if (t >= p.num_tokens) return;
   uint32_t err = 0;
@@ -518,29 +520,43 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
   }
   const int l = lane & 15, sub = lane >> 4;
   const RowAt at = row_at<KIND>(p, slot, l);
-  // heads two at once, of K and then of V; kAhead loads in flight
+  // heads two at once, of K and of V side by side, pointers a stride on; kSide rows of
+  // each in flight
   const int HK = p.num_kv_heads, nk = (HK + 1) / 2;
-  const int g0 = (int)((uint32_t)(part * 2 * nk) / (uint32_t)p.parts);
-  const int g1 = (int)((uint32_t)((part + 1) * 2 * nk) / (uint32_t)p.parts);
-  uint4 *ko = reinterpret_cast<uint4 *>(p.k_out) + t * HK * 16 + l, *vo = reinterpret_cast<uint4 *>(p.v_out) + t * HK * 16 + l;
-  for (int g = g0; g < g1; g += kAhead) {
-    RowBits r[kAhead];
-    float hs[kAhead];
+  const int g0 = (int)((uint32_t)(part * nk) / (uint32_t)p.parts);
+  const int g1 = (int)((uint32_t)((part + 1) * nk) / (uint32_t)p.parts);
+  int h = 2 * g0 + sub;
+  const uint8_t *k = at.k + h * at.head, *v = at.v + h * at.head;
+  const uint8_t *ks = at.ks + h * at.shead, *vs = at.vs + h * at.shead;
+  const int64_t step = 2 * at.head, sstep = 2 * at.shead;
+  uint4 *ko = reinterpret_cast<uint4 *>(p.k_out) + (t * HK + h) * 16 + l;
+  uint4 *vo = reinterpret_cast<uint4 *>(p.v_out) + (t * HK + h) * 16 + l;
+  for (int g = g0; g < g1; g += kSide) {
+    RowBits rk[kSide], rv[kSide];
+    float sk[kSide], sv[kSide];
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const bool is_v = g + k >= nk;
-      const int h = (g + k - (is_v ? nk : 0)) * 2 + sub;
-      if (g + k < g1 && h < HK) {
-        r[k] = get_row<KIND>((is_v ? at.v : at.k) + h * at.head, (is_v ? at.vs : at.ks) + h * at.shead);
-        if (KIND == kE4m3 || KIND == kFp4) hs[k] = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+    for (int i = 0; i < kSide; ++i)
+      if (g + i < g1 && h + 2 * i < HK) {
+        rk[i] = get_row<KIND>(k, ks);
+        rv[i] = get_row<KIND>(v, vs);
+        if (KIND == kE4m3 || KIND == kFp4) {
+          sk[i] = __ldg(p.k_scale + h + 2 * i);
+          sv[i] = __ldg(p.v_scale + h + 2 * i);
+        }
+        k += step;
+        v += step;
+        ks += sstep;
+        vs += sstep;
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const bool is_v = g + k >= nk;
-      const int h = (g + k - (is_v ? nk : 0)) * 2 + sub;
-      if (g + k < g1 && h < HK) (is_v ? vo : ko)[h * 16] = row_values<KIND>(r[k], hs[k]);
-    }
+    for (int i = 0; i < kSide; ++i)
+      if (g + i < g1 && h + 2 * i < HK) {
+        ko[32 * i] = row_values<KIND>(rk[i], sk[i]);
+        vo[32 * i] = row_values<KIND>(rv[i], sv[i]);
+      }
+    h += 2 * kSide;
+    ko += 32 * kSide;
+    vo += 32 * kSide;
   }
 }
 
@@ -578,7 +594,7 @@ cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t 
 
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  p.parts = kind == kLatent ? 1 : parts_for(p.num_tokens, 2 * ((p.num_kv_heads + 1) / 2), num_sms);
+  p.parts = kind == kLatent ? 1 : parts_for(p.num_tokens, (p.num_kv_heads + 1) / 2, num_sms);
   const unsigned grid = (unsigned)blocks_for((int64_t)p.num_tokens * p.parts);
   switch (kind) {
     case kBf16: return launch_dependent(gather_kernel<kBf16>, grid, kWarps * 32, 0, stream, p);
