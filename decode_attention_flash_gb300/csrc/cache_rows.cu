@@ -17,14 +17,17 @@
 // heads of the latent cache), nothing is exchanged, and the cosines and sines of its
 // pairs stay in registers for all heads of the token. Keys and values: 16 lanes of 8
 // elements a head, as the element kinds want them (block maxima are shuffles of 2, 4
-// or 16 lanes), a key's halves exchanged by shuffles. Addresses advance by a head's
-// stride; kAhead loads are in flight. (A token staged in shared memory by bulk copies
-// instead kept fewer warps on an SM: 33.9 -> 43.5 us for the e4m3 rows below.)
-// Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 65 us, 93 % of the
-// copy rate; 4099 tokens of 64 + 16 heads into e4m3 with token scales: 31.6 us (75 %, two
-// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 56.2 us (90 %;
-// one row in flight of K and of V instead of two: 70.7, four: 56.6; K first and then V,
-// with a head's address worked out for each row: 61.3, bound by instruction issue).
+// or 16 lanes), a key's halves exchanged by shuffles, K and V side by side, pointers that
+// advance by a head's stride; kAhead or 2 kSide loads are in flight. (A token staged in
+// shared memory by bulk copies instead kept fewer warps on an SM: 33.9 -> 43.5 us for the
+// e4m3 rows below; its first keys and values loaded before its queries are stored: 30.4
+// -> 32.8.)
+// Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 62.7 us, 97 % of the
+// copy rate; 4099 tokens of 64 + 16 heads into e4m3 with token scales: 30.4 us (77 %, two
+// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 56.2 us (90 %).
+// K first and then V, with a head's address worked out for each row: 65.2, 31.4 and
+// 61.3 us, bound by instruction issue; one row in flight of K and of V instead of two:
+// 65.2, 31.0 and 70.7.
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -34,8 +37,8 @@ namespace da {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kAhead = 4;  // loads in flight a lane (append)
-constexpr int kSide = 2;   // rows of K, and as many of V (gather)
+constexpr int kAhead = 4;  // loads of queries in flight a lane
+constexpr int kSide = 2;   // rows of K, and as many of V, in flight
 
 enum Kind { kBf16 = 0, kE4m3 = 1, kE4m3Token = 2, kInt4 = 3, kFp4 = 4, kLatent = 5 };
 
@@ -288,9 +291,9 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const __grid_con
   const int part = (int)(item - t * p.parts);
   if (t >= p.num_tokens) return;
   const int HQ = p.q ? p.num_q_heads : 0, HK = p.k_new ? p.num_kv_heads : 0;
-  // groups: queries kHeads at a time, then (not the latent cache) keys and values two at a time
+  // groups: queries kHeads at a time, then (not the latent cache) keys and values of two heads
   const int nq = (HQ + kHeads - 1) / kHeads, nk = KIND == kLatent ? 0 : (HK + 1) / 2;
-  const int groups = nq + 2 * nk;
+  const int groups = nq + nk;
   const int g0 = (int)((uint32_t)(part * groups) / (uint32_t)p.parts);
   const int g1 = (int)((uint32_t)((part + 1) * groups) / (uint32_t)p.parts);
 
@@ -378,7 +381,7 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const __grid_con
     const int partner = lane - kl + (kturned && !p.rope_adjacent ? (second ? kl - r : kl + r) : kl);
     const RowAt at = row_at<KIND>(p, slot, kl);
     const int first = max(g0, nq);
-    if (first < nq + nk && r > 0) {  // some key is this warp's
+    if (r > 0) {
       if (kturned) {
         if (p.rope_adjacent) load_turn<4>(p, t, 4 * kl, c, s);
         else load_turn<8>(p, t, 8 * (second ? kl - r : kl), c, s);
@@ -387,46 +390,58 @@ __global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = -s[i];
     }
-    const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + kl;
-    const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride) + kl;
-    for (int g = first; g < g1; g += kAhead) {
-      uint4 w[kAhead];
-      float hs[kAhead];
+    int h = 2 * (first - nq) + ksub;
+    const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + h * 16 + kl;
+    const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride) + h * 16 + kl;
+    uint8_t *kd = at.k + h * at.head, *vd = at.v + h * at.head;
+    uint8_t *ks = at.ks + h * at.shead, *vs = at.vs + h * at.shead;
+    for (int g = first; g < g1; g += kSide) {
+      uint4 w[kSide], u[kSide];
+      float sk[kSide], sv[kSide];
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        const bool is_v = g + k >= nq + nk;
-        const int h = (g + k - nq - (is_v ? nk : 0)) * 2 + ksub;
-        w[k] = make_uint4(0u, 0u, 0u, 0u);
-        hs[k] = 1.f;
-        if (g + k < g1 && h < HK) {
-          w[k] = __ldg((is_v ? vsrc : ksrc) + h * 16);
-          if (KIND == kE4m3 || KIND == kFp4) hs[k] = __ldg((is_v ? p.v_scale : p.k_scale) + h);
+      for (int i = 0; i < kSide; ++i) {
+        w[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
+        sk[i] = sv[i] = 1.f;
+        if (g + i < g1 && h + 2 * i < HK) {
+          w[i] = __ldg(ksrc + 32 * i);
+          u[i] = __ldg(vsrc + 32 * i);
+          if (KIND == kE4m3 || KIND == kFp4) {
+            sk[i] = __ldg(p.k_scale + h + 2 * i);
+            sv[i] = __ldg(p.v_scale + h + 2 * i);
+          }
         }
       }
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k) {
-        if (g + k >= g1) break;
-        const bool is_v = g + k >= nq + nk;
-        const int h = (g + k - nq - (is_v ? nk : 0)) * 2 + ksub;
-        if (!is_v && r > 0) {
+      for (int i = 0; i < kSide; ++i) {
+        if (g + i >= g1) break;
+        if (r > 0) {
           if (p.rope_adjacent) {
-            if (kturned) turn_adjacent(w[k], c, s, 0);
+            if (kturned) turn_adjacent(w[i], c, s, 0);
           } else {
-            const uint4 z = make_uint4(__shfl_sync(0xffffffffu, w[k].x, partner), __shfl_sync(0xffffffffu, w[k].y, partner),
-                                       __shfl_sync(0xffffffffu, w[k].z, partner), __shfl_sync(0xffffffffu, w[k].w, partner));
+            const uint4 z = make_uint4(__shfl_sync(0xffffffffu, w[i].x, partner), __shfl_sync(0xffffffffu, w[i].y, partner),
+                                       __shfl_sync(0xffffffffu, w[i].z, partner), __shfl_sync(0xffffffffu, w[i].w, partner));
             if (kturned) {
-              uint32_t x[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-              const uint32_t u[4] = {z.x, z.y, z.z, z.w};
+              uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+              const uint32_t y[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                x[i] = pack_bf16(__fsub_rn(__fmul_rn(bf_lo(x[i]), c[2 * i]), __fmul_rn(bf_lo(u[i]), s[2 * i])),
-                                 __fsub_rn(__fmul_rn(bf_hi(x[i]), c[2 * i + 1]), __fmul_rn(bf_hi(u[i]), s[2 * i + 1])));
-              w[k] = make_uint4(x[0], x[1], x[2], x[3]);
+              for (int j = 0; j < 4; ++j)
+                x[j] = pack_bf16(__fsub_rn(__fmul_rn(bf_lo(x[j]), c[2 * j]), __fmul_rn(bf_lo(y[j]), s[2 * j])),
+                                 __fsub_rn(__fmul_rn(bf_hi(x[j]), c[2 * j + 1]), __fmul_rn(bf_hi(y[j]), s[2 * j + 1])));
+              w[i] = make_uint4(x[0], x[1], x[2], x[3]);
             }
           }
         }
-        put_row<KIND>(p, h < HK, (is_v ? at.v : at.k) + h * at.head, (is_v ? at.vs : at.ks) + h * at.shead, hs[k], kl, w[k]);
+        const bool mine = h + 2 * i < HK;
+        put_row<KIND>(p, mine, kd, ks, sk[i], kl, w[i]);
+        put_row<KIND>(p, mine, vd, vs, sv[i], kl, u[i]);
+        kd += 2 * at.head;
+        vd += 2 * at.head;
+        ks += 2 * at.shead;
+        vs += 2 * at.shead;
       }
+      h += 2 * kSide;
+      ksrc += 32 * kSide;
+      vsrc += 32 * kSide;
     }
   }
 }
@@ -578,7 +593,7 @@ cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t 
   if (!p.q && !p.k_new) return cudaSuccess;
   const int per = kind == kLatent ? 8 : 4;
   const int groups = (p.q ? (p.num_q_heads + per - 1) / per : 0) +
-                     (p.k_new && kind != kLatent ? 2 * ((p.num_kv_heads + 1) / 2) : 0);
+                     (p.k_new && kind != kLatent ? (p.num_kv_heads + 1) / 2 : 0);
   p.parts = parts_for(p.num_tokens, groups < 1 ? 1 : groups, num_sms);
   const int64_t blocks = blocks_for((int64_t)p.num_tokens * p.parts);
   const unsigned grid = (unsigned)blocks;
