@@ -22,9 +22,11 @@
 // shared memory by bulk copies instead kept fewer warps on an SM: 33.9 -> 43.5 us for the
 // e4m3 rows below; its first keys and values loaded before its queries are stored: 30.4
 // -> 32.8.)
-// Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 62.7 us, 97 % of the
-// copy rate; 4099 tokens of 64 + 16 heads into e4m3 with token scales: 30.4 us (77 %, two
-// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 56.2 us (90 %).
+// Blocks of four warps leave an SM sooner than blocks of eight, so a last wave ends sooner
+// (eight: 62.7, 30.4 and 56.3 us for the three below, two: 62.7, 31.3 and 55.3).
+// Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 62.2 us, 98 % of the
+// copy rate; 4099 tokens of 64 + 16 heads into e4m3 with token scales: 29.7 us (79 %, two
+// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 54.9 us (93 %).
 // K first and then V, with a head's address worked out for each row: 65.2, 31.4 and
 // 61.3 us, bound by instruction issue; one row in flight of K and of V instead of two:
 // 65.2, 31.0 and 70.7.
@@ -36,7 +38,7 @@
 namespace da {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4;
 constexpr int kAhead = 4;  // loads of queries in flight a lane
 constexpr int kSide = 2;   // rows of K, and as many of V, in flight
 
@@ -278,7 +280,7 @@ __device__ __forceinline__ void turn_adjacent(uint4 &v, const float (&c)[8], con
 
 // HEAD: elements of a rotated head, 128 (the latent cache: 64).
 template <int KIND, int HEAD>
-__global__ void __launch_bounds__(kWarps * 32, 4) append_kernel(const __grid_constant__ CacheRowParams p) {
+__global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_constant__ CacheRowParams p) {
   constexpr int kChunks = HEAD / 8;        // 16-byte chunks of a head
   constexpr int kLanes = kChunks / 2;      // lanes of a head with both halves of its pairs
   constexpr int kHeads = 32 / kLanes;      // query heads a warp takes at once
