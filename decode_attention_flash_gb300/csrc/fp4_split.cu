@@ -29,10 +29,11 @@
 //  - V: a lane takes bytes 8r..8r+7 (one block) of its four tokens; two shifts and
 //    two bit selects interleave the nibbles of a token pair so that one
 //    conversion gives the (token, token + 1) pair of a V^T fragment;
-//  - the weights' reference is raised only when a sum of weights passes 2^10 (one
-//    warp vote per stage; the weights, at most 2^10, meet V as f16, which keeps 11 bits
-//    of each where V has 6; their sums are fp32), so a stage usually needs no shuffle
-//    and no rescaling of O;
+//  - the weights' reference, set 5 octaves below the greatest score, is raised only when a
+//    sum of weights passes 2^15 (one warp vote per stage; the weights, at most 2^15, meet V
+//    as f16, which keeps 11 bits of each where V has 6 and 2^-24 of the reference, 2^-29 of
+//    the greatest weight, as its smallest step; their sums are fp32), so a stage usually
+//    needs no shuffle and no rescaling of O;
 //  - no branch inside a stage: both granules are always computed, word by word in
 //    turn, and what a half that was not copied holds is masked (131 -> 119 us for 32
 //    rows of 16384 tokens).
@@ -64,7 +65,8 @@ constexpr int kGranBytes = 1152;     // 16 x 64 code bytes, then 16 x 8 scale by
 constexpr int kScaleOff = 1024;
 constexpr int kQueue = 8;             // described tiles a warp may have waiting or in its ring
 constexpr int kStageBytes = 2 * (kT / kGran) * kGranBytes;  // K granules, then V granules
-constexpr float kRaise = 1024.f;     // a sum of weights past this raises their reference
+constexpr float kRoom = 5.f;         // octaves from the weights' reference up to the greatest score so far
+constexpr float kRaise = 32768.f;    // a sum of weights past this raises the reference
 
 template <int NT>
 struct F4 {
@@ -778,7 +780,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           __syncwarp();
         }
         // The weights 2^(x - m) against the held reference m, and their sums. The
-        // reference is raised only when a sum passes 2^10 (so no weight does, and
+        // reference is raised only when a sum passes 2^15 (so no weight does, and
         // f16 holds them all; the sums are fp32), or when there is none yet.
         float y[NT][2][4], sum[NT][2];
         bool raise = fresh;
@@ -820,7 +822,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
               t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
               // while no score of the row is valid the reference is 0, with nothing to rescale
               const bool none = MOD == 0 ? first : no_ref[nt][e];
-              const float m_new = none ? t : fmaxf(-m_neg[nt][e], t);
+              const float m_new = none ? t - kRoom : fmaxf(-m_neg[nt][e], t - kRoom);
               const float mn = m_new == neg_inf() ? 0.f : m_new;
               alpha[e] = none ? 1.f : ex2(-m_neg[nt][e] - mn);
               if (MOD >= 1) no_ref[nt][e] = m_new == neg_inf();

@@ -2,6 +2,8 @@
 GPU, against a plain definition in 64 bits. The tolerances are the sums of the
 roundings that the kernel makes (tests/fp4_ref.py, attend_row)."""
 
+import math
+
 import pytest
 import torch
 
@@ -246,3 +248,31 @@ def test_stalled_wait_reports_timeout_then_the_context_recovers():
     out, lse = run(eng, t)
     assert eng.errors() == 0
     R.check(out, lse, R.reference(t, SCALE, hq=8, hkv=2, page=16))
+
+
+def test_one_great_weight_before_many_small_ones():
+    """The first token weighs 2^24 / 1.49 times every other: f16 alone would take each of the
+    others for 2/3 of its weight. More units than warps, so a warp sees a row in one piece; the
+    rows share their pages. The bound, as in fp4_ref: bf16 2^-8, f16 weights 2^-11 (2^-25 of the
+    reference for the smallest, which is 2^-5 of the greatest), the weight's own error."""
+    n, batch, page = 131072, 304, 64
+    k = torch.zeros(n // page, 8, page // 16, 1152, dtype=torch.uint8)
+    v = torch.full((n // page, 8, page // 16, 1152), 0xFF, dtype=torch.uint8)  # -6
+    k[..., 1024:] = 0x38
+    v[..., 1024:] = 0x38
+    k[0, :, 0, :64] = 0x22  # 1
+    v[0, :, 0, :64] = 0x11  # 0.5
+    t = dict(k=k, v=v, k_scale=torch.ones(8), v_scale=torch.ones(8), q=torch.ones(batch, 8, 128, dtype=torch.bfloat16),
+             seq_lens=torch.full((batch,), n, dtype=torch.int32),
+             block_table=torch.arange(n // page, dtype=torch.int32).repeat(batch, 1))
+    scale = float(torch.tensor(math.log(2 ** 24 / 1.49) / 128))
+    small = math.exp(-128 * scale)
+    total = 1 + (n - 1) * small
+    want = (0.5 - 6 * (n - 1) * small) / total
+    spread = (0.5 + 6 * (n - 1) * small) / total
+    tol = 2.0 ** -8 * abs(want) + (2.0 ** -11 + 2.0 ** -12) * spread + 6 * (n - 1) * 2.0 ** -30 / total
+    eng = engine(t, hq=8, hkv=8, page=page)
+    out, lse = run(eng, t, scale)
+    assert eng.errors() == 0
+    assert (out.double() - want).abs().max().item() <= tol
+    assert (lse.double() - (128 * scale + math.log(total))).abs().max().item() <= 2.0 ** -12
