@@ -17,6 +17,7 @@ struct da_ctx {
   int smem_per_sm;
   bool planned;
   da_plan_info plan;
+  int32_t few_tiles, few_ctas;  // of a 4-bit float cache's plan (Fp4Params)
   // tensor maps are re-encoded only when the cache base pointers change
   const void *map_k_base;
   const void *map_v_base;
@@ -318,6 +319,8 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
     f.v = reinterpret_cast<const uint8_t *>(a->v);
     f.o_head = reinterpret_cast<float *>(ws + da::fp4_head_offset(pl));
     f.whole = pl.writes_final;
+    f.few_tiles = ctx->few_tiles;
+    f.few_ctas = ctx->few_ctas;
     return da::launch_fp4(f, pl.grid_x, stream) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
   }
   if (da::launch_gqa(fp8, gp.group, ctx->kmap, ctx->vmap, ctx->qmap,
@@ -426,6 +429,8 @@ da_status decode_attn_plan_ex(da_ctx *ctx, const int32_t *seq_lens_host,
                                   kv_num_blks_host, num_splits_override, &info);
   if (st != DA_OK) return st;
   ctx->plan = info;
+  if (ctx->prob.kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS)
+    da::fp4_few(ctx->prob, info, seq_lens_host, num_splits_override, &ctx->few_tiles, &ctx->few_ctas);
   ctx->planned = true;
   if (workspace_bytes) *workspace_bytes = (size_t)info.workspace_bytes;
   return DA_OK;

@@ -16,6 +16,7 @@ struct Fp4Params {
   const uint8_t *k, *v;
   float *o_head;               // [ctas][warps][G][128]
   int32_t whole;               // CTA c has unit c, whole (the grid is the units)
+  int32_t few_tiles, few_ctas; // a call of at most few_tiles tiles takes at most few_ctas CTAs
 };
 
 // Which instantiation a call's score and mask modifications need: 0 none; 1
@@ -91,6 +92,8 @@ int fp4_warps(int group);      // warps of a CTA for `group` rows per unit
 cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream);
 // Byte offset of Fp4Params::o_head in the workspace (after the partial LSEs).
 int64_t fp4_head_offset(const da_plan_info &info);
+void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host, int32_t num_splits_override,
+             int32_t *few_tiles, int32_t *few_ctas);
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);

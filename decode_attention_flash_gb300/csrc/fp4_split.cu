@@ -152,24 +152,30 @@ __device__ __forceinline__ uint32_t f4_scale(uint32_t x, uint32_t s, int high) {
 }
 
 // `threads` threads (a whole number of warps, this one the `tid`-th, meeting at named
-// barrier `bar`) merge the n <= 32 pieces of `unit` that CTAs c_first .. c_first + n - 1
-// left (slots unit + cta) into the final output: a warp takes a row's LSEs, one
-// piece a lane, for the weights; the threads' loads of the pieces' O, kLoads at a
-// time, are in flight meanwhile. `scr`: shared memory, free.
-__device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first, int n, int G, float *scr,
-                                      int tid, int threads, int bar) {
+// barrier `bar`) merge the n <= 32 pieces of `unit` in slots slot0, slot0 + stride, .. into
+// the output (to < 0) or one piece in slot `to`, which may be the first of them: a warp
+// takes a row's LSEs, one piece a lane, for the weights; the threads' loads of the
+// pieces' O, kLoads at a time, are in flight meanwhile. `scr`: shared memory, free.
+__device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int64_t slot0, int stride, int n, int64_t to,
+                                      int G, float *scr, int tid, int threads, int bar) {
   constexpr int kLoads = 8;
   const int lane = tid & 31, warp = tid >> 5;
   const int nout = G * (kD / 4);
-  const int64_t slot0 = (int64_t)unit + c_first;
   float *w = scr;                                          // [G][32] weights over their sum
-  float4 *acc = reinterpret_cast<float4 *>(scr + G * 32);  // [parts][nout]
+  float *lse_to = scr + G * 32;                            // [16] of the piece (its slot is still read)
+  float4 *acc = reinterpret_cast<float4 *>(scr + G * 32 + 16);  // [parts][nout]
   const int parts = max(1, min(threads / nout, n));        // threads that share an output
   const float4 *src = reinterpret_cast<const float4 *>(p.o_part + slot0 * G * kD);
+  const int64_t step = (int64_t)stride * nout;
   const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
   const int64_t row0 = (int64_t)b * p.num_q_heads + h * G;
+  auto lse_of = [&](int g) {
+    return lane < n && g < G ? __ldcg(p.lse_part + (slot0 + lane * stride) * G + g) : neg_inf();
+  };
+  float ahead = lse_of(warp);
   for (int g = warp; g < G; g += threads / 32) {
-    const float l = lane < n ? __ldcg(p.lse_part + (slot0 + lane) * G + g) : neg_inf();
+    const float l = ahead;
+    ahead = lse_of(g + threads / 32);
     float M = l;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -178,7 +184,11 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     w[g * 32 + lane] = sum == 0.f ? 0.f : e / sum;
-    if (lane == 0 && p.lse) p.lse[row0 + g] = sum == 0.f ? neg_inf() : M + __log2f(sum) * 0.69314718055994531f;
+    if (lane == 0) {
+      const float lse = sum == 0.f ? neg_inf() : M + __log2f(sum) * 0.69314718055994531f;
+      if (to >= 0) lse_to[g] = lse;
+      else if (p.lse) p.lse[row0 + g] = lse;
+    }
   }
   // (items are warp-uniform in number: nout * parts is a multiple of 32)
   bool met = false;
@@ -189,7 +199,7 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
       float4 v[kLoads];
 #pragma unroll
       for (int k = 0; k < kLoads; ++k)
-        v[k] = s + k * parts < n ? __ldcg(src + (int64_t)(s + k * parts) * nout + o) : make_float4(0.f, 0.f, 0.f, 0.f);
+        v[k] = s + k * parts < n ? __ldcg(src + (int64_t)(s + k * parts) * step + o) : make_float4(0.f, 0.f, 0.f, 0.f);
       if (!met) named_barrier_sync(bar, threads);  // the weights are in w
       met = true;
 #pragma unroll
@@ -216,12 +226,14 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int c_first,
       a.z += v.z;
       a.w += v.w;
     }
-    *reinterpret_cast<uint2 *>(p.out + row0 * kD + 4 * o) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
+    if (to >= 0) reinterpret_cast<float4 *>(p.o_part + to * G * kD)[o] = a;
+    else *reinterpret_cast<uint2 *>(p.out + row0 * kD + 4 * o) = make_uint2(pack_bf16(a.x, a.y), pack_bf16(a.z, a.w));
   }
-  if (tid == 0) p.counters[unit] = 0u;  // ready for the next call
+  if (to >= 0 && tid < G) p.lse_part[to * G + tid] = lse_to[tid];
+  if (to < 0 && tid == 0) p.counters[unit] = 0u;  // ready for the next call
 }
 constexpr int kOneLevel = 32;  // pieces that f4_merge takes (a lane's worth); a unit of more is merged in
-                               // two levels, as in gqa_split.cuh
+                               // two levels, groups as in gqa_split.cuh (by its own merge: 2.3 us more)
 
 template <int NT, int MOD>
 __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
@@ -318,7 +330,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       T += v.x + v.y + v.z + v.w;
     }
     pre[threadIdx.x] = before + local;
-    CTAS = T < (int)gridDim.x ? T : (int)gridDim.x;  // never more ranges than tiles
+    // never more ranges than tiles; of few tiles, few enough that a unit is merged in one level
+    CTAS = min(min(T, (int)gridDim.x), T <= fp.few_tiles ? fp.few_ctas : T);
     if (cta >= CTAS) {
       if (dev_err) atomicOr(p.err, dev_err);
       return;
@@ -1100,8 +1113,8 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     constexpr int kHalf = (W + 1) / 2 * 32;
     const bool both = one0 && one1;
     const int mine = both ? (int)threadIdx.x / kHalf : 0, slot = (both ? mine : one0 ? 0 : 1) ? 28 : 24;
-    f4_merge(p, flags[slot], flags[slot + 1], flags[slot + 2], G, scr + mine * 4096, (int)threadIdx.x - mine * kHalf,
-             both ? kHalf : C::kThreads, 1 + mine);
+    f4_merge(p, flags[slot], (int64_t)flags[slot] + flags[slot + 1], 1, flags[slot + 2], -1, G, scr + mine * 4096,
+             (int)threadIdx.x - mine * kHalf, both ? kHalf : C::kThreads, 1 + mine);
     __syncthreads();
   }
   for (int slot = 24; slot <= 28; slot += 4) {
@@ -1109,15 +1122,16 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     if (unit < 0 || q < 0) continue;
     const int64_t slot0 = (int64_t)unit + cf;
     const int K = merge_group_size(ns), ng = (ns + K - 1) / K, gs = min(K, ns - q * K);
-    merge_slots_cta(p, unit, G, slot0 + (int64_t)q * K, 1, gs, false, slot0 + (int64_t)q * K, scr);
+    const int64_t first = slot0 + (int64_t)q * K;
+    f4_merge(p, unit, first, 1, gs, first, G, scr, (int)threadIdx.x, C::kThreads, 1);
+    __syncthreads();
     if (threadIdx.x == 0)
       *last_group = atomic_add_acq_rel_gpu(p.counters + unit, 1u) == (unsigned)(ng - 1) ? 1 : 0;
     __syncthreads();
     if (*last_group) {
-      merge_slots_cta(p, unit, G, slot0, K, ng, true, 0, scr);
       uint32_t *gc = p.counters + U + (int64_t)unit * max_merge_groups(gridDim.x);
       for (int i = threadIdx.x; i < ng; i += C::kThreads) gc[i] = 0u;
-      if (threadIdx.x == 0) p.counters[unit] = 0u;
+      f4_merge(p, unit, slot0, K, ng, -1, G, scr, (int)threadIdx.x, C::kThreads, 1);
     }
     __syncthreads();
   }

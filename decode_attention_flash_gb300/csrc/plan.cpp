@@ -110,6 +110,29 @@ int64_t fp4_head_offset(const da_plan_info &i) {
   return align256(i.partial_lse_offset + ((int64_t)i.num_units + i.grid_x) * i.rows_per_unit * 4);
 }
 
+// A unit in more than 32 pieces is merged in two levels (6 us more than in one: 18.7 us
+// against 12.3 for one row of 4096 tokens and one kv head), and an SM reads pieces at
+// about 45 GB/s. So a call that fewer CTAs would serve with at most four tiles a warp
+// takes no more than leave its longest unit 28 pieces, or 16 of more than 8 rows: one row
+// of 16384 tokens, one head: 17.9 -> 16.3 us; two heads of 16 rows: 31.4 -> 22.7 (28
+// pieces: 28.1). The longest unit's share is that of the planned lengths, or the mean.
+void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host, int32_t num_splits_override,
+             int32_t *few_tiles, int32_t *few_ctas) {
+  *few_tiles = *few_ctas = 0;
+  if (num_splits_override > 0) return;
+  const int64_t capacity = p.kv_layout == DA_KV_PAGED ? (int64_t)p.max_pages_per_seq * p.page_size : p.max_seq_len;
+  int64_t sum = 0, longest = 0;
+  for (int32_t b = 0; seq_lens_host && p.sparse_block_size == 0 && b < p.batch; ++b) {
+    const int64_t t = ceil_div(std::min<int64_t>(std::max<int32_t>(seq_lens_host[b], 0), capacity), info.kv_tile);
+    sum += t * p.num_kv_heads;
+    longest = std::max(longest, t);
+  }
+  const int64_t pieces = info.rows_per_unit <= 8 ? 28 : 16;
+  const int64_t most = longest > 0 ? std::max<int64_t>(pieces * sum / longest, 1) : pieces * info.num_units;
+  *few_ctas = (int32_t)std::min<int64_t>(most, INT32_MAX);
+  *few_tiles = (int32_t)std::min<int64_t>(most * 4 * fp4_warps(info.rows_per_unit), INT32_MAX);
+}
+
 // Resident CTAs of the split kernel per SM, from its shared-memory footprint.
 static int ctas_per_sm(const da_problem *p, int32_t smem_per_sm) {
   const bool mla = p->is_mla != 0;

@@ -73,6 +73,13 @@ def test_one_long_row_over_many_ctas(n, splits):
     check(R.make(lens=[n], hq=4, hkv=1, page=64, seed=n), hq=4, hkv=1, page=64, splits=splits)
 
 
+@pytest.mark.parametrize("group", [1, 5, 8, 12, 16])
+@pytest.mark.parametrize("splits", [33, 61, 0])
+def test_two_long_rows_merged_in_one_and_two_levels(group, splits):
+    # 33 and 61 pieces of a row, and the number that the planned lengths give
+    check(R.make(lens=[4100, 3999], hq=group, hkv=1, page=64, seed=group), hq=group, hkv=1, page=64, splits=splits)
+
+
 @pytest.mark.parametrize("rows,hi", [(70, 40), (150, 3), (40, 500)])
 def test_many_short_rows(rows, hi):
     # warps whose range holds several whole units, and pieces of two others
