@@ -330,8 +330,14 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
       T += v.x + v.y + v.z + v.w;
     }
     pre[threadIdx.x] = before + local;
-    // never more ranges than tiles; of few tiles, few enough that a unit is merged in one level
-    CTAS = min(min(T, (int)gridDim.x), T <= fp.few_tiles ? fp.few_ctas : T);
+    CTAS = min(T, (int)gridDim.x);  // never more ranges than tiles
+    // of few tiles so few that a unit is merged in one level (ranges of 1 and 2 tiles side
+    // by side would be twice as many for a unit of the short ones: none is short of the
+    // mean, rounded up; of 8 tiles and more one matters little)
+    if (T > 0 && T <= fp.few_tiles) {
+      const uint32_t n = (uint32_t)T, few = (uint32_t)fp.few_ctas;
+      CTAS = min(CTAS, (int)(n / 8 >= few ? few : n / ((n + few - 1) / few)));
+    }
     if (cta >= CTAS) {
       if (dev_err) atomicOr(p.err, dev_err);
       return;

@@ -129,7 +129,7 @@ void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_l
   }
   const int64_t pieces = info.rows_per_unit <= 8 ? 28 : 16;
   const int64_t most = longest > 0 ? std::max<int64_t>(pieces * sum / longest, 1) : pieces * info.num_units;
-  *few_ctas = (int32_t)std::min<int64_t>(most, INT32_MAX);
+  *few_ctas = (int32_t)std::min<int64_t>(most, info.grid_x);
   *few_tiles = (int32_t)std::min<int64_t>(most * 4 * fp4_warps(info.rows_per_unit), INT32_MAX);
 }
 
@@ -211,14 +211,15 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
     bool whole = false;
     if (fp4) {
       // A CTA for every unit saves the scan of the lengths and the merge between CTAs,
-      // about 3 us, and costs the time by which the longest unit passes an equal
-      // share: about 0.09 us a tile (8 heads of one 700-token row: 11.7 against 13.1 us;
-      // of a 3000-token row: 20 against 13).
+      // about 3 us (6 of 16 rows a unit), and costs the time by which the longest unit
+      // passes an equal share: about 0.09 us a tile (8 heads of one 700-token row: 11.7
+      // against 13.1 us; of a 3000-token row: 20 against 13; two heads of 16 rows in three
+      // rows of 1500 tokens: 17.6 against 21.9; of 3000: 25.1 against 22.3).
       int64_t longest = 0;
       for (int64_t len : unit_len) longest = std::max(longest, ceil_div(len, tile));
       whole = num_splits_override > 0
                   ? num_splits_override == 1 && units <= 65535
-                  : seq_lens_host && units <= num_sms && longest - tiles / num_sms <= 32;
+                  : seq_lens_host && units <= num_sms && longest - tiles / num_sms <= (rows <= 8 ? 32 : 48);
       if (whole) ctas = units;
     }
     info->kv_tile = tile;
