@@ -318,6 +318,9 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
     f.k = reinterpret_cast<const uint8_t *>(a->k);
     f.v = reinterpret_cast<const uint8_t *>(a->v);
     f.o_head = reinterpret_cast<float *>(ws + da::fp4_head_offset(pl));
+    f.kv_shift = da::fp4_kv_shift(p);
+    f.g.num_kv_heads <<= f.kv_shift;
+    f.g.group >>= f.kv_shift;
     f.whole = pl.writes_final;
     f.few_tiles = ctx->few_tiles;
     f.few_ctas = ctx->few_ctas;

@@ -16,6 +16,7 @@ struct Fp4Params {
   const uint8_t *k, *v;
   float *o_head;               // [ctas][warps][G][128]
   int32_t whole;               // CTA c has unit c, whole (the grid is the units)
+  int32_t kv_shift;            // a kv head's queries are 2^kv_shift units (g.num_kv_heads counts those)
   int32_t few_tiles, few_ctas; // a call of at most few_tiles tiles takes at most few_ctas CTAs
 };
 
@@ -89,6 +90,9 @@ cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned 
 cudaError_t fp4_prepare();
 int fp4_tile();                // tokens per stage
 int fp4_warps(int group);      // warps of a CTA for `group` rows per unit
+// log2 of the units that a kv head's queries are split into, so that each has at most 16 rows
+// (one query token, dense); -1: no such split.
+int fp4_kv_shift(const da_problem &p);
 cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream);
 // Byte offset of Fp4Params::o_head in the workspace (after the partial LSEs).
 int64_t fp4_head_offset(const da_plan_info &info);

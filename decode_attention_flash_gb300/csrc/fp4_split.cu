@@ -52,6 +52,8 @@
 // stream, and pieces shared by CTAs in global memory (counted and merged as in
 // gqa_split.cuh, without any CTA waiting for another). Small calls give a CTA to every
 // unit instead (plan.cpp): no scan, no merge between CTAs.
+// More than 16 query heads a kv head are units of up to 16 that read the same cache
+// (num_kv_heads counts them, shifted right by kv_shift it counts the cache's).
 #include "cache_ops.h"
 #include "cache_ptx.cuh"
 #include "gqa_split.cuh"
@@ -373,6 +375,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     const bool two_pages = p.paged && P < kT;
     const bool has_ids = p.paged || sparse;
     const int gran_unit = p.paged ? P / kGran : p.cache_len / kGran;  // granules per (page | row, head)
+    const int kv_heads = p.num_kv_heads >> fp.kv_shift;                // of the cache
     int u = 0, j = 0, ent = 0, sub = 0, nent = 0;  // unit, its tile, current entry, tile inside it, entries
     int id0 = -1, id1 = -1;                        // the current tile's ids
     int Pu = 0;                                    // the unit's first tile
@@ -455,20 +458,20 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
           const int left = x.n_valid - pos0;  // at least 1
           valid = left >= 32 ? 0xFFFFFFFFu : (1u << left) - 1u;
           if (!p.paged) {
-            gr0 = (int64_t)u * gran_unit + j * (kT / kGran);
+            gr0 = (int64_t)(u >> fp.kv_shift) * gran_unit + j * (kT / kGran);
             gr1 = gr0 + 1;
           } else if (two_pages) {
             const bool ok0 = (uint32_t)id0 < (uint32_t)p.num_pages, ok1 = (uint32_t)id1 < (uint32_t)p.num_pages;
             if (!ok0 || (left > kGran && !ok1)) dev_err |= DA_DEVERR_PAGE_INDEX;
             valid &= (ok0 ? 0xFFFFu : 0u) | (ok1 ? 0xFFFF0000u : 0u);
-            gr0 = (int64_t)id0 * p.num_kv_heads + x.h;
-            gr1 = (int64_t)id1 * p.num_kv_heads + x.h;
+            gr0 = (int64_t)id0 * kv_heads + (x.h >> fp.kv_shift);
+            gr1 = (int64_t)id1 * kv_heads + (x.h >> fp.kv_shift);
           } else {
             if ((uint32_t)id0 >= (uint32_t)p.num_pages) {
               dev_err |= DA_DEVERR_PAGE_INDEX;
               valid = 0;
             }
-            gr0 = ((int64_t)id0 * p.num_kv_heads + x.h) * gran_unit + sub * (kT / kGran);
+            gr0 = ((int64_t)id0 * kv_heads + (x.h >> fp.kv_shift)) * gran_unit + sub * (kT / kGran);
             gr1 = gr0 + 1;
           }
         }
@@ -670,7 +673,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
             qf[0][s][1] = bf16x2_to_f16x2(qw[0][s].y, q2);
           }
         }
-        sscale = p.score_scale * p.k_scale[h] * pow2f(-qexp);
+        sscale = p.score_scale * p.k_scale[h >> fp.kv_shift] * pow2f(-qexp);
         // a zero factor (uniform weights) as 2^-100: a finite score still weighs 1, and
         // an infinite one (a masked token's) 0
         if (sscale == 0.f) sscale = 0x1p-100f;
@@ -937,7 +940,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
               n_seg = cut.owner(seg_P + seg_tiles - 1) - c_first + 1;
             }
             lead[tail ? warp : W] = make_int4(unit, bw | (goes_on ? 256 : 0), c_first, n_seg);
-            reinterpret_cast<float *>(smem + C::oSum)[(tail ? warp : W) * 32 + 16] = p.v_scale[h];
+            reinterpret_cast<float *>(smem + C::oSum)[(tail ? warp : W) * 32 + 16] = p.v_scale[h >> fp.kv_shift];
           }
         }
 #pragma unroll
@@ -979,7 +982,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
             const int g = nt * 8 + 2 * q4 + e;
             if (g < G) {
               const int64_t row = (int64_t)b * p.num_q_heads + h * G + g;
-              const float mul = l == 0.f ? 0.f : p.v_scale[h] / l;  // no valid token: 0; NaN goes through
+              const float mul = l == 0.f ? 0.f : p.v_scale[h >> fp.kv_shift] / l;  // no valid token: 0; NaN goes through
               uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD + 16 * r8);
 #pragma unroll
               for (int k = 0; k < 2; ++k)

@@ -68,7 +68,8 @@ da_status validate_problem(const da_problem *p) {
   }
   if (p->num_q_heads % p->num_kv_heads) return DA_ERR_INVALID_ARG;
   const int G = p->num_q_heads / p->num_kv_heads;
-  if (G * Q > 16) return DA_ERR_UNSUPPORTED;  // the G x Q rows of a kv head: two n-tiles at most
+  // the G x Q rows of a kv head: two n-tiles at most (the 4-bit float decode splits more)
+  if (G * Q > 16 && (p->kv_dtype != DA_DTYPE_FP4_E2M1_BLOCKS || fp4_kv_shift(*p) < 0)) return DA_ERR_UNSUPPORTED;
   if (p->head_dim_qk != 128 || p->head_dim_v != 128) return DA_ERR_UNSUPPORTED;
   if (p->kv_layout == DA_KV_PAGED) {
     const int P = p->page_size;
@@ -94,8 +95,9 @@ da_status validate_problem(const da_problem *p) {
                                                     : (int64_t)p->max_seq_len;
     const int64_t list = (int64_t)p->sparse_block_size * p->max_sparse_blocks * 2;
     if (cap >= (1ll << 31) || list >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
-    const int64_t tiles = (int64_t)p->batch * p->num_kv_heads * ((std::max(cap, list) + 31) / 32);
-    if ((int64_t)p->batch * p->num_kv_heads >= (1ll << 31) || tiles >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+    const int64_t units = ((int64_t)p->batch * p->num_kv_heads) << fp4_kv_shift(*p);
+    const int64_t tiles = units * ((std::max(cap, list) + 31) / 32);
+    if (units >= (1ll << 31) || tiles >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
     return DA_OK;
   }
   // TMA row coordinates are 32-bit: (cache rows) x (rows per token) must fit
@@ -104,6 +106,15 @@ da_status validate_problem(const da_problem *p) {
                            : (int64_t)p->batch * p->num_kv_heads * p->max_seq_len;
   if (rows * 2 + kGqaTile * 2 >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
   return DA_OK;
+}
+
+int fp4_kv_shift(const da_problem &p) {
+  const int G = p.num_q_heads / p.num_kv_heads, Q = p.q_len > 1 ? p.q_len : 1;
+  if ((int64_t)G * Q <= 16) return 0;
+  if (Q > 1 || p.sparse_block_size > 0) return -1;
+  for (int s = 1; s <= 3; ++s)
+    if (G % (1 << s) == 0 && G >> s <= 16) return s;
+  return -1;
 }
 
 int64_t fp4_head_offset(const da_plan_info &i) {
@@ -124,7 +135,7 @@ void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_l
   int64_t sum = 0, longest = 0;
   for (int32_t b = 0; seq_lens_host && p.sparse_block_size == 0 && b < p.batch; ++b) {
     const int64_t t = ceil_div(std::min<int64_t>(std::max<int32_t>(seq_lens_host[b], 0), capacity), info.kv_tile);
-    sum += t * p.num_kv_heads;
+    sum += t * (info.num_units / p.batch);
     longest = std::max(longest, t);
   }
   const int64_t pieces = info.rows_per_unit <= 8 ? 28 : 16;
@@ -164,12 +175,13 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
   const int align = sparse ? p->sparse_block_size : tile;
   // units: GQA (row, kv head); MLA (row, query token), whose heads share the latent cache
   const int Q = p->q_len > 1 ? p->q_len : 1;
-  const int heads = mla ? Q : p->num_kv_heads;
+  const int shift = fp4 ? fp4_kv_shift(*p) : 0;
+  const int heads = mla ? Q : p->num_kv_heads << shift;
   const int64_t units = (int64_t)p->batch * heads;
   const int64_t capacity =
       paged ? (int64_t)p->max_pages_per_seq * p->page_size : (int64_t)p->max_seq_len;
   // rows per unit: the G query heads (times the query tokens) of a kv head; MLA: all heads
-  const int rows = mla ? p->num_q_heads : p->num_q_heads / p->num_kv_heads * Q;
+  const int rows = mla ? p->num_q_heads : (p->num_q_heads / p->num_kv_heads * Q) >> shift;
   const int dv = p->head_dim_v;
 
   // positions per unit the split kernel walks (sparse: the compacted list)

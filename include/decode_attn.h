@@ -121,7 +121,8 @@ enum {
  *        extents: row b and kv head h read table row (b % SZ, h % SH), the
  *        broadcast of the flex decode template (SPARSE_Z, SPARSE_HQ).
  *   q_len: query tokens per row, 0 or 1 = one. GQA: G * Q <= 16 (the G*Q rows
- *        of a kv head share one pass); block-sparse tables apply to every query
+ *        of a kv head share one pass; a dense 4-bit float cache with one query
+ *        token also takes 2, 4 or 8 times a G <= 16, in that many passes); block-sparse tables apply to every query
  *        token, the causal or tree mask on top of them. MLA: Q <= 16, each query
  *        token a row of its own over the shared latent cache (its pages come
  *        from L2 for the row's other tokens).

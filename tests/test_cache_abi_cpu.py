@@ -47,6 +47,16 @@ def test_fp4_problems_are_validated(lib):
     plan(**(paged | dict(num_pages=1 << 27, max_pages_per_seq=1 << 20)), page_size=16)
 
 
+def test_fp4_heads_of_many_queries_are_split(lib):
+    for hq, units, rows in ((32, 2, 16), (20, 2, 10), (48, 4, 12), (64, 4, 16), (128, 8, 16)):
+        got = plan([100], batch=1, num_q_heads=hq, num_kv_heads=1, max_seq_len=208)
+        assert (got["num_units"], got["rows_per_unit"]) == (units, rows)
+    for more in (dict(num_q_heads=19), dict(num_q_heads=144), dict(num_q_heads=32, q_len=2),
+                 dict(num_q_heads=32, max_seq_len=256, sparse_block_size=64, max_sparse_blocks=4),
+                 dict(num_q_heads=32, kv_dtype=da.DA_DTYPE_BF16)):
+        assert refused(**(dict(batch=1, num_kv_heads=1, max_seq_len=208) | more)) == da.DA_ERR_UNSUPPORTED
+
+
 def test_fp4_plan_takes_a_block_for_every_unit_where_that_is_shorter(lib):
     kw = dict(kv_layout=da.DA_KV_PAGED, num_pages=5000, max_pages_per_seq=1000, page_size=16)
     short = plan([700, 1, 64, 0], **kw)

@@ -73,6 +73,16 @@ def test_one_long_row_over_many_ctas(n, splits):
     check(R.make(lens=[n], hq=4, hkv=1, page=64, seed=n), hq=4, hkv=1, page=64, splits=splits)
 
 
+@pytest.mark.parametrize("hq,hkv", [(32, 1), (40, 2), (72, 3), (128, 1)])
+@pytest.mark.parametrize("page,splits", [(16, 0), (64, 0), (0, 0), (16, 3)])
+def test_more_than_16_queries_a_head(hq, hkv, page, splits):
+    t = R.make(lens=[300, 0, 17, 1, 1900], hq=hq, hkv=hkv, page=page, length=0 if page else 1904, seed=hq)
+    check(t, hq=hq, hkv=hkv, page=page, splits=splits)
+    t["mask_window"] = torch.tensor([50, -1, 7, 200] * (hq // 4), dtype=torch.int32)
+    t["alibi_slopes"] = torch.linspace(0.01, 0.2, hq)
+    check(t, hq=hq, hkv=hkv, page=page, splits=splits)
+
+
 @pytest.mark.parametrize("group", [1, 5, 8, 12, 16])
 @pytest.mark.parametrize("splits", [33, 61, 0])
 def test_two_long_rows_merged_in_one_and_two_levels(group, splits):
