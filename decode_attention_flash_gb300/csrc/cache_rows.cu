@@ -30,6 +30,8 @@
 // K first and then V, with a head's address worked out for each row: 65.2, 31.4 and
 // 61.3 us, bound by instruction issue; one row in flight of K and of V instead of two:
 // 65.2, 31.0 and 70.7.
+// The read-back gives half a warp to a token (two tokens of one head a warp: 65537 of
+// them 21.7 -> 12.4 us, of two heads 23.4 -> 16.5, of eight 54.7 either way).
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -515,13 +517,14 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
   const int lane = threadIdx.x & 31;
   wait_for_previous_kernel();
   let_next_kernel_start();
-  const int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  constexpr int kTeam = KIND == kLatent ? 32 : 16;  // lanes of a token
+  const int64_t item = (int64_t)blockIdx.x * (kWarps * 32 / kTeam) + threadIdx.x / kTeam;
   const int64_t t = p.parts == 1 ? item : (int64_t)((uint32_t)item / (uint32_t)p.parts);
   const int part = (int)(item - t * p.parts);
   if (t >= p.num_tokens) return;
   uint32_t err = 0;
   const int64_t slot = load_slot(p, t, err);
-  if (err && lane == 0) atomicOr(p.err, err);
+  if (err && lane % kTeam == 0) atomicOr(p.err, err);
   if (slot < 0) return;
   if (KIND == kLatent) {  // 512 + 64 elements: 72 chunks of 16 bytes
     const uint4 *ck = reinterpret_cast<const uint4 *>(p.k) + slot * 64;
@@ -535,45 +538,42 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
     ok[32 + lane] = b;
     return;
   }
-  const int l = lane & 15, sub = lane >> 4;
+  const int l = lane & 15;
   const RowAt at = row_at<KIND>(p, slot, l);
-  // heads two at once, of K and of V side by side, pointers a stride on; kSide rows of
-  // each in flight
-  const int HK = p.num_kv_heads, nk = (HK + 1) / 2;
-  const int g0 = (int)((uint32_t)(part * nk) / (uint32_t)p.parts);
-  const int g1 = (int)((uint32_t)((part + 1) * nk) / (uint32_t)p.parts);
-  int h = 2 * g0 + sub;
-  const uint8_t *k = at.k + h * at.head, *v = at.v + h * at.head;
-  const uint8_t *ks = at.ks + h * at.shead, *vs = at.vs + h * at.shead;
-  const int64_t step = 2 * at.head, sstep = 2 * at.shead;
-  uint4 *ko = reinterpret_cast<uint4 *>(p.k_out) + (t * HK + h) * 16 + l;
-  uint4 *vo = reinterpret_cast<uint4 *>(p.v_out) + (t * HK + h) * 16 + l;
-  for (int g = g0; g < g1; g += kSide) {
+  // head by head, of K and of V side by side, pointers a stride on; kSide rows of each in
+  // flight
+  const int HK = p.num_kv_heads;
+  const int h0 = (int)((uint32_t)(part * HK) / (uint32_t)p.parts);
+  const int h1 = (int)((uint32_t)((part + 1) * HK) / (uint32_t)p.parts);
+  const uint8_t *k = at.k + h0 * at.head, *v = at.v + h0 * at.head;
+  const uint8_t *ks = at.ks + h0 * at.shead, *vs = at.vs + h0 * at.shead;
+  uint4 *ko = reinterpret_cast<uint4 *>(p.k_out) + (t * HK + h0) * 16 + l;
+  uint4 *vo = reinterpret_cast<uint4 *>(p.v_out) + (t * HK + h0) * 16 + l;
+  for (int h = h0; h < h1; h += kSide) {
     RowBits rk[kSide], rv[kSide];
     float sk[kSide], sv[kSide];
 #pragma unroll
     for (int i = 0; i < kSide; ++i)
-      if (g + i < g1 && h + 2 * i < HK) {
+      if (h + i < h1) {
         rk[i] = get_row<KIND>(k, ks);
         rv[i] = get_row<KIND>(v, vs);
         if (KIND == kE4m3 || KIND == kFp4) {
-          sk[i] = __ldg(p.k_scale + h + 2 * i);
-          sv[i] = __ldg(p.v_scale + h + 2 * i);
+          sk[i] = __ldg(p.k_scale + h + i);
+          sv[i] = __ldg(p.v_scale + h + i);
         }
-        k += step;
-        v += step;
-        ks += sstep;
-        vs += sstep;
+        k += at.head;
+        v += at.head;
+        ks += at.shead;
+        vs += at.shead;
       }
 #pragma unroll
     for (int i = 0; i < kSide; ++i)
-      if (g + i < g1 && h + 2 * i < HK) {
-        ko[32 * i] = row_values<KIND>(rk[i], sk[i]);
-        vo[32 * i] = row_values<KIND>(rv[i], sv[i]);
+      if (h + i < h1) {
+        ko[16 * i] = row_values<KIND>(rk[i], sk[i]);
+        vo[16 * i] = row_values<KIND>(rv[i], sv[i]);
       }
-    h += 2 * kSide;
-    ko += 32 * kSide;
-    vo += 32 * kSide;
+    ko += 16 * kSide;
+    vo += 16 * kSide;
   }
 }
 
@@ -611,8 +611,9 @@ cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t 
 
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  p.parts = kind == kLatent ? 1 : parts_for(p.num_tokens, (p.num_kv_heads + 1) / 2, num_sms);
-  const unsigned grid = (unsigned)blocks_for((int64_t)p.num_tokens * p.parts);
+  p.parts = kind == kLatent ? 1 : parts_for((p.num_tokens + 1) / 2, p.num_kv_heads, num_sms);
+  const int64_t items = (int64_t)p.num_tokens * p.parts;  // half a warp each, but the latent rows
+  const unsigned grid = (unsigned)blocks_for(kind == kLatent ? items : (items + 1) / 2);
   switch (kind) {
     case kBf16: return launch_dependent(gather_kernel<kBf16>, grid, kWarps * 32, 0, stream, p);
     case kE4m3: return launch_dependent(gather_kernel<kE4m3>, grid, kWarps * 32, 0, stream, p);
