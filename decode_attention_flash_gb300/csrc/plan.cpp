@@ -232,7 +232,8 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
       whole = num_splits_override > 0
                   ? num_splits_override == 1 && units <= 65535
                   : seq_lens_host && units <= num_sms && longest - tiles / num_sms <= (rows <= 8 ? 32 : 48);
-      if (whole) ctas = units;
+      // (a unit's pieces, at most one a CTA, are merged in two levels of at most 32)
+      ctas = whole ? units : std::min<int64_t>(ctas, 1024);
     }
     info->kv_tile = tile;
     info->chunk_tokens = (int32_t)(ceil_div(tiles, ctas) * tile);

@@ -74,6 +74,14 @@ def test_fp4_plan_takes_a_block_for_every_unit_where_that_is_shorter(lib):
         assert p["workspace_bytes"] >= lse_end + ctas * 15 * rows * 512
 
 
+def test_fp4_plan_has_no_more_pieces_than_two_levels_of_32_merge(lib):
+    kw = dict(kv_layout=da.DA_KV_PAGED, num_pages=5000, max_pages_per_seq=5000, page_size=64)
+    for splits in (1024, 1025, 4000, 1 << 30):
+        assert plan([200000], batch=1, splits=splits, num_q_heads=4, num_kv_heads=1, **kw)["grid_x"] == 1024
+    assert plan([200000, 5], batch=2, splits=1000, **kw)["grid_x"] == 1024
+    assert plan([5] * 3000, batch=3000, splits=1, **kw)["grid_x"] == 6000  # a CTA a unit: nothing to merge
+
+
 def test_calls_refuse_null_and_report_it(lib):
     for name, args in (("build_tables", da.TableArgs()), ("append", da.AppendArgs()), ("gather", da.GatherArgs())):
         fn = getattr(lib, "decode_attn_" + name)

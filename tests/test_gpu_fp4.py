@@ -90,6 +90,11 @@ def test_two_long_rows_merged_in_one_and_two_levels(group, splits):
     check(R.make(lens=[4100, 3999], hq=group, hkv=1, page=64, seed=group), hq=group, hkv=1, page=64, splits=splits)
 
 
+@pytest.mark.parametrize("splits", [1000, 5000])
+def test_as_many_pieces_as_two_levels_merge(splits):
+    check(R.make(lens=[40000], hq=4, hkv=1, page=64, seed=6), hq=4, hkv=1, page=64, splits=splits)
+
+
 @pytest.mark.parametrize("rows,hi", [(70, 40), (150, 3), (40, 500)])
 def test_many_short_rows(rows, hi):
     # warps whose range holds several whole units, and pieces of two others
