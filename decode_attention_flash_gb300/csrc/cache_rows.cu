@@ -32,6 +32,8 @@
 // 65.2, 31.0 and 70.7.
 // The read-back gives half a warp to a token (two tokens of one head a warp: 65537 of
 // them 21.7 -> 12.4 us, of two heads 23.4 -> 16.5, of eight 54.7 either way).
+#include <algorithm>
+
 #include <cuda_fp16.h>
 
 #include "cache_ops.h"
@@ -583,7 +585,7 @@ int64_t blocks_for(int64_t items) { return (items + kWarps - 1) / kWarps; }
 int parts_for(int64_t tokens, int groups, int num_sms) {
   const int64_t want = (int64_t)num_sms * 48;
   const int64_t parts = (want + tokens - 1) / tokens;
-  return (int)(parts < 1 ? 1 : parts > groups ? groups : parts);
+  return (int)std::max<int64_t>(1, std::min<int64_t>({parts, groups, INT32_MAX / groups}));
 }
 
 // The append, whose parts look slot and angles up again: as many as one wave holds (32
@@ -594,7 +596,7 @@ int append_parts(int64_t tokens, int groups, int num_sms) {
   const int64_t wave = (int64_t)num_sms * 32;
   int64_t parts = wave / tokens;
   if (parts < 2) parts = groups >= 12 && tokens < 2 * wave ? 2 : 1;
-  return (int)(parts > groups ? groups : parts);
+  return (int)std::min<int64_t>({parts, groups, INT32_MAX / groups});
 }
 
 }  // namespace
@@ -620,7 +622,7 @@ cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t 
 
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  p.parts = kind == kLatent ? 1 : parts_for((p.num_tokens + 1) / 2, p.num_kv_heads, num_sms);
+  p.parts = kind == kLatent ? 1 : parts_for(((int64_t)p.num_tokens + 1) / 2, p.num_kv_heads, num_sms);
   const int64_t items = (int64_t)p.num_tokens * p.parts;  // half a warp each, but the latent rows
   const unsigned grid = (unsigned)blocks_for(kind == kLatent ? items : (items + 1) / 2);
   switch (kind) {
