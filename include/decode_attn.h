@@ -268,7 +268,8 @@ da_status decode_attn_create(const da_problem *problem, int device, da_ctx **out
  * *workspace_bytes. seq_lens_host (int32 [B], host memory, may be NULL)
  * lets the planner size splits from the real lengths; without it the plan
  * assumes every row is max_seq_len long. num_splits_override > 0 forces that
- * many splits per unit (positions are cut into equal tile-aligned chunks).
+ * many splits per unit (positions are cut into equal tile-aligned chunks; a
+ * 4-bit float cache takes at most 1024 CTAs in all, or one split).
  * Host-only; no GPU work. Errors: INVALID_ARG.
  */
 da_status decode_attn_plan(da_ctx *ctx, const int32_t *seq_lens_host, int32_t num_splits_override,
