@@ -54,6 +54,8 @@
 // unit instead (plan.cpp): no scan, no merge between CTAs.
 // More than 16 query heads a kv head are units of up to 16 that read the same cache
 // (num_kv_heads counts them, shifted right by kv_shift it counts the cache's).
+#include <type_traits>
+
 #include "cache_ops.h"
 #include "cache_ptx.cuh"
 #include "gqa_split.cuh"
@@ -156,8 +158,9 @@ __device__ __forceinline__ uint32_t f4_scale(uint32_t x, uint32_t s, int high) {
 // `threads` threads (a whole number of warps, this one the `tid`-th, meeting at named
 // barrier `bar`) merge the n <= 32 pieces of `unit` in slots slot0, slot0 + stride, .. into
 // the output (to < 0) or one piece in slot `to`, which may be the first of them: a warp
-// takes a row's LSEs, one piece a lane, for the weights; the threads' loads of the
+// takes a row's LSEs, or four rows' of few pieces, one piece a lane, for the weights; the threads' loads of the
 // pieces' O, kLoads at a time, are in flight meanwhile. `scr`: shared memory, free.
+template <int NT>
 __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int64_t slot0, int stride, int n, int64_t to,
                                       int G, float *scr, int tid, int threads, int bar) {
   constexpr int kLoads = 8;
@@ -171,27 +174,37 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int64_t slot
   const int64_t step = (int64_t)stride * nout;
   const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
   const int64_t row0 = (int64_t)b * p.num_q_heads + h * G;
-  auto lse_of = [&](int g) {
-    return lane < n && g < G ? __ldcg(p.lse_part + (slot0 + lane * stride) * G + g) : neg_inf();
-  };
-  float ahead = lse_of(warp);
-  for (int g = warp; g < G; g += threads / 32) {
-    const float l = ahead;
-    ahead = lse_of(g + threads / 32);
-    float M = l;
+  auto weights = [&](auto lanes) {  // `lanes` lanes a row
+    constexpr int kLanes = decltype(lanes)::value;
+    const int sub = lane & (kLanes - 1), rows = threads / kLanes;
+    auto lse_of = [&](int g) {
+      return sub < n && g < G ? __ldcg(p.lse_part + (slot0 + sub * stride) * G + g) : neg_inf();
+    };
+    float ahead = lse_of(tid / kLanes);
+    for (int g0 = 0; g0 < G; g0 += rows) {
+      const int g = g0 + tid / kLanes;
+      if (kLanes == 32 && g >= G) break;
+      const float l = ahead;
+      ahead = lse_of(g + rows);
+      float M = l;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    const float e = l == neg_inf() ? 0.f : ex2((l - M) * 1.4426950408889634f);
-    float sum = e;
+      for (int o = kLanes / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      const float e = l == neg_inf() ? 0.f : ex2((l - M) * 1.4426950408889634f);
+      float sum = e;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    w[g * 32 + lane] = sum == 0.f ? 0.f : e / sum;
-    if (lane == 0) {
-      const float lse = sum == 0.f ? neg_inf() : M + __log2f(sum) * 0.69314718055994531f;
-      if (to >= 0) lse_to[g] = lse;
-      else if (p.lse) p.lse[row0 + g] = lse;
+      for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (kLanes < 32 && g >= G) continue;
+      w[g * 32 + sub] = sum == 0.f ? 0.f : e / sum;
+      if (sub == 0) {
+        const float lse = sum == 0.f ? neg_inf() : M + __log2f(sum) * 0.69314718055994531f;
+        if (to >= 0) lse_to[g] = lse;
+        else if (p.lse) p.lse[row0 + g] = lse;
+      }
     }
-  }
+  };
+  // (more rows than a pass of warps takes, 16 rows of 1000..20000 tokens: 75.4 -> 74.4 us)
+  if (NT == 2 && n <= 8) weights(std::integral_constant<int, 8>());
+  else weights(std::integral_constant<int, 32>());
   // (items are warp-uniform in number: nout * parts is a multiple of 32)
   bool met = false;
   for (int item = tid; item < nout * parts; item += threads) {
@@ -1122,7 +1135,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     constexpr int kHalf = (W + 1) / 2 * 32;
     const bool both = one0 && one1;
     const int mine = both ? (int)threadIdx.x / kHalf : 0, slot = (both ? mine : one0 ? 0 : 1) ? 28 : 24;
-    f4_merge(p, flags[slot], (int64_t)flags[slot] + flags[slot + 1], 1, flags[slot + 2], -1, G, scr + mine * 4096,
+    f4_merge<NT>(p, flags[slot], (int64_t)flags[slot] + flags[slot + 1], 1, flags[slot + 2], -1, G, scr + mine * 4096,
              (int)threadIdx.x - mine * kHalf, both ? kHalf : C::kThreads, 1 + mine);
     __syncthreads();
   }
@@ -1132,7 +1145,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     const int64_t slot0 = (int64_t)unit + cf;
     const int K = merge_group_size(ns), ng = (ns + K - 1) / K, gs = min(K, ns - q * K);
     const int64_t first = slot0 + (int64_t)q * K;
-    f4_merge(p, unit, first, 1, gs, first, G, scr, (int)threadIdx.x, C::kThreads, 1);
+    f4_merge<NT>(p, unit, first, 1, gs, first, G, scr, (int)threadIdx.x, C::kThreads, 1);
     __syncthreads();
     if (threadIdx.x == 0)
       *last_group = atomic_add_acq_rel_gpu(p.counters + unit, 1u) == (unsigned)(ng - 1) ? 1 : 0;
@@ -1140,7 +1153,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     if (*last_group) {
       uint32_t *gc = p.counters + U + (int64_t)unit * max_merge_groups(gridDim.x);
       for (int i = threadIdx.x; i < ng; i += C::kThreads) gc[i] = 0u;
-      f4_merge(p, unit, slot0, K, ng, -1, G, scr, (int)threadIdx.x, C::kThreads, 1);
+      f4_merge<NT>(p, unit, slot0, K, ng, -1, G, scr, (int)threadIdx.x, C::kThreads, 1);
     }
     __syncthreads();
   }
