@@ -438,3 +438,36 @@ def test_refusals():
     with pytest.raises(ValueError):
         c.eng.gather(t | dict(k_out=t["k_new"][:4], v_out=t["v_new"]))
     assert c.eng.errors() == 0
+
+
+@pytest.mark.parametrize("n,hq,hkv", [(60, 32, 8), (1201, 15, 5), (3001, 32, 8), (3001, 6, 3), (10001, 8, 1)])
+def test_many_tokens_in_one_part_and_in_several(n, hq, hkv):
+    # a token's heads in as many parts as a wave of warps holds, in two, and whole
+    c = Cache("bf16", hq, hkv, page=64, pages=160)
+    t = make_inputs(c, n, rot=128, axes=3, fused=True, seed=n)
+    slots, live, turned = check_append(c, t, rot=128, pair_axis=axis_of(128, 3, False), adjacent=False)
+    want, size = turned(t["k_new"])
+    near_bf16(c.values("k", slots), want[live], size[live])
+
+
+@pytest.mark.parametrize("kind", ["fp4", "int4x4", "token", "bf16"])
+@pytest.mark.parametrize("n,hkv", [(1, 1), (3, 5), (1000, 3), (15001, 1), (30001, 2)])
+def test_read_back_of_few_and_of_many_rows(kind, n, hkv):
+    # two tokens a warp: odd numbers of them, one of the two a padded one
+    c = Cache(kind, hkv, hkv, page=32, pages=20)
+    t = make_inputs(c, 500, rot=64, axes=1, fused=False, seed=hkv)
+    c.eng.append(t | c.t)
+    gen = torch.Generator().manual_seed(n)
+    pick = t["slot_map"].cpu()
+    slots = pick[torch.randint(0, len(pick), (n,), generator=gen)]
+    slots[torch.rand(n, generator=gen) < 0.1] = -1
+    out = {k: torch.full((n, hkv, 128), 99.0, dtype=torch.bfloat16, device="cuda") for k in ("k_out", "v_out")}
+    c.eng.gather(c.t | out | dict(slot_map=slots.cuda()))
+    torch.cuda.synchronize()
+    assert c.eng.errors() == 0
+    live = slots >= 0
+    for name in ("k", "v"):
+        got = out[name + "_out"].cpu().double()
+        want = c.values(name, slots[live])
+        assert (got[~live] == 99.0).all()
+        assert ((got[live] - want).abs() <= 2.0 ** -8 * (1 + 2.0 ** -14) * want.abs() + 2.0 ** -120).all()
