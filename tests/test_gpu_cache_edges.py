@@ -161,3 +161,40 @@ def test_one_row_of_many_new_tokens():
     assert torch.equal(t["positions"].long(), pos)
     assert torch.equal(table[0, 1:1 + used], free[:pages - 1].flip(0)[:used])
     assert torch.equal(t["slot_map"], table[0, pos // page].long() * page + pos % page)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n", [1, 40, 3000])
+def test_every_call_reads_what_the_one_before_wrote(kind, n):
+    """The same rows written and read back over and over, nothing waited for in between: a call
+    that starts early must not see what an SM had of a row from the call before the last."""
+    steps, hkv = 60, 2
+    dtype = da.DA_DTYPE_BF16 if kind == "bf16" else da.DA_DTYPE_FP8_E4M3
+    eng = da.DecodeAttention(device=0, batch=1, num_q_heads=2, num_kv_heads=hkv, head_dim_qk=128, head_dim_v=128,
+                             q_dtype=da.DA_DTYPE_BF16, kv_dtype=dtype, kv_layout=da.DA_KV_PAGED, page_size=16,
+                             num_pages=200, max_pages_per_seq=200, max_seq_len=3200)
+    kb, vb, _ = eng._cache_sizes()
+    cache = dict(k=torch.zeros(kb, dtype=torch.uint8, device="cuda"), v=torch.zeros(vb, dtype=torch.uint8, device="cuda"))
+    if kind != "bf16":
+        cache |= dict(k_scale=torch.ones(hkv, device="cuda"), v_scale=torch.ones(hkv, device="cuda"))
+    value = [(1 + i % 16) * (-1) ** (i // 16) for i in range(steps)]  # exact in e4m3
+    x = torch.tensor(value, dtype=torch.bfloat16, device="cuda")[:, None, None, None].expand(steps, n, hkv, 128).contiguous()
+    maps = [torch.randperm(3200, generator=torch.Generator().manual_seed(s))[:n].cuda() for s in range(2)]
+    out = torch.zeros(2, steps, n, hkv, 128, dtype=torch.bfloat16, device="cuda")
+
+    def loop():
+        for i in range(steps):
+            slots = maps[i % 3 == 0]
+            eng.append(cache | dict(k_new=x[i], v_new=-x[i], slot_map=slots))
+            eng.gather(cache | dict(slot_map=slots, k_out=out[0, i], v_out=out[1, i]))
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        loop()
+    for go in (loop, graph.replay, graph.replay):
+        out.zero_()
+        go()
+        torch.cuda.synchronize()
+        assert eng.errors() == 0
+        assert torch.equal(out[0], x) and torch.equal(out[1], -x)
