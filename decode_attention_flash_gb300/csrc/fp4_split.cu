@@ -169,7 +169,10 @@ __device__ __noinline__ void f4_merge(const GqaParams &p, int unit, int64_t slot
   float *w = scr;                                          // [G][32] weights over their sum
   float *lse_to = scr + G * 32;                            // [16] of the piece (its slot is still read)
   float4 *acc = reinterpret_cast<float4 *>(scr + G * 32 + 16);  // [parts][nout]
-  const int parts = max(1, min(threads / nout, n));        // threads that share an output
+  // sums of every parts-th piece that an output is the sum of: as many as the whole block has
+  // threads for, also where half of it merges (a half then takes two rounds). The order of the
+  // sum must not follow from whether this block came last for one unit or for two.
+  const int parts = max(1, min(F4<NT>::kThreads / nout, n));
   const float4 *src = reinterpret_cast<const float4 *>(p.o_part + slot0 * G * kD);
   const int64_t step = (int64_t)stride * nout;
   const int b = unit / p.num_kv_heads, h = unit - b * p.num_kv_heads;
