@@ -18,7 +18,10 @@ __device__ __forceinline__ uint32_t ld_acquire_cta(const uint32_t *p) {
 // ---------------------------------------------------------------- dependent launches
 // Kernels launched with launch_dependent (cache_ops.h) may start while the previous
 // kernel of the stream is still running: nothing that it may have written is read,
-// and nothing at all is written, before this returns.
+// and nothing at all is written, before this returns. They are alive while that kernel
+// writes, so what a kernel of a serving step may write (slots, positions, tables, queries,
+// cache rows) is read by ordinary loads, which the wait orders; __ldg, whose memory nobody may
+// write during a kernel's life, takes constants alone: cosines, head scales, masks.
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next kernel of the stream start its blocks (they wait as above).
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }

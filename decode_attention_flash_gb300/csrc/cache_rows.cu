@@ -213,7 +213,7 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_
 // Slot of token t, checked: -1 for padding (and, with the error bit, for a slot outside the cache).
 __device__ __forceinline__ int64_t load_slot(const CacheRowParams &p, int64_t t, uint32_t &err) {
   if (!p.slot_map) return -1;
-  const int64_t s = __ldg(p.slot_map + t);
+  const int64_t s = p.slot_map[t];
   if (s >= p.num_slots || s < -1) {
     err |= DA_DEVERR_SLOT;
     return -2;
@@ -227,7 +227,7 @@ template <int kPairs>
 __device__ __forceinline__ bool load_turn(const CacheRowParams &p, int64_t t, int pair0, float (&c)[8], float (&s)[8]) {
   const int n = p.rope_pairs;
   if (p.rope_whole) {  // they share an axis: vector loads
-    const int pos = __ldg(p.positions + (int64_t)p.pair_axis[pair0] * p.position_stride + t);
+    const int pos = p.positions[(int64_t)p.pair_axis[pair0] * p.position_stride + t];
     if (pos < 0 || pos >= p.max_position) return false;
     const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + pair0);
     const float4 *row2 = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + n + pair0);
@@ -242,7 +242,7 @@ __device__ __forceinline__ bool load_turn(const CacheRowParams &p, int64_t t, in
   bool ok = true;
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {
-    const int pos = __ldg(p.positions + (int64_t)p.pair_axis[pair0 + i] * p.position_stride + t);
+    const int pos = p.positions[(int64_t)p.pair_axis[pair0 + i] * p.position_stride + t];
     const bool in = pos >= 0 && pos < p.max_position;
     ok = ok && in;
     c[i] = in ? __ldg(p.cos_sin + (int64_t)pos * 2 * n + pair0 + i) : 1.f;
@@ -318,8 +318,8 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
     for (int k = 0; k < kDeep; ++k) {
       const int hd = (g + k) * kHeads + sub;
       if (g + k < gq1 && hd < HQ) {
-        a[k] = __ldg(qsrc + hd * kChunks + ca);
-        b[k] = __ldg(qsrc + hd * kChunks + cb);
+        a[k] = qsrc[hd * kChunks + ca];
+        b[k] = qsrc[hd * kChunks + cb];
       }
     }
   };
@@ -362,12 +362,13 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
     if (part != p.parts - 1) return;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + lane;
     uint4 *dst = reinterpret_cast<uint4 *>(p.k) + slot * 64 + lane;
-    const uint4 x = __ldg(src), y = __ldg(src + 32);
+    const uint4 x = src[0], y = src[32];
+    const uint4 *rope = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride);
+    uint4 u, v;
+    if (lane < kLanes) u = rope[ca], v = rope[cb];
     dst[0] = x;
     dst[32] = y;
     if (lane < kLanes) {
-      const uint4 *rope = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride);
-      uint4 u = __ldg(rope + ca), v = __ldg(rope + cb);
       if (split) {
         turn_halves(u, v, c, s);
       } else if (turned) {
@@ -409,8 +410,8 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
         w[i] = u[i] = make_uint4(0u, 0u, 0u, 0u);
         sk[i] = sv[i] = 1.f;
         if (g + i < g1 && h + 2 * i < HK) {
-          w[i] = __ldg(ksrc + 32 * i);
-          u[i] = __ldg(vsrc + 32 * i);
+          w[i] = ksrc[32 * i];
+          u[i] = vsrc[32 * i];
           if (KIND == kE4m3 || KIND == kFp4) {
             sk[i] = __ldg(p.k_scale + h + 2 * i);
             sv[i] = __ldg(p.v_scale + h + 2 * i);
@@ -463,15 +464,15 @@ __device__ __forceinline__ RowBits get_row(const uint8_t *src, const uint8_t *ss
   RowBits r;
   r.a = make_uint4(0u, 0u, 0u, 0u);
   r.s = 0;
-  if (KIND == kBf16) r.a = __ldg(reinterpret_cast<const uint4 *>(src));
+  if (KIND == kBf16) r.a = *reinterpret_cast<const uint4 *>(src);
   if (KIND == kE4m3 || KIND == kE4m3Token) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(src));
+    const uint2 v = *reinterpret_cast<const uint2 *>(src);
     r.a.x = v.x;
     r.a.y = v.y;
   }
-  if (KIND == kInt4 || KIND == kFp4) r.a.x = __ldg(reinterpret_cast<const uint32_t *>(src));
-  if (KIND == kInt4 || KIND == kE4m3Token) r.s = __ldg(reinterpret_cast<const uint32_t *>(ssrc));
-  if (KIND == kFp4) r.s = __ldg(ssrc);
+  if (KIND == kInt4 || KIND == kFp4) r.a.x = *reinterpret_cast<const uint32_t *>(src);
+  if (KIND == kInt4 || KIND == kE4m3Token) r.s = *reinterpret_cast<const uint32_t *>(ssrc);
+  if (KIND == kFp4) r.s = *ssrc;
   return r;
 }
 template <int KIND>
@@ -531,9 +532,9 @@ __global__ void __launch_bounds__(kWarps * 32) gather_kernel(const __grid_consta
   if (KIND == kLatent) {  // 512 + 64 elements: 72 chunks of 16 bytes
     const uint4 *ck = reinterpret_cast<const uint4 *>(p.k) + slot * 64;
     uint4 *ok = reinterpret_cast<uint4 *>(p.k_out) + t * 64;
-    const uint4 a = __ldg(ck + lane), b = __ldg(ck + 32 + lane);
+    const uint4 a = ck[lane], b = ck[32 + lane];
     if (lane < 8) {
-      const uint4 c = __ldg(reinterpret_cast<const uint4 *>(p.v) + slot * 8 + lane);
+      const uint4 c = reinterpret_cast<const uint4 *>(p.v)[slot * 8 + lane];
       *(reinterpret_cast<uint4 *>(p.v_out) + t * 8 + lane) = c;
     }
     ok[lane] = a;

@@ -401,9 +401,9 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
     auto load_id = [&](int e) -> int {
       if (e >= nent) return -1;
       if (sparse)
-        return e < x.nbp ? __ldg(p.kv_idx + (int64_t)x.trow * p.max_sparse_blocks + e)
-                         : __ldg(p.kv_full_idx + (int64_t)x.trow * p.max_sparse_blocks + e - x.nbp);
-      return __ldg(p.block_table + (int64_t)x.b * p.max_pages + e);
+        return e < x.nbp ? p.kv_idx[(int64_t)x.trow * p.max_sparse_blocks + e]
+                         : p.kv_full_idx[(int64_t)x.trow * p.max_sparse_blocks + e - x.nbp];
+      return p.block_table[(int64_t)x.b * p.max_pages + e];
     };
     auto load_ids = [&]() {
       id0 = load_id(ent);
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(F4<NT>::kThreads, 1)
               p.q + ((int64_t)b * p.num_q_heads + h * G + (g < G ? g : 0)) * kD + 32 * q4);
 #pragma unroll
           for (int s = 0; s < 4; ++s) {
-            const uint4 v = __ldg(src + s);
+            const uint4 v = src[s];
             qw[nt][2 * s] = make_uint2(v.x, v.y);
             qw[nt][2 * s + 1] = make_uint2(v.z, v.w);
           }

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
 
   auto served = [&](int64_t ahead, int64_t need) { return need == 0 || ahead + need <= nf; };
   auto free_id = [&](int64_t a) -> int {  // the a-th page taken
-    const int id = __ldg(p.free_pages + (nf - 1 - a));
+    const int id = p.free_pages[nf - 1 - a];
     if (id < 0 || id >= p.num_pages) {
       err |= DA_DEVERR_PAGE_INDEX;
       return -1;
