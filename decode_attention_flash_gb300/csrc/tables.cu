@@ -30,7 +30,9 @@ struct Row {
   int64_t first, need;      // pages it has, pages it needs
 };
 
-__device__ __forceinline__ Row row_of(const TableParams &p, int b, uint32_t &err) {
+// Row b, `at` tokens behind the first: those that neither its capacity nor the slot map holds
+// are not among the ones that fit, so no length counts a position that nothing was written to.
+__device__ __forceinline__ Row row_of(const TableParams &p, int b, int64_t at, uint32_t &err) {
   Row r;
   int64_t o = p.seq_lens[b], a = p.new_lens[b];
   if (o < 0 || o > p.capacity) {
@@ -48,6 +50,7 @@ __device__ __forceinline__ Row row_of(const TableParams &p, int b, uint32_t &err
     err |= DA_DEVERR_SEQ_LEN;
     r.nw = p.capacity - o;
   }
+  r.nw = max((int64_t)0, min(r.nw, p.slot_capacity - at));
   r.first = r.need = 0;
   if (p.paged) {
     const uint32_t P = (uint32_t)p.page_size;
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   }
   int64_t tok = 0, pg = 0;
   for (int b = b0; b < b1; ++b) {
-    const Row r = row_of(p, b, err);
+    const Row r = row_of(p, b, 0, err);
     tok += r.asked;
     pg += r.need;
   }
@@ -108,7 +111,28 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   s_pg[tid + 1] = ip;
   if (tid == 0) s_tok[0] = s_pg[0] = 0;
   __syncthreads();
-  const int64_t total = s_tok[kThreads], pages = s_pg[kThreads];
+  const int64_t total = s_tok[kThreads];
+  if (total > p.slot_capacity) {  // fewer pages than counted: the scan again, tokens cut off
+    uint32_t ignored = 0;
+    int64_t at = s_tok[tid];
+    ip = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Row r = row_of(p, b, at, ignored);
+      at += r.asked;
+      ip += r.need;
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, ip, o);
+      if (lane >= o) ip += y;
+    }
+    if (lane == 31) w_pg[warp] = ip;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) ip += w_pg[w];
+    s_pg[tid + 1] = ip;
+    __syncthreads();
+  }
+  const int64_t pages = s_pg[kThreads];
 
   auto served = [&](int64_t ahead, int64_t need) { return need == 0 || ahead + need <= nf; };
   auto free_id = [&](int64_t a) -> int {  // the a-th page taken
@@ -140,11 +164,11 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
       int64_t at = s_tok[c], ahead = s_pg[c];
       int b = c * per;
       uint32_t ignored = 0;
-      Row r = row_of(p, b, ignored);
+      Row r = row_of(p, b, at, ignored);
       while (i >= at + r.asked) {
         at += r.asked;
         ahead += r.need;
-        r = row_of(p, ++b, ignored);
+        r = row_of(p, ++b, at, ignored);
       }
       row = b;
       const int64_t k = i - at;
@@ -175,13 +199,14 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   // ---- new table entries
   for (int64_t a = start; a < pages; a += stride) {
     const int c = find(s_pg, a);
-    int64_t ahead = s_pg[c];
+    int64_t at = s_tok[c], ahead = s_pg[c];
     int b = c * per;
     uint32_t ignored = 0;
-    Row r = row_of(p, b, ignored);
+    Row r = row_of(p, b, at, ignored);
     while (a >= ahead + r.need) {
+      at += r.asked;
       ahead += r.need;
-      r = row_of(p, ++b, ignored);
+      r = row_of(p, ++b, at, ignored);
     }
     if (served(ahead, r.need)) {
       const int id = free_id(a);
@@ -204,7 +229,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   if (mine) {
     int64_t at = s_tok[tid], ahead = s_pg[tid], used = 0;
     for (int b = b0; b < b1; ++b) {
-      const Row r = row_of(p, b, err);
+      const Row r = row_of(p, b, at, err);
       const bool ok = served(ahead, r.need);
       if (!ok) err |= DA_DEVERR_NO_PAGES;
       else if (r.need > 0) used = ahead + r.need;  // (rows served without a page may stand after one refused)

@@ -101,7 +101,7 @@ enum {
   DA_DEVERR_NO_PAGES = 16u,    /* the free pages do not cover a row's new tokens, or num_free
                                   is outside [0, free_capacity]                            */
   DA_DEVERR_SLOT = 32u,        /* a slot outside the cache (token skipped), or more new
-                                  tokens than slot_map holds                               */
+                                  tokens than slot_map holds (left out)                    */
   DA_DEVERR_POSITION = 64u     /* a position outside the cosine table: token skipped       */
 };
 
@@ -427,7 +427,8 @@ typedef struct {
  * b, each row's pages in order of position. A row whose pages are not all there
  * gets no token (its length, its table row and its slots say so, -1) and neither
  * does a later row that needs a page: DA_DEVERR_NO_PAGES. Tokens past the row's
- * capacity get no slot (DA_DEVERR_SEQ_LEN), and a page id outside the pool gives -1
+ * capacity (DA_DEVERR_SEQ_LEN) or past slot_map's end (DA_DEVERR_SLOT) get neither slot nor
+ * page, and no length counts them. A page id outside the pool gives -1
  * (DA_DEVERR_PAGE_INDEX). No output may overlap an input except where said.
  * Errors: INVALID_ARG, UNSUPPORTED (a capacity of 2^31 positions), WORKSPACE,
  * NOT_PLANNED, CUDA.
