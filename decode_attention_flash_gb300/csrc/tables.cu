@@ -6,15 +6,18 @@
 // free stack F[0 .. n): its k-th new page is F[n - 1 - (a_b + k)]. New token i of
 // row b stands at position old + i, in slot page(pos / P) * P + pos % P, where the
 // page is the table's for the pages that the row had and the stack's for the others
-// (so no token waits for the table to be written).
+// (so no token waits for the table to be written). An id outside the pool ends the stack
+// (every block looks all ids over that the rows ask for, the first kThreads of them while the
+// scan runs), so a row has all of its new pages or none, and its length says which.
 //
 // What bounds it. A decode step moves a few KB: latency. So it is one launch,
 // and no block waits for another: every block scans all rows' lengths again (two
 // block scans of a few thousand integers from L2) and then writes its own share of
 // the tokens, of the new table entries and (block 0) of the per-row results;
 // a token finds its row by bisecting the scan, kept per thread in shared memory.
-// 256 rows of one token: 4.9 us, a launch and three dependent loads; 125 000 tokens of
-// 61 rows: 7.9 us (four tokens a thread in fewer blocks: 9.8).
+// 256 rows of one token: 5.0 us, a launch and three dependent loads (4.85 before the ids
+// were looked over); 125 000 tokens of 61 rows: 8.1 us (7.5 before; four tokens a thread in fewer
+// blocks took 1.9 more).
 // Results written over the lengths they came from wait for the block that is last
 // to have read them (a counter in the workspace, back at zero afterwards).
 #include "cache_ops.h"
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   __shared__ int64_t s_tok[kThreads + 1], s_pg[kThreads + 1];
   __shared__ int64_t w_tok[kThreads / 32], w_pg[kThreads / 32];
   __shared__ int64_t s_used;
-  __shared__ int s_last;
+  __shared__ int s_last, s_bad;  // s_bad: depth in the stack of the first id outside the pool
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (p.batch + kThreads - 1) / kThreads;
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
@@ -79,9 +82,11 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
       nf = nf < 0 ? 0 : p.free_capacity;
     }
   }
+  const int top = tid < nf ? p.free_pages[nf - 1 - tid] : 0;
   if (tid == 0) {
     s_used = 0;
     s_last = 1;
+    s_bad = INT32_MAX;
   }
   int64_t tok = 0, pg = 0;
   for (int b = b0; b < b1; ++b) {
@@ -110,6 +115,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
   s_tok[tid + 1] = it;
   s_pg[tid + 1] = ip;
   if (tid == 0) s_tok[0] = s_pg[0] = 0;
+  if ((uint32_t)top >= (uint32_t)p.num_pages && tid < nf) atomicMin(&s_bad, tid);
   __syncthreads();
   const int64_t total = s_tok[kThreads];
   if (total > p.slot_capacity) {  // fewer pages than counted: the scan again, tokens cut off
@@ -133,16 +139,25 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
     __syncthreads();
   }
   const int64_t pages = s_pg[kThreads];
-
-  auto served = [&](int64_t ahead, int64_t need) { return need == 0 || ahead + need <= nf; };
-  auto free_id = [&](int64_t a) -> int {  // the a-th page taken
-    const int id = p.free_pages[nf - 1 - a];
-    if (id < 0 || id >= p.num_pages) {
-      err |= DA_DEVERR_PAGE_INDEX;
-      return -1;
+  const int64_t deep = min(pages, nf);
+  if (deep > kThreads) {
+    constexpr int kLoads = 8;
+    const int32_t *f = p.free_pages + (nf - 1);
+    for (int64_t a = kThreads + tid; a < deep; a += kLoads * kThreads) {
+      int id[kLoads];
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k) id[k] = a + k * kThreads < deep ? f[-(a + k * kThreads)] : 0;
+#pragma unroll
+      for (int k = 0; k < kLoads; ++k)
+        if ((uint32_t)id[k] >= (uint32_t)p.num_pages) atomicMin(&s_bad, (int)a + k * kThreads);
     }
-    return id;
-  };
+    __syncthreads();
+  }
+  const int64_t usable = min(nf, (int64_t)s_bad);
+  if (s_bad < deep) err |= DA_DEVERR_PAGE_INDEX;
+
+  auto served = [&](int64_t ahead, int64_t need) { return need == 0 || ahead + need <= usable; };
+  auto free_id = [&](int64_t a) { return p.free_pages[nf - 1 - a]; };  // the a-th page taken (of a row that is served)
   // the thread whose rows hold item i of a prefix array
   auto find = [&](const int64_t *s, int64_t i) {
     int lo = 0, hi = kThreads;
@@ -208,10 +223,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
       ahead += r.need;
       r = row_of(p, ++b, at, ignored);
     }
-    if (served(ahead, r.need)) {
-      const int id = free_id(a);
-      if (id >= 0) p.block_table[(int64_t)b * p.max_pages + r.first + (a - ahead)] = id;
-    }
+    if (served(ahead, r.need)) p.block_table[(int64_t)b * p.max_pages + r.first + (a - ahead)] = free_id(a);
   }
   // ---- per-row results: block 0, or the last block to have read the lengths
   bool mine = blockIdx.x == 0;
@@ -231,8 +243,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const TableParams p) {
     for (int b = b0; b < b1; ++b) {
       const Row r = row_of(p, b, at, err);
       const bool ok = served(ahead, r.need);
-      if (!ok) err |= DA_DEVERR_NO_PAGES;
-      else if (r.need > 0) used = ahead + r.need;  // (rows served without a page may stand after one refused)
+      if (!ok && ahead + r.need > nf) err |= DA_DEVERR_NO_PAGES;
+      if (ok && r.need > 0) used = ahead + r.need;  // (rows served without a page may stand after one refused)
       if (p.cu_new) p.cu_new[b] = (int32_t)min(at, (int64_t)INT32_MAX);
       p.seq_lens_out[b] = (int32_t)(ok ? r.old + r.nw : r.old);
       at += r.asked;

@@ -428,8 +428,10 @@ typedef struct {
  * gets no token (its length, its table row and its slots say so, -1) and neither
  * does a later row that needs a page: DA_DEVERR_NO_PAGES. Tokens past the row's
  * capacity (DA_DEVERR_SEQ_LEN) or past slot_map's end (DA_DEVERR_SLOT) get neither slot nor
- * page, and no length counts them. A page id outside the pool gives -1
- * (DA_DEVERR_PAGE_INDEX). No output may overlap an input except where said.
+ * page, and no length counts them. An id outside the pool ends the stack for the rows that
+ * ask for it, as if no page lay below (DA_DEVERR_PAGE_INDEX); one in the table gives the
+ * tokens of its page no slot (DA_DEVERR_PAGE_INDEX), and the length counts them, as
+ * decode_attn_run skips such a page and reports it too. No output may overlap an input except where said.
  * Errors: INVALID_ARG, UNSUPPORTED (a capacity of 2^31 positions), WORKSPACE,
  * NOT_PLANNED, CUDA.
  */

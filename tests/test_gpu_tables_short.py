@@ -1,4 +1,5 @@
-"""Block tables when something runs out or is wrong: a slot map too small for the new tokens.
+"""Block tables when something runs out or is wrong: a slot map too small for the new tokens,
+ids outside the pool on the stack of free pages.
 Whatever a row does not get, its length must not count: the decode reads every position
 that a length counts."""
 
@@ -11,17 +12,17 @@ from test_gpu_tables import case, engine, i32
 pytestmark = pytest.mark.gpu
 
 
-def plain(old, new, page, table, free, cap, slot_capacity):
+def plain(old, new, page, table, free, cap, slot_capacity, pages=1 << 30):
     """The definition, one token at a time: a row takes the tokens that its capacity and the slot
-    map hold, and the pages for those; a row that misses a page takes none, nor does a later row
-    that needs one."""
+    map hold, and the pages for those; a row that misses a page, or would get one that is none,
+    takes nothing, nor does a later row that needs a page."""
     table = [list(r) for r in table]
     free = list(free)
     out, slots, cu, closed = [], [], [0], False
     for b, (o, n) in enumerate(zip(old, new)):
         fits = min(n, cap - o, max(0, slot_capacity - len(slots)))
         need = -(-(o + fits) // page) - -(-o // page)
-        ok = need == 0 or (not closed and need <= len(free))
+        ok = need == 0 or (not closed and need <= len(free) and all(0 <= x < pages for x in free[-need:]))
         closed = closed or not ok
         if ok:
             for k in range(need):
@@ -77,6 +78,44 @@ def test_lengths_leave_out_what_the_slot_map_does_not_hold(batch, new_hi, spare,
             assert want[2] != got
             got, have, tab = want[2], want[1], want[0]
         assert len(have) == len(free) - sum(-(-(o + n) // 16) - -(-o // 16) for o, n in zip(old, new))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("batch,new_hi,spare", [(1, 50, 3), (1, 40000, 700), (7, 300, 5), (61, 90, 5), (61, 900, -20), (700, 40, 5)])
+@pytest.mark.parametrize("where", [0.0, 0.2, 0.7, 1.0])
+@pytest.mark.parametrize("bad", [-1, 1 << 30, "pool"])
+def test_an_id_outside_the_pool_ends_the_stack(batch, new_hi, spare, where, bad, in_place):
+    old, new, table, free, cols, pages = case(batch, batch, 16, 40, new_hi, spare)
+    new[0] = new[0] or 1
+    need = sum(-(-(o + n) // 16) - -(-o // 16) for o, n in zip(old, new))
+    depth = min(int(where * need), len(free) - 1)  # (at 1.0 nobody asks for it, or it is the last there is)
+    free[len(free) - 1 - depth] = pages if bad == "pool" else bad
+    eng = engine(batch, 16, cols, pages)
+    want = plain(old, new, 16, table, free, cols * 16, sum(new), pages)
+    t, err = call(eng, old, new, table, free, sum(new), in_place)
+    ask = depth < min(need, len(free))
+    assert err == (da.DA_DEVERR_PAGE_INDEX if ask else 0) | (da.DA_DEVERR_NO_PAGES if need > len(free) else 0)
+    same(t, want)
+    if not ask and need <= len(free):
+        assert want[2] == [o + n for o, n in zip(old, new)]
+
+
+def test_a_decode_behind_a_bad_id_reads_no_other_row():
+    """Row 1's new page is no page: its table entry, of an earlier request, must not be read."""
+    eng = da.DecodeAttention(device=0, batch=2, num_q_heads=1, num_kv_heads=1, head_dim_qk=128, head_dim_v=128,
+                             kv_layout=da.DA_KV_PAGED, page_size=16, num_pages=8, max_pages_per_seq=2, max_seq_len=32,
+                             q_dtype=da.DA_DTYPE_BF16, kv_dtype=da.DA_DTYPE_BF16)
+    lens, table = i32([0, 0]), i32([[3, 3], [3, 3]])
+    t = dict(seq_lens=lens, seq_lens_out=lens, new_lens=i32([1, 1]), free_pages=i32([5, 8, 4]), num_free=i32([3]),
+             num_free_out=i32([0]), block_table=table, slot_map=torch.zeros(2, dtype=torch.int64, device="cuda"))
+    eng.build_tables(t)
+    assert eng.errors() == da.DA_DEVERR_PAGE_INDEX
+    assert lens.tolist() == [1, 0] and table[:, 0].tolist() == [4, 3] and t["num_free_out"].item() == 2
+    assert t["slot_map"].tolist() == [64, -1]
+    kv = torch.full((8, 1, 16, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = eng.run(dict(q=torch.ones(2, 1, 128, dtype=torch.bfloat16, device="cuda"), k=kv, v=kv, seq_lens=lens,
+                       block_table=table), 1.0)
+    assert eng.errors() == 0 and (out[0] == 7).all() and (out[1] == 0).all()
 
 
 def test_no_slots_at_all_leave_the_state_as_it_was():
