@@ -508,7 +508,7 @@ da_status decode_attn_get_error(da_ctx *ctx, void *workspace, da_stream_t stream
       auto *ws = reinterpret_cast<uint8_t *>(workspace);
       // every counter (the region between the counters and the partials)
       const size_t nbytes = (size_t)(ctx->plan.partial_o_offset - ctx->plan.counters_offset);
-      if (cudaMemsetAsync(ws + ctx->plan.counters_offset, 0, nbytes, s) != cudaSuccess)
+      if (nbytes && cudaMemsetAsync(ws + ctx->plan.counters_offset, 0, nbytes, s) != cudaSuccess)
         return DA_ERR_CUDA;
     }
     if (cudaStreamSynchronize(s) != cudaSuccess) return DA_ERR_CUDA;

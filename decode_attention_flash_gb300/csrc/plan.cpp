@@ -247,6 +247,13 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
     info->writes_final = whole ? 1 : 0;  // else decided per unit on the device
     int64_t off = kWorkspaceHeader;
     info->counters_offset = off;  // per unit: its counter, then its merge-group counters
+    if (whole && num_splits_override > 0) {
+      // A CTA for every unit counts nothing and writes no piece, and a forced one may have
+      // 65535 of them (gigabytes of pieces). A plan that takes this form by itself, of at most
+      // an SM's worth of units, keeps their room, so that one workspace serves its next lengths.
+      info->partial_o_offset = info->partial_lse_offset = info->workspace_bytes = off;
+      return DA_OK;
+    }
     off = align256(off + units * (1 + max_merge_groups((int)ctas)) * 4);
     info->partial_o_offset = off;  // slots unit + cta
     off = align256(off + (units + ctas) * rows * (int64_t)dv * 4);
