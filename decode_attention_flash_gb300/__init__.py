@@ -357,7 +357,10 @@ def make_append_args(tensors: dict, pair_axis=None, rope_adjacent: bool = False,
         if pair_axis is not None:
             if len(pair_axis) != a.rope_dim // 2:
                 raise ValueError(f"pair_axis must have {a.rope_dim // 2} entries")
-            a._pairs = (ctypes.c_uint8 * len(pair_axis))(*[int(x) for x in pair_axis])
+            axes = [int(x) for x in pair_axis]
+            if any(not 0 <= x <= 255 for x in axes):  # (a byte each; ctypes would wrap them)
+                raise ValueError("pair_axis must name axes of 0..255")
+            a._pairs = (ctypes.c_uint8 * len(axes))(*axes)
             a.pair_axis = ctypes.cast(a._pairs, ctypes.c_void_p)
     return a
 
