@@ -329,7 +329,8 @@ def _token_rows(t, name: str, tokens: int):
 def make_append_args(tensors: dict, pair_axis=None, rope_adjacent: bool = False, q_len: int = 1) -> AppendArgs:
     """Arguments of ``decode_attn_append`` from a dict with the names of the C struct. The number
     of tokens is that of ``slot_map`` (or of ``q``, for queries alone), the rotated dimensions are
-    ``cos_sin``'s width, the axes ``positions``' rows; ``pair_axis`` is a sequence of ints."""
+    ``cos_sin``'s width, the axes ``positions``' rows (a column range of a wider tensor is fine);
+    ``pair_axis`` is a sequence of ints."""
     first = tensors.get("slot_map") if tensors.get("slot_map") is not None else tensors["q"]
     n = first.shape[0]
     a = AppendArgs()
@@ -351,9 +352,13 @@ def make_append_args(tensors: dict, pair_axis=None, rope_adjacent: bool = False,
         if table.dim() != 2 or pos is None or pos.shape[-1] != n or pos.dim() > 2:
             raise ValueError("cos_sin must be [positions, rope_dim] and positions [tokens] or [axes, tokens]")
         a.cos_sin = _typed_ptr(tensors, "cos_sin", torch.float32)
-        a.positions = _typed_ptr(tensors, "positions", torch.int32)
+        # (an axis' positions are contiguous; the axes may be a column range of wider rows)
+        if pos.dtype != torch.int32 or (n > 1 and pos.stride(-1) != 1):
+            raise ValueError("positions must be int32, the tokens of an axis contiguous")
+        a.positions = _ptr(pos.select(0, 0) if pos.dim() == 2 and pos.shape[0] > 0 else pos)
         a.max_position, a.rope_dim = table.shape
-        a.rope_axes, a.position_stride = (pos.shape[0] if pos.dim() == 2 else 1), n
+        a.rope_axes = pos.shape[0] if pos.dim() == 2 else 1
+        a.position_stride = pos.stride(0) if a.rope_axes > 1 else n
         if pair_axis is not None:
             if len(pair_axis) != a.rope_dim // 2:
                 raise ValueError(f"pair_axis must have {a.rope_dim // 2} entries")
