@@ -6,7 +6,9 @@
 
 namespace da {
 
-constexpr int64_t kTicketOffset = 64;  // in the workspace's header: block counter of build_tables, zero between calls
+// The workspace's header (kWorkspaceHeader bytes) is the error word at byte 0 and, in what the
+// decode kernels know as its padding, build_tables' block counter here, zero between calls.
+constexpr int64_t kTicketOffset = 64;
 
 // Decode over the 4-bit float cache (fp4_split.cu): granules of 16 rows, 1152
 // bytes each, read through their addresses; o_head holds, per CTA and warp, the

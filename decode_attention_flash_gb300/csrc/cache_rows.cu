@@ -24,9 +24,13 @@
 // -> 32.8.)
 // Blocks of four warps leave an SM sooner than blocks of eight, so a last wave ends sooner
 // (eight: 62.7, 30.4 and 56.3 us for the three below, two: 62.7, 31.3 and 55.3).
-// Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 62.2 us, 98 % of the
+// At eight blocks an SM the append has 64 registers a thread; every form of it spills a little
+// (4 to 28 bytes). 96 registers and fewer warps took longer: 30.4 -> 33.8 for the e4m3 rows.
+// Measured: 16381 tokens of 32 + 16 heads, three axes, bf16 cache: 62.3 us, 97 % of the
 // copy rate; 4099 tokens of 64 + 16 heads into e4m3 with token scales: 29.7 us (79 %, two
-// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 54.9 us (93 %).
+// thirds of a wave short of two); 65537 4-bit rows of 8 heads read back: 54.8 us (93 %); 2048
+// latent rows with 128 heads: 13.7 us (78 %; the rope key loaded after the latent row is
+// stored: 14.0).
 // K first and then V, with a head's address worked out for each row: 65.2, 31.4 and
 // 61.3 us, bound by instruction issue; one row in flight of K and of V instead of two:
 // 65.2, 31.0 and 70.7.

@@ -43,7 +43,11 @@
 // warps end one after another, 2 for the pieces of a CTA and 4 for units that CTAs
 // share. Measured and not kept: 16 streaming warps with a register split (more
 // instructions: 42.0 -> 45.4 us), shares weighted by scheduler (115 -> 124 us), the walk
-// and the end as functions of their own (42.1 -> 45.5 us).
+// and the end as functions of their own (42.1 -> 45.5 us). Not built: tiles handed to
+// whichever warp has room, against the 4 us in which warps end one after another.
+// 9 to 16 rows a unit (three warps a scheduler, 168 registers, 16 to 18 bytes of spill) are
+// bound by latency, no pipe being full: 16 rows of 1000..20000, 4 query tokens: 74.7 us,
+// floor 28.9, issue 42 %, ALU 32 %.
 //
 // The split. As in gqa_split.cuh the tiles of all (row, kv head) units are laid
 // end to end and cut into equal ranges, one per CTA; a CTA's range is cut again

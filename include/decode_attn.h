@@ -169,7 +169,7 @@ typedef struct {
  *              Element type bf16, or e4m3 bytes when kv_dtype is an e4m3 type;
  *              DA_DTYPE_INT4_GROUPS: int32 rows of kv_groups + D / 8 words.
  *              DA_DTYPE_FP4_E2M1_BLOCKS: granules of 1152 bytes (see da_dtype).
- *              Base addresses 16-byte aligned.
+ *              Base addresses of q, q_pe, k and v 128-byte aligned
  *   k_scale, v_scale  DA_DTYPE_FP8_E4M3 and DA_DTYPE_FP4_E2M1_BLOCKS only: fp32 [HKV];
  *              dequantised value = e4m3 * scale, or e2m1 * block scale * scale
  *   k_scale_shift, v_scale_shift  DA_DTYPE_FP8_E4M3_TOKEN_SCALE only: int32, one word per
@@ -195,7 +195,8 @@ typedef struct {
  *              kernel, SPEC_DEC, for Q <= 32): every position before the row's Q new
  *              ones is attended, and new position N_b - Q + j by query token t when
  *              bit j of word [b][t] is set. NULL: causal (bits 0..t). Ignored for Q = 1
- *   out        bf16 [B][HQ][Dv]    (q_len Q > 1: [B][HQ][Q][Dv])
+ *   out        bf16 [B][HQ][Dv]    (q_len Q > 1: [B][HQ][Q][Dv]); 8-byte aligned (MLA and
+ *              the 4-bit float cache: 16-byte)
  *   lse        fp32 [B][HQ], natural log; may be NULL (q_len Q > 1: [B][HQ][Q])
  *   mask_window, mask_sink  GQA, optional: int32 [HQ] each (mask_sink may be NULL, meaning
  *              0): a mask_mod per query head in the sense of flex attention (which
@@ -269,7 +270,8 @@ da_status decode_attn_create(const da_problem *problem, int device, da_ctx **out
  * lets the planner size splits from the real lengths; without it the plan
  * assumes every row is max_seq_len long. num_splits_override > 0 forces that
  * many splits per unit (positions are cut into equal tile-aligned chunks; a
- * 4-bit float cache takes at most 1024 CTAs in all, or one split).
+ * 4-bit float cache takes at most 1024 CTAs in all, or one split, whose workspace is
+ * 256 bytes).
  * Host-only; no GPU work. Errors: INVALID_ARG.
  */
 da_status decode_attn_plan(da_ctx *ctx, const int32_t *seq_lens_host, int32_t num_splits_override,
@@ -382,7 +384,9 @@ da_status decode_attn_get_error_noalloc(da_ctx *ctx, da_stream_t stream, uint32_
  * those that overlap on the GPU need workspaces of their own; appends and gathers may
  * share one with anything). They only enqueue one kernel on `stream`, which may take
  * its place on the SMs while the stream's previous kernel drains, but reads and writes
- * nothing before that has ended. A slot is one position of the cache: page * page_size + offset, or
+ * nothing before that has ended (what may change between calls it reads by ordinary loads;
+ * cos_sin, the head scales and the masks are constants, and a kernel of the caller's own that
+ * lets its dependents start early must not be writing them). A slot is one position of the cache: page * page_size + offset, or
  * batch row * max_seq_len + position in a contiguous cache.
  */
 
