@@ -24,7 +24,7 @@ __all__ = [
     "decode_attn_get_error_noalloc", "decode_attn_destroy",
     "decode_attn_status_string", "DecodeAttention", "DA_KV_CONTIGUOUS", "DA_KV_PAGED",
     "DA_DTYPE_BF16", "DA_DTYPE_FP8_E4M3", "DA_DTYPE_FP8_E4M3_TOKEN_SCALE", "DA_DTYPE_INT4_GROUPS",
-    "DA_DTYPE_FP4_E2M1_BLOCKS", "TableArgs", "AppendArgs", "GatherArgs", "make_args",
+    "DA_DTYPE_FP4_E2M1_BLOCKS", "DA_DTYPE_FP8_E4M3_BLOCKS", "DA_DTYPE_INT8_BLOCKS", "TableArgs", "AppendArgs", "GatherArgs", "make_args",
     "make_table_args", "make_append_args", "make_gather_args", "decode_attn_build_tables",
     "decode_attn_append", "decode_attn_gather",
 ]
@@ -33,7 +33,7 @@ DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_CUDA = 0, 1, 2, 3
 DA_ERR_WORKSPACE, DA_ERR_NOT_PLANNED, DA_ERR_DEVICE = 4, 5, 6
 DA_KV_CONTIGUOUS, DA_KV_PAGED = 0, 1
 DA_DTYPE_BF16, DA_DTYPE_FP8_E4M3, DA_DTYPE_FP8_E4M3_TOKEN_SCALE, DA_DTYPE_INT4_GROUPS = 0, 1, 2, 3
-DA_DTYPE_FP4_E2M1_BLOCKS = 4
+DA_DTYPE_FP4_E2M1_BLOCKS, DA_DTYPE_FP8_E4M3_BLOCKS, DA_DTYPE_INT8_BLOCKS = 4, 5, 6
 DA_DEVERR_PAGE_INDEX, DA_DEVERR_SPARSE_INDEX, DA_DEVERR_SEQ_LEN, DA_DEVERR_TIMEOUT = 1, 2, 4, 8
 DA_DEVERR_NO_PAGES, DA_DEVERR_SLOT, DA_DEVERR_POSITION = 16, 32, 64
 
@@ -492,7 +492,9 @@ class DecodeAttention:
             if t.numel() * t.element_size() != want:
                 raise ValueError(f"{name} must be a cache of {want} bytes, got {t.numel() * t.element_size()}")
         per_head = p.kv_dtype in (DA_DTYPE_FP8_E4M3, DA_DTYPE_FP4_E2M1_BLOCKS)
-        for name, on, want in (("k_scale", per_head, p.num_kv_heads), ("v_scale", per_head, p.num_kv_heads),
+        blocks = p.kv_dtype in (DA_DTYPE_FP8_E4M3_BLOCKS, DA_DTYPE_INT8_BLOCKS)
+        scales = slots // p.kv_groups * p.num_kv_heads if blocks else p.num_kv_heads
+        for name, on, want in (("k_scale", per_head or blocks, scales), ("v_scale", per_head or blocks, scales),
                                ("k_scale_shift", p.kv_dtype == DA_DTYPE_FP8_E4M3_TOKEN_SCALE, slots * p.num_kv_heads),
                                ("v_scale_shift", p.kv_dtype == DA_DTYPE_FP8_E4M3_TOKEN_SCALE, slots * p.num_kv_heads)):
             if on and (tensors.get(name) is None or tensors[name].numel() != want):

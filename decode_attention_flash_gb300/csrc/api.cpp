@@ -17,7 +17,7 @@ struct da_ctx {
   int smem_per_sm;
   bool planned;
   da_plan_info plan;
-  int32_t few_tiles, few_ctas;  // of a 4-bit float cache's plan (Fp4Params)
+  int32_t few_tiles, few_ctas;  // of a plan for a cache in granules (StreamParams)
   // tensor maps are re-encoded only when the cache base pointers change
   const void *map_k_base;
   const void *map_v_base;
@@ -209,7 +209,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   const bool fp8 = p.kv_dtype != DA_DTYPE_BF16;
   const bool token_scale = p.kv_dtype == DA_DTYPE_FP8_E4M3_TOKEN_SCALE;
   const bool int4 = p.kv_dtype == DA_DTYPE_INT4_GROUPS;  // takes the f16 (fp8) kernel path
-  const bool fp4 = p.kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS;  // fp4_split.cu: no tensor maps
+  const bool granules = da::is_stream(p);  // stream_split.cuh: no tensor maps
   const bool paged = p.kv_layout == DA_KV_PAGED;
   const bool sparse = p.sparse_block_size > 0;
   if (!a->q || !a->k || !a->v || !a->seq_lens || !a->out) return DA_ERR_INVALID_ARG;
@@ -221,7 +221,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   if (token_scale && (!a->k_scale_shift || !a->v_scale_shift || !aligned(a->k_scale_shift, 16) ||
                       !aligned(a->v_scale_shift, 16)))
     return DA_ERR_INVALID_ARG;
-  if (!aligned(a->k, 128) || !aligned(a->v, 128) || !aligned(a->q, 128) || !aligned(a->out, fp4 ? 16 : 8))
+  if (!aligned(a->k, 128) || !aligned(a->v, 128) || !aligned(a->q, 128) || !aligned(a->out, granules ? 16 : 8))
     return DA_ERR_INVALID_ARG;
 
   const uint64_t rows = paged ? (uint64_t)p.num_pages * p.num_kv_heads * p.page_size
@@ -231,7 +231,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   // R = G x Q consecutive rows of q viewed as [B * HQ * Q][D]
   const int Q = p.q_len > 1 ? p.q_len : 1;
   const int R = p.num_q_heads / p.num_kv_heads * Q;
-  if (!fp4 && (ctx->map_k_base != a->k || ctx->map_v_base != a->v || ctx->map_q_base != a->q)) {
+  if (!granules && (ctx->map_k_base != a->k || ctx->map_v_base != a->v || ctx->map_q_base != a->q)) {
     ctx->map_k_base = ctx->map_v_base = ctx->map_q_base = nullptr;
     da_status st;
     if (int4) {
@@ -312,18 +312,25 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   gp.fp8_mma = p.fp8_mma;
   gp.test_stall_ns = ctx->test_stall_ns;
   ctx->test_stall_ns = 0;  // one call only
-  if (fp4) {
-    da::Fp4Params f;
+  if (granules) {
+    da::StreamParams f;
+    std::memset(&f, 0, sizeof f);
     f.g = gp;
     f.k = reinterpret_cast<const uint8_t *>(a->k);
     f.v = reinterpret_cast<const uint8_t *>(a->v);
-    f.o_head = reinterpret_cast<float *>(ws + da::fp4_head_offset(pl));
-    f.kv_shift = da::fp4_kv_shift(p);
+    f.o_head = reinterpret_cast<float *>(ws + da::stream_head_offset(pl));
+    f.kv_shift = da::stream_kv_shift(p);
     f.g.num_kv_heads <<= f.kv_shift;
     f.g.group >>= f.kv_shift;
     f.whole = pl.writes_final;
     f.few_tiles = ctx->few_tiles;
     f.few_ctas = ctx->few_ctas;
+    if (da::is_block8(p)) {
+      f.scale_shift = 11;  // granules of 2048 bytes
+      for (int n = p.kv_groups; n > 16; n /= 2) ++f.scale_shift;
+      return da::launch_block8(f, p.kv_dtype == DA_DTYPE_INT8_BLOCKS, pl.grid_x, stream) == cudaSuccess ? DA_OK
+                                                                                                        : DA_ERR_CUDA;
+    }
     return da::launch_fp4(f, pl.grid_x, stream) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
   }
   if (da::launch_gqa(fp8, gp.group, ctx->kmap, ctx->vmap, ctx->qmap,
@@ -408,6 +415,7 @@ da_status decode_attn_create(const da_problem *problem, int device, da_ctx **out
   if (cudaGetDevice(&prev) != cudaSuccess) return DA_ERR_CUDA;
   if (cudaSetDevice(device) != cudaSuccess) return DA_ERR_CUDA;
   cudaError_t e = problem->is_mla ? da::mla_prepare(device)
+                  : da::is_block8(*problem) ? da::block8_prepare()
                   : problem->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS ? da::fp4_prepare()
                                                                   : da::gqa_prepare(device);
   cudaSetDevice(prev);
@@ -432,8 +440,8 @@ da_status decode_attn_plan_ex(da_ctx *ctx, const int32_t *seq_lens_host,
                                   kv_num_blks_host, num_splits_override, &info);
   if (st != DA_OK) return st;
   ctx->plan = info;
-  if (ctx->prob.kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS)
-    da::fp4_few(ctx->prob, info, seq_lens_host, num_splits_override, &ctx->few_tiles, &ctx->few_ctas);
+  if (da::is_stream(ctx->prob))
+    da::stream_few(ctx->prob, info, seq_lens_host, num_splits_override, &ctx->few_tiles, &ctx->few_ctas);
   ctx->planned = true;
   if (workspace_bytes) *workspace_bytes = (size_t)info.workspace_bytes;
   return DA_OK;

@@ -1,0 +1,263 @@
+// block8_split.cu -- persistent split-KV GQA decode over a cache of 8-bit codes with an fp32 scale
+// for each block of 16 to 256 positions and kv head, for sm_103a.
+//
+// The mathematics. A cached key or value element is code * scale[block]: an e4m3 or a signed
+// integer code, exact in f16. A granule of 16 positions lies in one block, so
+//   S^T = (K codes) Q^T * kscale,   O^T += vscale * (V codes)^T P^T
+// with the products on f16 operands with fp32 sums and the scales applied to them in fp32: any
+// fp32 scale serves, and 16 positions cost 4 + 32 multiplies a lane beside their 16 products.
+//
+// What bounds it. 16 positions of one kv head are 4096 bytes, 732 cycles of a scheduler at the
+// measured copy bandwidth; their conversions, products and weights take about 250. So HBM does.
+// How tiles are walked, cut and merged stands in stream_split.cuh.
+//
+// The stage. Rows of 128 bytes land with their eight 16-byte chunks turned by the row: chunk c of
+// row r at c ^ (r & 7). A quad reads chunks 2 q, 2 q + 1 of a K row (its dims 32 q .. 32 q + 31: the
+// contraction's order is free and Q is read in the same), a lane chunk r of its V rows, both
+// without bank conflicts.
+#include "stream_split.cuh"
+
+namespace da {
+namespace {
+
+// Two pairs of codes (bytes 0, 1 and 2, 3 of w) as f16 pairs, exact. Integers come with 128 added,
+// as bytes below 0x64: 1024 + byte, less 1152.
+template <bool INT>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  if (INT) {
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const uint32_t a = prmt(w, 0x64646464u, 0x4140), b = prmt(w, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), off);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+  } else {
+    lo = e4m3x2_to_f16x2((uint16_t)w);
+    hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
+  }
+}
+template <bool INT>
+__device__ __forceinline__ uint32_t biased(uint32_t w) {
+  return INT ? w ^ 0x80808080u : w;
+}
+__device__ __forceinline__ uint32_t word(const uint4 &v, int c) {
+  return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
+}
+
+template <bool INT>
+struct Block8Format {
+  static constexpr int kT = 32;
+  static constexpr int kH = kT / 16;
+  static constexpr int kGranBytes = 2048;
+  static constexpr int kSideBytes = 16;  // K's scales, then V's
+  static constexpr bool kHeadScales = false;
+  static constexpr bool kCareful = true;
+  static constexpr int kWarps(int) { return 7; }
+  static constexpr int kStages(int) { return 3; }
+  static constexpr bool kQShared(int) { return false; }
+
+  const uint8_t *k_lane, *v_lane;
+  const float *scale;  // lane 0: K's, lane 1: V's
+  int lane, shift, dst, k0, k1, v0, v1;
+  __device__ __forceinline__ Block8Format(const StreamParams &fp, int l)
+      : k_lane(fp.k + l * 16), v_lane(fp.v + l * 16), scale(l == 0 ? fp.g.k_scale : fp.g.v_scale), lane(l),
+        shift(fp.scale_shift) {
+    const int q4 = l & 3, r8 = l >> 2;
+    dst = (l >> 3) * 128 + (((l & 7) ^ (l >> 3)) << 4);  // rows 0 .. 3; rows 4 .. 7: chunks ^ 4
+    k0 = r8 * 128 + (((2 * q4) ^ r8) << 4);
+    k1 = r8 * 128 + (((2 * q4 + 1) ^ r8) << 4);
+    v0 = 2 * q4 * 128 + ((r8 ^ (2 * q4)) << 4);
+    v1 = (2 * q4 + 1) * 128 + ((r8 ^ (2 * q4 + 1)) << 4);
+  }
+  __device__ __forceinline__ void copy(uint32_t k, uint32_t v, int64_t off, uint8_t *scales, int gi) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cp_async_16(k + j * 512 + (dst ^ ((j & 1) << 6)), k_lane + off + j * 512);
+      cp_async_16(v + j * 512 + (dst ^ ((j & 1) << 6)), v_lane + off + j * 512);
+    }
+    if (lane < 2) cp_async_4(scales + 4 * (lane * kH + gi), scale + (off >> shift));
+  }
+  template <int NT>
+  __device__ __forceinline__ void scores(const uint8_t *stage, const uint8_t *scales, const uint32_t (&qf)[NT][8][2],
+                                         const uint4 *, float (&s)[NT][kH][4]) const {
+    const float *ks = reinterpret_cast<const float *>(scales);
+#pragma unroll
+    for (int gi = 0; gi < kH; ++gi) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][gi][0] = s[nt][gi][1] = s[nt][gi][2] = s[nt][gi][3] = 0.f;
+      const uint8_t *gk = stage + gi * kGranBytes;
+      uint4 a[2], b[2];  // rows r8 and r8 + 8
+      a[0] = *reinterpret_cast<const uint4 *>(gk + k0);
+      a[1] = *reinterpret_cast<const uint4 *>(gk + k1);
+      b[0] = *reinterpret_cast<const uint4 *>(gk + k0 + 1024);
+      b[1] = *reinterpret_cast<const uint4 *>(gk + k1 + 1024);
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t a0, a1, a2, a3;
+        codes_to_f16<INT>(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
+        codes_to_f16<INT>(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][gi], a0, a1, a2, a3, qf[nt][c][0], qf[nt][c][1]);
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[nt][gi][e] *= ks[gi];
+    }
+  }
+  // Masked tokens weigh 0: their rows must not hold NaN codes, nor a granule that was not copied
+  // any scale.
+  __device__ __forceinline__ void drop(uint8_t *stage, uint8_t *scales, uint32_t valid) const {
+    if (!INT && lane < kT && !((valid >> lane) & 1u)) {
+      uint4 *row = reinterpret_cast<uint4 *>(stage + kH * kGranBytes + lane * 128);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) row[j ^ (lane & 7)] = make_uint4(0u, 0u, 0u, 0u);
+    }
+    if (lane < kH && ((valid >> (16 * lane)) & 0xFFFFu) == 0) reinterpret_cast<float *>(scales)[kH + lane] = 0.f;
+  }
+  template <int NT>
+  __device__ __forceinline__ void values(const uint8_t *v, const uint8_t *scales, const uint32_t (&pb)[NT][kH][2],
+                                         float (&oacc)[NT][8][4]) const {
+#pragma unroll
+    for (int gi = 0; gi < kH; ++gi) {
+      const uint8_t *gv = v + gi * kGranBytes;
+      const float vs = reinterpret_cast<const float *>(scales)[kH + gi];
+      // tokens 2 q4, 2 q4 + 1 and the same + 8, dims 16 r8 .. 16 r8 + 15 of each
+      const uint4 w0 = *reinterpret_cast<const uint4 *>(gv + v0), w1 = *reinterpret_cast<const uint4 *>(gv + v1);
+      const uint4 w8 = *reinterpret_cast<const uint4 *>(gv + v0 + 1024);
+      const uint4 w9 = *reinterpret_cast<const uint4 *>(gv + v1 + 1024);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t x0 = biased<INT>(word(w0, c)), x1 = biased<INT>(word(w1, c));
+        const uint32_t x8 = biased<INT>(word(w8, c)), x9 = biased<INT>(word(w9, c));
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {  // dims 16 r8 + 4 c + 2 k and the next
+          uint32_t a0, a1, a2, a3;
+          codes_to_f16<INT>(prmt(x0, x1, k ? 0x7362 : 0x5140), a0, a1);
+          codes_to_f16<INT>(prmt(x8, x9, k ? 0x7362 : 0x5140), a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float o[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16_16816(o, a0, a1, a2, a3, pb[nt][gi][0], pb[nt][gi][1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) oacc[nt][2 * c + k][e] = fmaf(o[e], vs, oacc[nt][2 * c + k][e]);
+          }
+        }
+      }
+    }
+  }
+  // Whether a valid token of the stage has a NaN value code, or a V scale is not finite.
+  __device__ __forceinline__ bool not_finite(const uint8_t *v, const uint8_t *scales, uint32_t valid) const {
+    bool odd = false;
+    if (!INT && lane < kT && ((valid >> lane) & 1u)) {
+      const uint4 *row = reinterpret_cast<const uint4 *>(v + lane * 128);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint4 x = row[j ^ (lane & 7)];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) odd = odd || (((word(x, c) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
+      }
+    }
+    if (lane < kH) odd = odd || !(fabsf(reinterpret_cast<const float *>(scales)[kH + lane]) < __int_as_float(0x7f800000));
+    return __any_sync(0xffffffffu, odd);
+  }
+  // values() token by token, leaving out what a row's mask leaves out.
+  template <int NT>
+  __device__ __forceinline__ void values_kept(const uint8_t *v, const uint8_t *scales, uint32_t valid,
+                                              const float (&s)[NT][kH][4], const float (&y)[NT][2][2 * kH],
+                                              float (&oacc)[NT][8][4]) const {
+    const int q4 = lane & 3, r8 = lane >> 2;
+    const float ninf = -__int_as_float(0x7f800000);
+#pragma unroll
+    for (int k = 0; k < 2 * kH; ++k) {
+      const float vs = reinterpret_cast<const float *>(scales)[kH + (k >> 1)];
+      for (int r = 0; r < 8; ++r) {  // token 8 k + r, whose weights lane (r, q4) has
+        float w[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // (-1: not kept; a masked score is -inf)
+            const bool kept = ((valid >> (8 * k + r8)) & 1u) && s[nt][k >> 1][(k & 1) * 2 + e] != ninf;
+            w[nt][e] = __shfl_sync(0xffffffffu, kept ? y[nt][e][k] : -1.f, r * 4 + q4);
+          }
+        const uint4 x = *reinterpret_cast<const uint4 *>(v + (8 * k + r) * 128 + ((r8 ^ r) << 4));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t h[2];
+          codes_to_f16<INT>(biased<INT>(word(x, c)), h[0], h[1]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float2 d = __half22float2(*reinterpret_cast<const __half2 *>(&h[j]));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                if (w[nt][e] < 0.f) continue;  // (NaN weights go through)
+                oacc[nt][2 * c + j][e] = fmaf(w[nt][e], d.x * vs, oacc[nt][2 * c + j][e]);
+                oacc[nt][2 * c + j][2 + e] = fmaf(w[nt][e], d.y * vs, oacc[nt][2 * c + j][2 + e]);
+              }
+          }
+        }
+      }
+    }
+  }
+};
+
+template <bool INT, int NT, int MOD>
+__global__ void __launch_bounds__(StreamLayout<Block8Format<INT>, NT>::kThreads, 1)
+    block8_split_kernel(const StreamParams fp) {
+  begin_dependent();
+  stream_split<Block8Format<INT>, NT, MOD>(fp);
+}
+
+template <bool INT, int NT, int MOD>
+cudaError_t block8_attr() {
+  return cudaFuncSetAttribute(block8_split_kernel<INT, NT, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              StreamLayout<Block8Format<INT>, NT>::kTotal);
+}
+template <bool INT>
+cudaError_t block8_attrs() {
+  cudaError_t e;
+  if ((e = block8_attr<INT, 1, 0>()) != cudaSuccess) return e;
+  if ((e = block8_attr<INT, 1, 1>()) != cudaSuccess) return e;
+  if ((e = block8_attr<INT, 1, 2>()) != cudaSuccess) return e;
+  if ((e = block8_attr<INT, 2, 0>()) != cudaSuccess) return e;
+  if ((e = block8_attr<INT, 2, 1>()) != cudaSuccess) return e;
+  return block8_attr<INT, 2, 2>();
+}
+
+template <bool INT>
+cudaError_t launch(const StreamParams &p, int ctas, cudaStream_t stream) {
+  const int mod = gqa_mod(p.g);
+#define DA_B8(NT, M)                                                                                          \
+  return launch_dependent(block8_split_kernel<INT, NT, M>, (unsigned)ctas,                                     \
+                          StreamLayout<Block8Format<INT>, NT>::kThreads, StreamLayout<Block8Format<INT>, NT>::kTotal, \
+                          stream, p)
+  if (p.g.group <= 8) {
+    if (mod == 0) DA_B8(1, 0);
+    else if (mod == 1) DA_B8(1, 1);
+    else DA_B8(1, 2);
+  } else {
+    if (mod == 0) DA_B8(2, 0);
+    else if (mod == 1) DA_B8(2, 1);
+    else DA_B8(2, 2);
+  }
+#undef DA_B8
+}
+
+}  // namespace
+
+int block8_tile() { return Block8Format<false>::kT; }
+int block8_warps(int group) { return Block8Format<false>::kWarps(group <= 8 ? 1 : 2); }
+
+cudaError_t block8_prepare() {
+  const cudaError_t e = block8_attrs<false>();
+  return e != cudaSuccess ? e : block8_attrs<true>();
+}
+
+cudaError_t launch_block8(const StreamParams &p, bool integers, int ctas, cudaStream_t stream) {
+  return integers ? launch<true>(p, ctas, stream) : launch<false>(p, ctas, stream);
+}
+
+}  // namespace da

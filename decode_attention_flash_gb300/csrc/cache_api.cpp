@@ -45,6 +45,7 @@ da_status cache_params(const da_ctx *ctx, const void *k, const void *v, const fl
                        const int32_t *kss, const int32_t *vss, void *ws, da::CacheRowParams *c) {
   const da_problem &p = da::ctx_problem(ctx);
   const int kind = kind_of(p);
+  if (da::is_block8(p)) return DA_ERR_UNSUPPORTED;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return DA_ERR_INVALID_ARG;
   if ((kind == 1 || kind == 4) && (!k_scale || !v_scale)) return DA_ERR_INVALID_ARG;
   if (kind == 2 && (!kss || !vss)) return DA_ERR_INVALID_ARG;

@@ -1,5 +1,5 @@
 // cache_ops.h -- host/device structures of the cache calls (cache_api.cpp, cache_rows.cu,
-// tables.cu) and of the decode over the 4-bit float cache (fp4_split.cu).
+// tables.cu) and of the decode over caches in granules (stream_split.cuh).
 #pragma once
 
 #include "internal.h"
@@ -10,16 +10,17 @@ namespace da {
 // decode kernels know as its padding, build_tables' block counter here, zero between calls.
 constexpr int64_t kTicketOffset = 64;
 
-// Decode over the 4-bit float cache (fp4_split.cu): granules of 16 rows, 1152
-// bytes each, read through their addresses; o_head holds, per CTA and warp, the
-// piece of a unit that ended inside that warp's range.
-struct Fp4Params {
-  GqaParams g;
+// Decode over a cache in granules of 16 rows, read through their addresses (stream_split.cuh):
+// 4-bit floats (fp4_split.cu, 1152 bytes each) or 8-bit blocks (block8_split.cu, 2048 bytes);
+// o_head holds, per CTA and warp, the piece of a unit that ended inside that warp's range.
+struct StreamParams {
+  GqaParams g;                 // (8-bit blocks: k_scale, v_scale are the blocks' scales)
   const uint8_t *k, *v;
   float *o_head;               // [ctas][warps][G][128]
   int32_t whole;               // CTA c has unit c, whole (the grid is the units)
   int32_t kv_shift;            // a kv head's queries are 2^kv_shift units (g.num_kv_heads counts those)
   int32_t few_tiles, few_ctas; // a call of at most few_tiles tiles takes at most few_ctas CTAs
+  int32_t scale_shift;         // 8-bit blocks: a granule's byte offset to the index of its block's scale
 };
 
 // Which instantiation a call's score and mask modifications need: 0 none; 1
@@ -89,17 +90,28 @@ cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned 
   return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
 }
 
+// Kinds whose decode is stream_split.cuh.
+inline bool is_block8(const da_problem &p) {
+  return p.kv_dtype == DA_DTYPE_FP8_E4M3_BLOCKS || p.kv_dtype == DA_DTYPE_INT8_BLOCKS;
+}
+inline bool is_stream(const da_problem &p) { return p.kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS || is_block8(p); }
 cudaError_t fp4_prepare();
+cudaError_t block8_prepare();
 int fp4_tile();                // tokens per stage
+int block8_tile();
 int fp4_warps(int group);      // warps of a CTA for `group` rows per unit
+int block8_warps(int group);
+inline int stream_tile(const da_problem &p) { return is_block8(p) ? block8_tile() : fp4_tile(); }
+inline int stream_warps(const da_problem &p, int group) { return is_block8(p) ? block8_warps(group) : fp4_warps(group); }
 // log2 of the units that a kv head's queries are split into, so that each has at most 16 rows
 // (one query token, dense); -1: no such split.
-int fp4_kv_shift(const da_problem &p);
-cudaError_t launch_fp4(const Fp4Params &p, int ctas, cudaStream_t stream);
-// Byte offset of Fp4Params::o_head in the workspace (after the partial LSEs).
-int64_t fp4_head_offset(const da_plan_info &info);
-void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host, int32_t num_splits_override,
-             int32_t *few_tiles, int32_t *few_ctas);
+int stream_kv_shift(const da_problem &p);
+cudaError_t launch_fp4(const StreamParams &p, int ctas, cudaStream_t stream);
+cudaError_t launch_block8(const StreamParams &p, bool integers, int ctas, cudaStream_t stream);
+// Byte offset of StreamParams::o_head in the workspace (after the partial LSEs).
+int64_t stream_head_offset(const da_plan_info &info);
+void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host,
+                int32_t num_splits_override, int32_t *few_tiles, int32_t *few_ctas);
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);

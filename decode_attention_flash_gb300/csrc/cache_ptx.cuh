@@ -26,6 +26,12 @@ __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("gridd
 // Lets the next kernel of the stream start its blocks (they wait as above).
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Both: how a kernel that has nothing to do before the wait begins.
+__device__ __forceinline__ void begin_dependent() {
+  wait_for_previous_kernel();
+  let_next_kernel_start();
+}
+
 // ---------------------------------------------------------------- cp.async
 
 // 16 bytes to the shared address `smem_dst` (both sides 16-byte aligned), past L1.

@@ -36,8 +36,15 @@ da_status validate_problem(const da_problem *p) {
   if (p->kv_layout != DA_KV_CONTIGUOUS && p->kv_layout != DA_KV_PAGED) return DA_ERR_INVALID_ARG;
   if (p->kv_dtype != DA_DTYPE_BF16 && p->kv_dtype != DA_DTYPE_FP8_E4M3 &&
       p->kv_dtype != DA_DTYPE_FP8_E4M3_TOKEN_SCALE && p->kv_dtype != DA_DTYPE_INT4_GROUPS &&
-      p->kv_dtype != DA_DTYPE_FP4_E2M1_BLOCKS)
+      !is_stream(*p))
     return DA_ERR_INVALID_ARG;
+  if (is_block8(*p)) {
+    // positions of a scale: a power of two of granules that divides a page (or the cache's length)
+    const int n = p->kv_groups;
+    if (n < 16 || n > 256 || (n & (n - 1)) != 0) return DA_ERR_INVALID_ARG;
+    if (p->kv_layout == DA_KV_CONTIGUOUS && p->max_seq_len % n != 0) return DA_ERR_INVALID_ARG;
+    if (p->kv_layout == DA_KV_PAGED && p->page_size % n != 0) return DA_ERR_INVALID_ARG;
+  }
   if (p->kv_dtype == DA_DTYPE_INT4_GROUPS) {
     if (!(p->kv_groups == 1 || p->kv_groups == 2 || p->kv_groups == 4 || p->kv_groups == 8))
       return DA_ERR_INVALID_ARG;
@@ -68,8 +75,8 @@ da_status validate_problem(const da_problem *p) {
   }
   if (p->num_q_heads % p->num_kv_heads) return DA_ERR_INVALID_ARG;
   const int G = p->num_q_heads / p->num_kv_heads;
-  // the G x Q rows of a kv head: two n-tiles at most (the 4-bit float decode splits more)
-  if (G * Q > 16 && (p->kv_dtype != DA_DTYPE_FP4_E2M1_BLOCKS || fp4_kv_shift(*p) < 0)) return DA_ERR_UNSUPPORTED;
+  // the G x Q rows of a kv head: two n-tiles at most (the decodes of stream_split.cuh split more)
+  if (G * Q > 16 && (!is_stream(*p) || stream_kv_shift(*p) < 0)) return DA_ERR_UNSUPPORTED;
   if (p->head_dim_qk != 128 || p->head_dim_v != 128) return DA_ERR_UNSUPPORTED;
   if (p->kv_layout == DA_KV_PAGED) {
     const int P = p->page_size;
@@ -87,7 +94,7 @@ da_status validate_problem(const da_problem *p) {
     if (p->kv_layout != DA_KV_CONTIGUOUS) return DA_ERR_UNSUPPORTED;
     if (p->max_sparse_blocks <= 0) return DA_ERR_INVALID_ARG;
   }
-  if (p->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS) {
+  if (is_stream(*p)) {
     // granules of 16 rows, read through 64-bit addresses; positions and the
     // tiles of all units are counted in 32 bits
     if (p->kv_layout == DA_KV_CONTIGUOUS && p->max_seq_len % 16 != 0) return DA_ERR_UNSUPPORTED;
@@ -95,7 +102,7 @@ da_status validate_problem(const da_problem *p) {
                                                     : (int64_t)p->max_seq_len;
     const int64_t list = (int64_t)p->sparse_block_size * p->max_sparse_blocks * 2;
     if (cap >= (1ll << 31) || list >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
-    const int64_t units = ((int64_t)p->batch * p->num_kv_heads) << fp4_kv_shift(*p);
+    const int64_t units = ((int64_t)p->batch * p->num_kv_heads) << stream_kv_shift(*p);
     const int64_t tiles = units * ((std::max(cap, list) + 31) / 32);
     if (units >= (1ll << 31) || tiles >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
     return DA_OK;
@@ -108,7 +115,7 @@ da_status validate_problem(const da_problem *p) {
   return DA_OK;
 }
 
-int fp4_kv_shift(const da_problem &p) {
+int stream_kv_shift(const da_problem &p) {
   const int G = p.num_q_heads / p.num_kv_heads, Q = p.q_len > 1 ? p.q_len : 1;
   if ((int64_t)G * Q <= 16) return 0;
   if (Q > 1 || p.sparse_block_size > 0) return -1;
@@ -117,7 +124,7 @@ int fp4_kv_shift(const da_problem &p) {
   return -1;
 }
 
-int64_t fp4_head_offset(const da_plan_info &i) {
+int64_t stream_head_offset(const da_plan_info &i) {
   return align256(i.partial_lse_offset + ((int64_t)i.num_units + i.grid_x) * i.rows_per_unit * 4);
 }
 
@@ -127,7 +134,7 @@ int64_t fp4_head_offset(const da_plan_info &i) {
 // takes no more than leave its longest unit 28 pieces, or 16 of more than 8 rows: one row
 // of 16384 tokens, one head: 17.9 -> 16.3 us; two heads of 16 rows: 31.4 -> 22.7 (28
 // pieces: 28.1). The longest unit's share is that of the planned lengths, or the mean.
-void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host, int32_t num_splits_override,
+void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host, int32_t num_splits_override,
              int32_t *few_tiles, int32_t *few_ctas) {
   *few_tiles = *few_ctas = 0;
   if (num_splits_override > 0) return;
@@ -141,13 +148,13 @@ void fp4_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_l
   const int64_t pieces = info.rows_per_unit <= 8 ? 28 : 16;
   const int64_t most = longest > 0 ? std::max<int64_t>(pieces * sum / longest, 1) : pieces * info.num_units;
   *few_ctas = (int32_t)std::min<int64_t>(most, info.grid_x);
-  *few_tiles = (int32_t)std::min<int64_t>(most * 4 * fp4_warps(info.rows_per_unit), INT32_MAX);
+  *few_tiles = (int32_t)std::min<int64_t>(most * 4 * stream_warps(p, info.rows_per_unit), INT32_MAX);
 }
 
 // Resident CTAs of the split kernel per SM, from its shared-memory footprint.
 static int ctas_per_sm(const da_problem *p, int32_t smem_per_sm) {
   const bool mla = p->is_mla != 0;
-  if (p->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS) return 1;  // its rings fill an SM
+  if (is_stream(*p)) return 1;  // its rings fill an SM
   const int per_cta = (mla ? mla_smem_bytes()
                            : gqa_smem_bytes(p->kv_dtype != DA_DTYPE_BF16,
                                             p->num_q_heads / p->num_kv_heads *
@@ -170,12 +177,12 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
   const bool mla = p->is_mla != 0;
   const bool sparse = !mla && p->sparse_block_size > 0;
   const bool paged = p->kv_layout == DA_KV_PAGED;
-  const bool fp4 = p->kv_dtype == DA_DTYPE_FP4_E2M1_BLOCKS;
-  const int tile = mla ? kMlaTile : fp4 ? fp4_tile() : kGqaTile;
+  const bool stream = is_stream(*p);
+  const int tile = mla ? kMlaTile : stream ? stream_tile(*p) : kGqaTile;
   const int align = sparse ? p->sparse_block_size : tile;
   // units: GQA (row, kv head); MLA (row, query token), whose heads share the latent cache
   const int Q = p->q_len > 1 ? p->q_len : 1;
-  const int shift = fp4 ? fp4_kv_shift(*p) : 0;
+  const int shift = stream ? stream_kv_shift(*p) : 0;
   const int heads = mla ? Q : p->num_kv_heads << shift;
   const int64_t units = (int64_t)p->batch * heads;
   const int64_t capacity =
@@ -221,7 +228,7 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
     ctas = std::max<int64_t>(1, std::min<int64_t>(ctas, tiles));
     ctas = std::min<int64_t>(ctas, 65535);
     bool whole = false;
-    if (fp4) {
+    if (stream) {
       // A CTA for every unit saves the scan of the lengths and the merge between CTAs,
       // about 3 us (6 of 16 rows a unit), and costs the time by which the longest unit
       // passes an equal share: about 0.09 us a tile (8 heads of one 700-token row: 11.7
@@ -259,7 +266,7 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
     off = align256(off + (units + ctas) * rows * (int64_t)dv * 4);
     info->partial_lse_offset = off;
     off = align256(off + (units + ctas) * rows * 4);
-    if (fp4) off = fp4_head_offset(*info) + align256(ctas * fp4_warps(rows) * rows * (int64_t)dv * 4);
+    if (stream) off = stream_head_offset(*info) + align256(ctas * stream_warps(*p, rows) * rows * (int64_t)dv * 4);
     info->workspace_bytes = off;
     return DA_OK;
   }

@@ -82,13 +82,18 @@ typedef enum { DA_KV_CONTIGUOUS = 0, DA_KV_PAGED = 1 } da_kv_layout;
  * 2 j (low four bits) and 2 j + 1 of row r, byte 1024 + 8 r + i the e4m3 scale of
  * the row's elements 16 i .. 16 i + 15; with one fp32 scale per kv head (k_scale /
  * v_scale) an element is code * block scale * head scale. An e4m3 NaN scale makes
- * its block NaN. */
+ * its block NaN; or 8-bit codes, e4m3 or signed integers, of the caches' plain layout
+ * ([B][HKV][L][D] or [num_pages][HKV][page_size][D], a byte an element) with one fp32 scale for
+ * each block of kv_groups positions and kv head, in k_scale / v_scale ([B][HKV][L / kv_groups] or
+ * [num_pages][HKV][page_size / kv_groups]): an element is code * scale of its block. */
 typedef enum {
   DA_DTYPE_BF16 = 0,
   DA_DTYPE_FP8_E4M3 = 1,
   DA_DTYPE_FP8_E4M3_TOKEN_SCALE = 2,
   DA_DTYPE_INT4_GROUPS = 3,
-  DA_DTYPE_FP4_E2M1_BLOCKS = 4
+  DA_DTYPE_FP4_E2M1_BLOCKS = 4,
+  DA_DTYPE_FP8_E4M3_BLOCKS = 5,
+  DA_DTYPE_INT8_BLOCKS = 6
 } da_dtype;
 
 /* Bits of the device error word (sticky until decode_attn_get_error clears it). */
@@ -121,7 +126,7 @@ enum {
  *        extents: row b and kv head h read table row (b % SZ, h % SH), the
  *        broadcast of the flex decode template (SPARSE_Z, SPARSE_HQ).
  *   q_len: query tokens per row, 0 or 1 = one. GQA: G * Q <= 16 (the G*Q rows
- *        of a kv head share one pass; a dense 4-bit float cache with one query
+ *        of a kv head share one pass; a dense 4-bit float or 8-bit block cache with one query
  *        token also takes 2, 4 or 8 times a G <= 16, in that many passes); block-sparse tables apply to every query
  *        token, the causal or tree mask on top of them. MLA: Q <= 16, each query
  *        token a row of its own over the shared latent cache (its pages come
@@ -146,7 +151,9 @@ typedef struct {
   int32_t kv_groups;          /* DA_DTYPE_INT4_GROUPS: groups per row, 4 or 8 (rows of 1 or
                                  2 groups are not a multiple of 16 bytes: unsupported);
                                  contiguous caches need max_seq_len a multiple of 8 (4
-                                 groups) or 4 (8 groups) */
+                                 groups) or 4 (8 groups). DA_DTYPE_FP8_E4M3_BLOCKS and
+                                 DA_DTYPE_INT8_BLOCKS: positions of a scale's block, 16, 32, 64,
+                                 128 or 256, a divisor of page_size (contiguous: max_seq_len) */
   int32_t fp8_mma;            /* GQA with DA_DTYPE_FP8_E4M3 K/V only, optional: 1 runs QK and PV
                                  on e4m3 tensor cores. Each query row is quantised to e4m3
                                  in fp32 steps (amax = max |q|, code = e4m3(q * (448 / amax)),
@@ -170,8 +177,10 @@ typedef struct {
  *              DA_DTYPE_INT4_GROUPS: int32 rows of kv_groups + D / 8 words.
  *              DA_DTYPE_FP4_E2M1_BLOCKS: granules of 1152 bytes (see da_dtype).
  *              Base addresses of q, q_pe, k and v 128-byte aligned
- *   k_scale, v_scale  DA_DTYPE_FP8_E4M3 and DA_DTYPE_FP4_E2M1_BLOCKS only: fp32 [HKV];
- *              dequantised value = e4m3 * scale, or e2m1 * block scale * scale
+ *   k_scale, v_scale  DA_DTYPE_FP8_E4M3 and DA_DTYPE_FP4_E2M1_BLOCKS: fp32 [HKV];
+ *              dequantised value = e4m3 * scale, or e2m1 * block scale * scale.
+ *              DA_DTYPE_FP8_E4M3_BLOCKS and DA_DTYPE_INT8_BLOCKS: fp32, one a block of
+ *              positions and kv head (see da_dtype)
  *   k_scale_shift, v_scale_shift  DA_DTYPE_FP8_E4M3_TOKEN_SCALE only: int32, one word per
  *              cache row of k / v (contiguous [B][HKV][L], paged [num_pages][HKV][page_size]):
  *              fp16 scale in the low half, fp16 shift in the high half; dequantised
@@ -195,8 +204,8 @@ typedef struct {
  *              kernel, SPEC_DEC, for Q <= 32): every position before the row's Q new
  *              ones is attended, and new position N_b - Q + j by query token t when
  *              bit j of word [b][t] is set. NULL: causal (bits 0..t). Ignored for Q = 1
- *   out        bf16 [B][HQ][Dv]    (q_len Q > 1: [B][HQ][Q][Dv]); 8-byte aligned (MLA and
- *              the 4-bit float cache: 16-byte)
+ *   out        bf16 [B][HQ][Dv]    (q_len Q > 1: [B][HQ][Q][Dv]); 8-byte aligned (MLA,
+ *              the 4-bit float and the 8-bit block caches: 16-byte)
  *   lse        fp32 [B][HQ], natural log; may be NULL (q_len Q > 1: [B][HQ][Q])
  *   mask_window, mask_sink  GQA, optional: int32 [HQ] each (mask_sink may be NULL, meaning
  *              0): a mask_mod per query head in the sense of flex attention (which
@@ -270,7 +279,7 @@ da_status decode_attn_create(const da_problem *problem, int device, da_ctx **out
  * lets the planner size splits from the real lengths; without it the plan
  * assumes every row is max_seq_len long. num_splits_override > 0 forces that
  * many splits per unit (positions are cut into equal tile-aligned chunks; a
- * 4-bit float cache takes at most 1024 CTAs in all, or one split, whose workspace is
+ * 4-bit float or 8-bit block cache takes at most 1024 CTAs in all, or one split, whose workspace is
  * 256 bytes).
  * Host-only; no GPU work. Errors: INVALID_ARG.
  */
