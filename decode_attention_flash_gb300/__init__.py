@@ -26,7 +26,7 @@ __all__ = [
     "DA_DTYPE_BF16", "DA_DTYPE_FP8_E4M3", "DA_DTYPE_FP8_E4M3_TOKEN_SCALE", "DA_DTYPE_INT4_GROUPS",
     "DA_DTYPE_FP4_E2M1_BLOCKS", "DA_DTYPE_FP8_E4M3_BLOCKS", "DA_DTYPE_INT8_BLOCKS", "TableArgs", "AppendArgs", "GatherArgs", "make_args",
     "make_table_args", "make_append_args", "make_gather_args", "decode_attn_build_tables",
-    "decode_attn_append", "decode_attn_gather",
+    "decode_attn_append", "decode_attn_gather", "NormArgs", "make_norm_args", "decode_attn_append_normed",
 ]
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_CUDA = 0, 1, 2, 3
@@ -96,6 +96,10 @@ class AppendArgs(ctypes.Structure):
     ]
 
 
+class NormArgs(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
+
+
 class GatherArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "k", "v", "k_scale", "v_scale", "k_scale_shift", "v_scale_shift", "slot_map", "k_out",
@@ -143,6 +147,8 @@ def load(build_if_missing: bool = False):
         "decode_attn_get_error_noalloc": (st, [vp, vp, ctypes.POINTER(ctypes.c_uint32)]),
         "decode_attn_build_tables": (st, [vp, ctypes.POINTER(TableArgs), vp, ctypes.c_size_t, vp]),
         "decode_attn_append": (st, [vp, ctypes.POINTER(AppendArgs), vp, ctypes.c_size_t, vp]),
+        "decode_attn_append_normed": (st, [vp, ctypes.POINTER(AppendArgs), ctypes.POINTER(NormArgs), vp,
+                                           ctypes.c_size_t, vp]),
         "decode_attn_gather": (st, [vp, ctypes.POINTER(GatherArgs), vp, ctypes.c_size_t, vp]),
         "decode_attn_destroy": (None, [vp]),
         "decode_attn_status_string": (ctypes.c_char_p, [st]),
@@ -370,6 +376,19 @@ def make_append_args(tensors: dict, pair_axis=None, rope_adjacent: bool = False,
     return a
 
 
+def make_norm_args(tensors: dict, eps: float = 1e-6) -> NormArgs:
+    """The norm of ``decode_attn_append_normed``: ``q_weight`` and ``k_weight``, fp32, of a head's elements
+    (or none of one of them)."""
+    a = NormArgs()
+    for name in ("q_weight", "k_weight"):
+        t = tensors.get(name)
+        if t is not None and t.numel() not in (128, 512):
+            raise ValueError(f"{name} must have 128 elements (a latent row: 512), got {t.numel()}")
+        setattr(a, name, _typed_ptr(tensors, name, torch.float32))
+    a.eps = float(eps)
+    return a
+
+
 def make_gather_args(tensors: dict) -> GatherArgs:
     """Arguments of ``decode_attn_gather`` from a dict with the names of the C struct."""
     a = GatherArgs()
@@ -387,7 +406,7 @@ def make_gather_args(tensors: dict) -> GatherArgs:
     return a
 
 
-def _enqueue(fn, name: str, ctx, args, workspace, stream):
+def _enqueue(fn, name: str, ctx, args, workspace, stream, *more):
     """One call of an entry point that enqueues on a stream. Decode steps make a few of these a
     token, so the arguments go over as plain integers (no ctypes objects are made here)."""
     if not workspace.is_cuda or not workspace.is_contiguous():
@@ -396,7 +415,7 @@ def _enqueue(fn, name: str, ctx, args, workspace, stream):
         stream = torch._C._cuda_getCurrentRawStream(workspace.get_device())
     else:
         stream = _stream(stream)
-    status = fn(ctx, args, workspace.data_ptr(), workspace.nbytes, stream)
+    status = fn(ctx, args, *more, workspace.data_ptr(), workspace.nbytes, stream)
     if status != DA_OK:
         raise DecodeAttnError(status, name)
 
@@ -409,6 +428,11 @@ def decode_attn_build_tables(ctx, args: TableArgs, workspace: torch.Tensor, stre
 def decode_attn_append(ctx, args: AppendArgs, workspace: torch.Tensor, stream=None):
     """Rotates queries and new keys, and writes keys and values into the cache (one kernel)."""
     _enqueue(load().decode_attn_append, "decode_attn_append", ctx, args, workspace, stream)
+
+
+def decode_attn_append_normed(ctx, args: AppendArgs, norm: NormArgs, workspace: torch.Tensor, stream=None):
+    """``decode_attn_append`` with queries and keys normed head by head first (one kernel)."""
+    _enqueue(load().decode_attn_append_normed, "decode_attn_append_normed", ctx, args, workspace, stream, norm)
 
 
 def decode_attn_gather(ctx, args: GatherArgs, workspace: torch.Tensor, stream=None):
@@ -510,8 +534,9 @@ class DecodeAttention:
             raise ValueError(f"block_table must be [{p.batch}, {p.max_pages_per_seq}]")
         decode_attn_build_tables(self.ctx, make_table_args(tensors), self.workspace, stream)
 
-    def append(self, tensors: dict, pair_axis=None, rope_adjacent=False, q_len=1, stream=None):
-        """``decode_attn_append`` with the sizes checked against the problem."""
+    def append(self, tensors: dict, pair_axis=None, rope_adjacent=False, q_len=1, stream=None, norm_eps=1e-6):
+        """``decode_attn_append`` with the sizes checked against the problem; with ``q_weight`` or ``k_weight``
+        among the tensors, ``decode_attn_append_normed``."""
         p = self.problem
         d = 64 if p.is_mla else 128
         if tensors.get("k_new") is not None:
@@ -521,8 +546,14 @@ class DecodeAttention:
             t = tensors.get(name)
             if t is not None and math.prod(t.shape[1:]) != row:
                 raise ValueError(f"the rows of {name} must have {row} elements")
-        decode_attn_append(self.ctx, make_append_args(tensors, pair_axis, rope_adjacent, q_len),
-                           self.workspace, stream)
+        args = make_append_args(tensors, pair_axis, rope_adjacent, q_len)
+        if tensors.get("q_weight") is None and tensors.get("k_weight") is None:
+            decode_attn_append(self.ctx, args, self.workspace, stream)
+        else:
+            for name, n in (("q_weight", 128), ("k_weight", 512 if p.is_mla else 128)):
+                if tensors.get(name) is not None and tensors[name].numel() != n:
+                    raise ValueError(f"{name} must have {n} elements")
+            decode_attn_append_normed(self.ctx, args, make_norm_args(tensors, norm_eps), self.workspace, stream)
         return tensors.get("q_out")
 
     def gather(self, tensors: dict, stream=None):

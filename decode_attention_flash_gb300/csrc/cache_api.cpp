@@ -36,6 +36,8 @@ int kind_of(const da_problem &p) {
     case DA_DTYPE_FP8_E4M3_TOKEN_SCALE: return 2;
     case DA_DTYPE_INT4_GROUPS: return 3;
     case DA_DTYPE_FP4_E2M1_BLOCKS: return 4;
+    case DA_DTYPE_FP8_E4M3_BLOCKS: return 6;
+    case DA_DTYPE_INT8_BLOCKS: return 7;
     default: return 0;
   }
 }
@@ -45,14 +47,18 @@ da_status cache_params(const da_ctx *ctx, const void *k, const void *v, const fl
                        const int32_t *kss, const int32_t *vss, void *ws, da::CacheRowParams *c) {
   const da_problem &p = da::ctx_problem(ctx);
   const int kind = kind_of(p);
-  if (da::is_block8(p)) return DA_ERR_UNSUPPORTED;
   if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return DA_ERR_INVALID_ARG;
-  if ((kind == 1 || kind == 4) && (!k_scale || !v_scale)) return DA_ERR_INVALID_ARG;
+  if ((kind == 1 || kind == 4 || kind >= 6) && (!k_scale || !v_scale)) return DA_ERR_INVALID_ARG;
   if (kind == 2 && (!kss || !vss)) return DA_ERR_INVALID_ARG;
   c->k = const_cast<void *>(k);
   c->v = const_cast<void *>(v);
   c->k_scale = k_scale;
   c->v_scale = v_scale;
+  if (kind >= 6) {
+    if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return DA_ERR_INVALID_ARG;
+    c->k_block_scale = const_cast<float *>(k_scale);
+    c->v_block_scale = const_cast<float *>(v_scale);
+  }
   c->k_scale_shift = const_cast<int32_t *>(kss);
   c->v_scale_shift = const_cast<int32_t *>(vss);
   const bool paged = p.kv_layout == DA_KV_PAGED;
@@ -64,59 +70,18 @@ da_status cache_params(const da_ctx *ctx, const void *k, const void *v, const fl
   return DA_OK;
 }
 
-}  // namespace
-
-extern "C" {
-
-da_status decode_attn_build_tables(da_ctx *ctx, const da_table_args *a, void *workspace,
-                                   size_t workspace_bytes, da_stream_t stream) {
-  da_status st = check_call(ctx, a, workspace, workspace_bytes);
-  if (st != DA_OK) return st;
-  const da_problem &p = da::ctx_problem(ctx);
-  const bool paged = p.kv_layout == DA_KV_PAGED;
-  if (!a->seq_lens || !a->new_lens || !a->seq_lens_out || a->slot_capacity < 0) return DA_ERR_INVALID_ARG;
-  if (a->slot_capacity > 0 && !a->slot_map) return DA_ERR_INVALID_ARG;
-  if (paged != (a->block_table != nullptr)) return DA_ERR_INVALID_ARG;
-  const bool alloc = a->free_pages != nullptr;
-  if (alloc && (!paged || !a->num_free || !a->num_free_out || a->free_capacity < 0)) return DA_ERR_INVALID_ARG;
-  if (!alloc && (a->num_free || a->num_free_out)) return DA_ERR_INVALID_ARG;
-  const int64_t capacity = paged ? (int64_t)p.max_pages_per_seq * p.page_size : (int64_t)p.max_seq_len;
-  if (capacity >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
-  da::TableParams t;
-  std::memset(&t, 0, sizeof t);
-  t.seq_lens = a->seq_lens;
-  t.new_lens = a->new_lens;
-  t.free_pages = a->free_pages;
-  t.num_free = a->num_free;
-  t.block_table = a->block_table;
-  t.seq_lens_out = a->seq_lens_out;
-  t.num_free_out = a->num_free_out;
-  t.slot_map = a->slot_map;
-  t.positions = a->positions;
-  t.token_row = a->token_row;
-  t.cu_new = a->cu_new;
-  t.err = reinterpret_cast<uint32_t *>(workspace);
-  t.ticket = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(workspace) + da::kTicketOffset);
-  t.capacity = capacity;
-  t.batch = p.batch;
-  t.page_size = paged ? p.page_size : 1;
-  t.max_pages = p.max_pages_per_seq;
-  t.num_pages = p.num_pages;
-  t.free_capacity = a->free_capacity;
-  t.slot_capacity = a->slot_capacity;
-  t.paged = paged ? 1 : 0;
-  t.in_place = (a->seq_lens_out == a->seq_lens || (alloc && a->num_free_out == a->num_free)) ? 1 : 0;
-  return da::launch_tables(t, da::ctx_num_sms(ctx), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? DA_OK
-             : DA_ERR_CUDA;
-}
-
-da_status decode_attn_append(da_ctx *ctx, const da_append_args *a, void *workspace, size_t workspace_bytes,
-                             da_stream_t stream) {
+da_status append(da_ctx *ctx, const da_append_args *a, const da_norm_args *norm, void *workspace,
+                 size_t workspace_bytes, da_stream_t stream) {
   da_status st = check_call(ctx, a, workspace, workspace_bytes);
   if (st != DA_OK) return st;
   const da_problem &p = da::ctx_problem(ctx);
   const bool mla = p.is_mla != 0, has_kv = a->k_new != nullptr;
+  if (norm) {
+    if (!(norm->eps >= 0.f) || norm->eps > 3.4e38f) return DA_ERR_INVALID_ARG;  // negative, NaN, infinite
+    if (!aligned(norm->q_weight, 16) || !aligned(norm->k_weight, 16)) return DA_ERR_INVALID_ARG;
+    if ((norm->q_weight && !a->q) || (norm->k_weight && !has_kv)) return DA_ERR_INVALID_ARG;
+    if (norm->q_weight && mla) return DA_ERR_UNSUPPORTED;  // (q is the rope part of a query alone)
+  }
   if (a->num_tokens < 0 || a->q_len < 0) return DA_ERR_INVALID_ARG;
   if (a->num_tokens == 0) return DA_OK;  // (empty tensors may have no address)
   if ((a->q != nullptr) != (a->q_out != nullptr) || has_kv != (a->v_new != nullptr)) return DA_ERR_INVALID_ARG;
@@ -178,9 +143,74 @@ da_status decode_attn_append(da_ctx *ctx, const da_append_args *a, void *workspa
   c.num_tokens = a->num_tokens;
   c.num_q_heads = p.num_q_heads;
   c.q_len = a->q_len;
-  return da::launch_append(c, kind_of(p), da::ctx_num_sms(ctx), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+  if (norm) {
+    c.q_weight = norm->q_weight;
+    c.k_weight = norm->k_weight;
+    c.norm_eps = norm->eps;
+  }
+  const auto s = reinterpret_cast<cudaStream_t>(stream);
+  const int kind = kind_of(p), sms = da::ctx_num_sms(ctx);
+  const cudaError_t e = kind >= 6 && has_kv ? da::launch_append_blocks(c, kind == 7, sms, s)
+                                            : da::launch_append(c, kind >= 6 ? 0 : kind, sms, s);  // (queries alone)
+  return e == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+da_status decode_attn_build_tables(da_ctx *ctx, const da_table_args *a, void *workspace,
+                                   size_t workspace_bytes, da_stream_t stream) {
+  da_status st = check_call(ctx, a, workspace, workspace_bytes);
+  if (st != DA_OK) return st;
+  const da_problem &p = da::ctx_problem(ctx);
+  const bool paged = p.kv_layout == DA_KV_PAGED;
+  if (!a->seq_lens || !a->new_lens || !a->seq_lens_out || a->slot_capacity < 0) return DA_ERR_INVALID_ARG;
+  if (a->slot_capacity > 0 && !a->slot_map) return DA_ERR_INVALID_ARG;
+  if (paged != (a->block_table != nullptr)) return DA_ERR_INVALID_ARG;
+  const bool alloc = a->free_pages != nullptr;
+  if (alloc && (!paged || !a->num_free || !a->num_free_out || a->free_capacity < 0)) return DA_ERR_INVALID_ARG;
+  if (!alloc && (a->num_free || a->num_free_out)) return DA_ERR_INVALID_ARG;
+  const int64_t capacity = paged ? (int64_t)p.max_pages_per_seq * p.page_size : (int64_t)p.max_seq_len;
+  if (capacity >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+  da::TableParams t;
+  std::memset(&t, 0, sizeof t);
+  t.seq_lens = a->seq_lens;
+  t.new_lens = a->new_lens;
+  t.free_pages = a->free_pages;
+  t.num_free = a->num_free;
+  t.block_table = a->block_table;
+  t.seq_lens_out = a->seq_lens_out;
+  t.num_free_out = a->num_free_out;
+  t.slot_map = a->slot_map;
+  t.positions = a->positions;
+  t.token_row = a->token_row;
+  t.cu_new = a->cu_new;
+  t.err = reinterpret_cast<uint32_t *>(workspace);
+  t.ticket = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(workspace) + da::kTicketOffset);
+  t.capacity = capacity;
+  t.batch = p.batch;
+  t.page_size = paged ? p.page_size : 1;
+  t.max_pages = p.max_pages_per_seq;
+  t.num_pages = p.num_pages;
+  t.free_capacity = a->free_capacity;
+  t.slot_capacity = a->slot_capacity;
+  t.paged = paged ? 1 : 0;
+  t.in_place = (a->seq_lens_out == a->seq_lens || (alloc && a->num_free_out == a->num_free)) ? 1 : 0;
+  return da::launch_tables(t, da::ctx_num_sms(ctx), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DA_OK
              : DA_ERR_CUDA;
+}
+
+da_status decode_attn_append(da_ctx *ctx, const da_append_args *args, void *workspace, size_t workspace_bytes,
+                             da_stream_t stream) {
+  return append(ctx, args, nullptr, workspace, workspace_bytes, stream);
+}
+
+da_status decode_attn_append_normed(da_ctx *ctx, const da_append_args *args, const da_norm_args *norm,
+                                    void *workspace, size_t workspace_bytes, da_stream_t stream) {
+  if (!norm) return DA_ERR_INVALID_ARG;
+  return append(ctx, args, norm, workspace, workspace_bytes, stream);
 }
 
 da_status decode_attn_gather(da_ctx *ctx, const da_gather_args *a, void *workspace, size_t workspace_bytes,

@@ -1,5 +1,5 @@
 // cache_ops.h -- host/device structures of the cache calls (cache_api.cpp, cache_rows.cu,
-// tables.cu) and of the decode over caches in granules (stream_split.cuh).
+// cache_blocks.cu, tables.cu) and of the decode over caches in granules (stream_split.cuh).
 #pragma once
 
 #include "internal.h"
@@ -31,7 +31,7 @@ inline int gqa_mod(const GqaParams &p) {
              : (p.q_len > 1 || p.spec_mask != nullptr || p.softcap_l2 > 0.f) ? 1 : 0;
 }
 
-// Rows of the cache written (append) or read back (gather), cache_rows.cu. A
+// Rows of the cache written (append) or read back (gather), cache_rows.cu and cache_blocks.cu. A
 // slot is page * rows_per_page + offset (contiguous: batch row * cache length +
 // position, rows_per_page the cache length).
 struct CacheRowParams {
@@ -53,6 +53,10 @@ struct CacheRowParams {
   int32_t rope_adjacent;       // pairs are elements 2i, 2i + 1 (else i, i + n)
   int32_t rope_whole;          // a lane's pairs share an axis (vector loads of the table)
   int32_t parts;               // warps a token's heads are spread over (the launcher's)
+  const float *q_weight, *k_weight;  // the norm's weights of a head (latent: k_weight of 512); null: no norm
+  float norm_eps;
+  float *k_block_scale, *v_block_scale;  // 8-bit blocks: [pages][HKV][rows_per_page / kv_groups]
+  int32_t window;              // 8-bit blocks: tokens that one group of warps looks through (the launcher's)
   uint8_t pair_axis[64];
 };
 
@@ -114,6 +118,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
                 int32_t num_splits_override, int32_t *few_tiles, int32_t *few_ctas);
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
+cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream);
 

@@ -40,31 +40,17 @@
 
 #include <cuda_fp16.h>
 
-#include "cache_ops.h"
-#include "cache_ptx.cuh"
+#include "cache_rows.cuh"
 
 namespace da {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kAhead = 4;  // loads of queries in flight a lane
 constexpr int kSide = 2;   // rows of K, and as many of V, in flight
 
-enum Kind { kBf16 = 0, kE4m3 = 1, kE4m3Token = 2, kInt4 = 3, kFp4 = 4, kLatent = 5 };
+// (the append of 8-bit blocks is cache_blocks.cu)
+enum Kind { kBf16 = 0, kE4m3 = 1, kE4m3Token = 2, kInt4 = 3, kFp4 = 4, kLatent = 5, kE4m3Block = 6, kInt8Block = 7 };
 
-__device__ __forceinline__ float bf_lo(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float r;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 // e2m1 codes of (lo, hi), to nearest even, in the low and high nibble of a byte.
 __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
   uint32_t r;
@@ -113,6 +99,12 @@ __device__ __forceinline__ RowAt row_at(const CacheRowParams &p, int64_t slot, i
       a.ks = reinterpret_cast<uint8_t *>(p.k) + sc;
       a.vs = reinterpret_cast<uint8_t *>(p.v) + sc;
       a.shead = a.head;
+    }
+    if (KIND == kE4m3Block || KIND == kInt8Block) {
+      const int64_t per = P / p.kv_groups, sc = page * p.num_kv_heads * per + off / p.kv_groups;
+      a.ks = reinterpret_cast<uint8_t *>(p.k_block_scale + sc);
+      a.vs = reinterpret_cast<uint8_t *>(p.v_block_scale + sc);
+      a.shead = per * 4;
     }
     if (KIND == kE4m3Token) {
       a.ks = reinterpret_cast<uint8_t *>(p.k_scale_shift + row0);
@@ -214,85 +206,13 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_
   }
 }
 
-// Slot of token t, checked: -1 for padding (and, with the error bit, for a slot outside the cache).
-__device__ __forceinline__ int64_t load_slot(const CacheRowParams &p, int64_t t, uint32_t &err) {
-  if (!p.slot_map) return -1;
-  const int64_t s = p.slot_map[t];
-  if (s >= p.num_slots || s < -1) {
-    err |= DA_DEVERR_SLOT;
-    return -2;
-  }
-  return s;
-}
-
-// The cosines and sines of pairs pair0 .. pair0 + 7 (or + 3: kPairs) of token t;
-// false when a position is outside the table.
-template <int kPairs>
-__device__ __forceinline__ bool load_turn(const CacheRowParams &p, int64_t t, int pair0, float (&c)[8], float (&s)[8]) {
-  const int n = p.rope_pairs;
-  if (p.rope_whole) {  // they share an axis: vector loads
-    const int pos = p.positions[(int64_t)p.pair_axis[pair0] * p.position_stride + t];
-    if (pos < 0 || pos >= p.max_position) return false;
-    const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + pair0);
-    const float4 *row2 = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + n + pair0);
-#pragma unroll
-    for (int j = 0; j < kPairs / 4; ++j) {
-      const float4 a = __ldg(row + j), b = __ldg(row2 + j);
-      c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
-      s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
-    }
-    return true;
-  }
-  bool ok = true;
-#pragma unroll
-  for (int i = 0; i < kPairs; ++i) {
-    const int pos = p.positions[(int64_t)p.pair_axis[pair0 + i] * p.position_stride + t];
-    const bool in = pos >= 0 && pos < p.max_position;
-    ok = ok && in;
-    c[i] = in ? __ldg(p.cos_sin + (int64_t)pos * 2 * n + pair0 + i) : 1.f;
-    s[i] = in ? __ldg(p.cos_sin + (int64_t)pos * 2 * n + n + pair0 + i) : 0.f;
-  }
-  return ok;
-}
-
-// (a c - b s, b c + a s), every product and sum rounded to fp32
-__device__ __forceinline__ void turn(float a, float b, float c, float s, float &x, float &y) {
-  x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-  y = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-}
-// Pairs (element i of `lo`, element i of `hi`), i < 8.
-__device__ __forceinline__ void turn_halves(uint4 &lo, uint4 &hi, const float (&c)[8], const float (&s)[8]) {
-  uint32_t a[4] = {lo.x, lo.y, lo.z, lo.w}, b[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x0, y0, x1, y1;
-    turn(bf_lo(a[i]), bf_lo(b[i]), c[2 * i], s[2 * i], x0, y0);
-    turn(bf_hi(a[i]), bf_hi(b[i]), c[2 * i + 1], s[2 * i + 1], x1, y1);
-    a[i] = pack_bf16(x0, x1);
-    b[i] = pack_bf16(y0, y1);
-  }
-  lo = make_uint4(a[0], a[1], a[2], a[3]);
-  hi = make_uint4(b[0], b[1], b[2], b[3]);
-}
-// Pairs of neighbours: elements 2i, 2i + 1 of `v`, i < 4, with cosines c[at + i].
-__device__ __forceinline__ void turn_adjacent(uint4 &v, const float (&c)[8], const float (&s)[8], int at) {
-  uint32_t a[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float x, y;
-    turn(bf_lo(a[i]), bf_hi(a[i]), c[at + i], s[at + i], x, y);
-    a[i] = pack_bf16(x, y);
-  }
-  v = make_uint4(a[0], a[1], a[2], a[3]);
-}
-
 // HEAD: elements of a rotated head, 128 (the latent cache: 64).
-template <int KIND, int HEAD>
-__global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_constant__ CacheRowParams p) {
-  constexpr int kChunks = HEAD / 8;        // 16-byte chunks of a head
-  constexpr int kLanes = kChunks / 2;      // lanes of a head with both halves of its pairs
+// NORM: heads over their root mean square first (p.q_weight, p.k_weight); its weights take
+// registers, so fewer blocks an SM.
+template <int KIND, int HEAD, bool NORM>
+__global__ void __launch_bounds__(kWarps * 32, NORM ? 5 : 8) append_kernel(const __grid_constant__ CacheRowParams p) {
+  constexpr int kLanes = HEAD / 16;        // lanes of a query head
   constexpr int kHeads = 32 / kLanes;      // query heads a warp takes at once
-  constexpr int kDeep = kAhead / 2;        // groups of them in flight
   const int lane = threadIdx.x & 31;
   wait_for_previous_kernel();
   let_next_kernel_start();
@@ -306,70 +226,27 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
   const int groups = nq + nk;
   const int g0 = (int)((uint32_t)(part * groups) / (uint32_t)p.parts);
   const int g1 = (int)((uint32_t)((part + 1) * groups) / (uint32_t)p.parts);
-
-  // ---- queries: this lane's chunks of a head. Half-split pairs of r chunks: lane i < r
-  // has chunks i and i + r; neighbours as pairs: chunks 2i and 2i + 1; elements past
-  // the rotated ones stay, two chunks a lane.
-  const int l = lane % kLanes, sub = lane / kLanes, r = p.rope_pairs / 8;
-  const bool turned = l < r;
-  const bool split = turned && !p.rope_adjacent;
-  const int ca = split ? l : 2 * l, cb = split ? l + r : 2 * l + 1;
-  const int gq1 = min(g1, nq);
-  const uint4 *qsrc = reinterpret_cast<const uint4 *>(p.q + t * p.q_stride);
-  uint4 a[kDeep], b[kDeep];
-  auto load_q = [&](int g) {
-#pragma unroll
-    for (int k = 0; k < kDeep; ++k) {
-      const int hd = (g + k) * kHeads + sub;
-      if (g + k < gq1 && hd < HQ) {
-        a[k] = qsrc[hd * kChunks + ca];
-        b[k] = qsrc[hd * kChunks + cb];
-      }
-    }
-  };
-  load_q(g0);  // in flight while the slot and the positions are looked up
-  uint32_t err = 0;
-  const int64_t slot = load_slot(p, t, err);
-  const bool padding = p.slot_map != nullptr && slot < 0;
+  const QueryLane<HEAD> ql(p, lane);
+  const int r = p.rope_pairs / 8, ca = ql.ca, cb = ql.cb;
+  const bool turned = ql.turned, split = ql.split;
+  int64_t slot;
   float c[8], s[8];
-  bool bad = false;
-  if (turned) bad = !load_turn<8>(p, t, 8 * l, c, s);
-  bad = __any_sync(0xffffffffu, bad);
-  if (bad && !padding) err |= DA_DEVERR_POSITION;
-  if (err && lane == 0) atomicOr(p.err, err);
-  if (bad || padding) return;
-  {
-    const bool many = p.q_len > 1;
-    const int64_t row0 = many ? (t / p.q_len * p.num_q_heads) * p.q_len + t % p.q_len : t * p.num_q_heads;
-    const int step = (many ? p.q_len : 1) * kChunks;
-    uint4 *dst = reinterpret_cast<uint4 *>(p.q_out) + row0 * kChunks;
-    for (int g = g0; g < gq1; g += kDeep) {
-      if (g > g0) load_q(g);
-#pragma unroll
-      for (int k = 0; k < kDeep; ++k) {
-        const int hd = (g + k) * kHeads + sub;
-        if (g + k >= gq1 || hd >= HQ) continue;
-        if (split) {
-          turn_halves(a[k], b[k], c, s);
-        } else if (turned) {
-          turn_adjacent(a[k], c, s, 0);
-          turn_adjacent(b[k], c, s, 4);
-        }
-        dst[(int64_t)hd * step + ca] = a[k];
-        dst[(int64_t)hd * step + cb] = b[k];
-      }
-    }
-  }
+  if (!append_queries<HEAD, NORM>(p, t, lane, ql, g0, min(g1, nq), HQ, slot, c, s)) return;
   if (HK == 0) return;
   if constexpr (KIND == kLatent) {
     // the row of the latent cache: 512 elements as they are, 64 turned, by the last part
     if (part != p.parts - 1) return;
     const uint4 *src = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + lane;
     uint4 *dst = reinterpret_cast<uint4 *>(p.k) + slot * 64 + lane;
-    const uint4 x = src[0], y = src[32];
+    uint4 x = src[0], y = src[32];
     const uint4 *rope = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride);
     uint4 u, v;
     if (lane < kLanes) u = rope[ca], v = rope[cb];
+    if (NORM && p.k_weight) {
+      const float n = head_rsqrt<32>(x, y, p.norm_eps);
+      x = normed(x, n, p.k_weight + 8 * lane);
+      y = normed(y, n, p.k_weight + 256 + 8 * lane);
+    }
     dst[0] = x;
     dst[32] = y;
     if (lane < kLanes) {
@@ -401,6 +278,11 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = -s[i];
     }
+    float wo[8], wp[8];  // the norm's weights of the lane's elements and of its partner's
+    if (NORM && p.k_weight) {
+      load8(p.k_weight + 8 * kl, wo);
+      load8(p.k_weight + 8 * (partner & 15), wp);
+    }
     int h = 2 * (first - nq) + ksub;
     const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + h * 16 + kl;
     const uint4 *vsrc = reinterpret_cast<const uint4 *>(p.v_new + t * p.v_stride) + h * 16 + kl;
@@ -425,22 +307,10 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
 #pragma unroll
       for (int i = 0; i < kSide; ++i) {
         if (g + i >= g1) break;
-        if (r > 0) {
-          if (p.rope_adjacent) {
-            if (kturned) turn_adjacent(w[i], c, s, 0);
-          } else {
-            const uint4 z = make_uint4(__shfl_sync(0xffffffffu, w[i].x, partner), __shfl_sync(0xffffffffu, w[i].y, partner),
-                                       __shfl_sync(0xffffffffu, w[i].z, partner), __shfl_sync(0xffffffffu, w[i].w, partner));
-            if (kturned) {
-              uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-              const uint32_t y[4] = {z.x, z.y, z.z, z.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                x[j] = pack_bf16(__fsub_rn(__fmul_rn(bf_lo(x[j]), c[2 * j]), __fmul_rn(bf_lo(y[j]), s[2 * j])),
-                                 __fsub_rn(__fmul_rn(bf_hi(x[j]), c[2 * j + 1]), __fmul_rn(bf_hi(y[j]), s[2 * j + 1])));
-              w[i] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          }
+        if (NORM && p.k_weight) {
+          norm_key(p, w[i], kl, partner, kturned, c, s, wo, wp);
+        } else if (r > 0) {
+          turn_key(p, w[i], partner, kturned, c, s);
         }
         const bool mine = h + 2 * i < HK;
         put_row<KIND>(p, mine, kd, ks, sk[i], kl, w[i]);
@@ -461,7 +331,7 @@ __global__ void __launch_bounds__(kWarps * 32, 8) append_kernel(const __grid_con
 // product (and sum) of its parts, rounded once more to bf16.
 struct RowBits {
   uint4 a;      // the lane's codes (bf16: its values)
-  uint32_t s;   // block scale byte, or scale and shift halves
+  uint32_t s;   // block scale byte, scale and shift halves, or an fp32 scale
 };
 template <int KIND>
 __device__ __forceinline__ RowBits get_row(const uint8_t *src, const uint8_t *ssrc) {
@@ -469,13 +339,14 @@ __device__ __forceinline__ RowBits get_row(const uint8_t *src, const uint8_t *ss
   r.a = make_uint4(0u, 0u, 0u, 0u);
   r.s = 0;
   if (KIND == kBf16) r.a = *reinterpret_cast<const uint4 *>(src);
-  if (KIND == kE4m3 || KIND == kE4m3Token) {
+  if (KIND == kE4m3 || KIND == kE4m3Token || KIND == kE4m3Block || KIND == kInt8Block) {
     const uint2 v = *reinterpret_cast<const uint2 *>(src);
     r.a.x = v.x;
     r.a.y = v.y;
   }
   if (KIND == kInt4 || KIND == kFp4) r.a.x = *reinterpret_cast<const uint32_t *>(src);
-  if (KIND == kInt4 || KIND == kE4m3Token) r.s = *reinterpret_cast<const uint32_t *>(ssrc);
+  if (KIND == kInt4 || KIND == kE4m3Token || KIND == kE4m3Block || KIND == kInt8Block)
+    r.s = *reinterpret_cast<const uint32_t *>(ssrc);
   if (KIND == kFp4) r.s = *ssrc;
   return r;
 }
@@ -483,15 +354,20 @@ template <int KIND>
 __device__ __forceinline__ uint4 row_values(const RowBits &r, float head_scale) {
   if (KIND == kBf16) return r.a;
   float x[8];
-  if (KIND == kE4m3 || KIND == kE4m3Token) {
+  if (KIND == kInt8Block) {
+    const float sc = __uint_as_float(r.s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[i] = __fmul_rn((float)(int8_t)((i < 4 ? r.a.x : r.a.y) >> (8 * (i & 3))), sc);
+  } else if (KIND == kE4m3 || KIND == kE4m3Token || KIND == kE4m3Block) {
     const uint32_t h[4] = {e4m3x2_to_f16x2((uint16_t)r.a.x), e4m3x2_to_f16x2((uint16_t)(r.a.x >> 16)),
                            e4m3x2_to_f16x2((uint16_t)r.a.y), e4m3x2_to_f16x2((uint16_t)(r.a.y >> 16))};
-    const float sc = KIND == kE4m3 ? head_scale : f16_value(r.s & 0xFFFFu);
-    const float sh = KIND == kE4m3 ? 0.f : f16_value(r.s >> 16);
+    const float sc = KIND == kE4m3 ? head_scale : KIND == kE4m3Block ? __uint_as_float(r.s) : f16_value(r.s & 0xFFFFu);
+    const float sh = KIND == kE4m3Token ? f16_value(r.s >> 16) : 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float c = f16_value((h[i >> 1] >> (16 * (i & 1))) & 0xFFFFu);
-      x[i] = KIND == kE4m3 ? __fmul_rn(c, sc) : fmaf(c, sc, sh);
+      x[i] = KIND != kE4m3Token ? __fmul_rn(c, sc) : fmaf(c, sc, sh);
     }
   } else if (KIND == kInt4) {
     const float sc = f16_value(r.s & 0xFFFFu), sh = f16_value(r.s >> 16);
@@ -604,6 +480,18 @@ int append_parts(int64_t tokens, int groups, int num_sms) {
   return (int)std::min<int64_t>({parts, groups, INT32_MAX / groups});
 }
 
+template <bool NORM>
+cudaError_t append_of(const CacheRowParams &p, int kind, unsigned grid, cudaStream_t stream) {
+  switch (kind) {
+    case kBf16: return launch_dependent(append_kernel<kBf16, 128, NORM>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3: return launch_dependent(append_kernel<kE4m3, 128, NORM>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3Token: return launch_dependent(append_kernel<kE4m3Token, 128, NORM>, grid, kWarps * 32, 0, stream, p);
+    case kInt4: return launch_dependent(append_kernel<kInt4, 128, NORM>, grid, kWarps * 32, 0, stream, p);
+    case kFp4: return launch_dependent(append_kernel<kFp4, 128, NORM>, grid, kWarps * 32, 0, stream, p);
+    default: return launch_dependent(append_kernel<kLatent, 64, NORM>, grid, kWarps * 32, 0, stream, p);
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
@@ -615,14 +503,7 @@ cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t 
   p.parts = append_parts(p.num_tokens, groups < 1 ? 1 : groups, num_sms);
   const int64_t blocks = blocks_for((int64_t)p.num_tokens * p.parts);
   const unsigned grid = (unsigned)blocks;
-  switch (kind) {
-    case kBf16: return launch_dependent(append_kernel<kBf16, 128>, grid, kWarps * 32, 0, stream, p);
-    case kE4m3: return launch_dependent(append_kernel<kE4m3, 128>, grid, kWarps * 32, 0, stream, p);
-    case kE4m3Token: return launch_dependent(append_kernel<kE4m3Token, 128>, grid, kWarps * 32, 0, stream, p);
-    case kInt4: return launch_dependent(append_kernel<kInt4, 128>, grid, kWarps * 32, 0, stream, p);
-    case kFp4: return launch_dependent(append_kernel<kFp4, 128>, grid, kWarps * 32, 0, stream, p);
-    default: return launch_dependent(append_kernel<kLatent, 64>, grid, kWarps * 32, 0, stream, p);
-  }
+  return p.q_weight || p.k_weight ? append_of<true>(p, kind, grid, stream) : append_of<false>(p, kind, grid, stream);
 }
 
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream) {
@@ -636,6 +517,8 @@ cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t 
     case kE4m3Token: return launch_dependent(gather_kernel<kE4m3Token>, grid, kWarps * 32, 0, stream, p);
     case kInt4: return launch_dependent(gather_kernel<kInt4>, grid, kWarps * 32, 0, stream, p);
     case kFp4: return launch_dependent(gather_kernel<kFp4>, grid, kWarps * 32, 0, stream, p);
+    case kE4m3Block: return launch_dependent(gather_kernel<kE4m3Block>, grid, kWarps * 32, 0, stream, p);
+    case kInt8Block: return launch_dependent(gather_kernel<kInt8Block>, grid, kWarps * 32, 0, stream, p);
     default: return launch_dependent(gather_kernel<kLatent>, grid, kWarps * 32, 0, stream, p);
   }
 }

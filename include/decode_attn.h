@@ -475,7 +475,7 @@ da_status decode_attn_build_tables(da_ctx *ctx, const da_table_args *args, void 
  *                D (MLA 64). Pair i is (i, i + rope_dim / 2), or (2 i, 2 i + 1) with
  *                rope_adjacent
  *   k, v, k_scale, v_scale, k_scale_shift, v_scale_shift  the cache, as in da_args (the
- *                scale words are written; the per-head scales are read)
+ *                scale words and the blocks' scales are written; the per-head scales are read)
  */
 typedef struct {
   const void *q;
@@ -516,12 +516,46 @@ typedef struct {
  *   4-bit float  block scale = e4m3(max |x| / (6 scale[h])) of 16 elements; the e2m1 nearest
  *                to x / (block scale * scale[h]), ties to even; zeros when that product is
  *                below 2^-126. A NaN makes its block NaN, an infinity saturates
+ *   8-bit blocks the block's scale is the least power of two that brings every |x| written to it
+ *                into the codes' range (448, or 127), or the scale that it has where that is
+ *                greater; a call that writes a block's first row starts it anew, without its old
+ *                scale. Codes are x / scale to nearest even. Where the scale grows, the block's
+ *                rows that the call does not write are rounded again to its codes (by powers of two:
+ *                e4m3 codes above the subnormal ones stay exact, integers end within one step).
+ *                Infinities saturate; e4m3 keeps a NaN as a NaN code, and integers make the scale,
+ *                so the block, NaN until it is started anew. Tokens of a call that belong to one
+ *                block of the cache stand next to each other in slot_map, nothing between them (as
+ *                decode_attn_build_tables lists them); k_scale and v_scale are written
  * (rows outside f16's range make an infinite scale or shift). A slot outside the
  * cache (DA_DEVERR_SLOT) or a position outside the table (DA_DEVERR_POSITION) skips
  * its token whole. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, NOT_PLANNED, CUDA.
  */
 da_status decode_attn_append(da_ctx *ctx, const da_append_args *args, void *workspace,
                              size_t workspace_bytes, da_stream_t stream);
+
+/*
+ * The norm of decode_attn_append_normed: a query or key head of 128 elements (MLA: the latent row of
+ * 512) divided by its root mean square, times a weight, before it is turned:
+ *   y = x / sqrt(mean x^2 + eps) * weight
+ * in fp32, the turned result rounded once to bf16. Values, and MLA's rope parts, are not normed.
+ *
+ *   q_weight     fp32 [D], for every query head; NULL: queries are not normed (MLA: NULL)
+ *   k_weight     fp32 [D] (MLA [512]), for every key head; NULL: keys are not normed
+ *   eps          not negative, finite
+ * Weights are 16-byte aligned and kept as cos_sin is.
+ */
+typedef struct {
+  const float *q_weight;
+  const float *k_weight;
+  float eps;
+} da_norm_args;
+
+/*
+ * decode_attn_append with queries and keys normed head by head first (for models that norm them,
+ * and for the latent row of MLA). Errors: as decode_attn_append.
+ */
+da_status decode_attn_append_normed(da_ctx *ctx, const da_append_args *args, const da_norm_args *norm,
+                                    void *workspace, size_t workspace_bytes, da_stream_t stream);
 
 /*
  * Arguments of decode_attn_gather: the cache (as in da_args), slot_map int64 [T],

@@ -19,8 +19,9 @@ def codes_of(y, kind):
     """float64 quotients -> codes, to nearest even, saturating."""
     if kind == "int8":
         return y.round().clamp(-127, 127).to(torch.int8)
+    y = y.clamp(-448, 448)  # (infinities too; NaN stays)
     unit = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)
-    z = torch.where(torch.isnan(y), y, ((y / unit).round() * unit).clamp(-448, 448))
+    z = torch.where(torch.isnan(y), y, (y / unit).round() * unit)
     return z.float().to(torch.float8_e4m3fn)  # exact
 
 
