@@ -27,6 +27,7 @@ __all__ = [
     "DA_DTYPE_FP4_E2M1_BLOCKS", "DA_DTYPE_FP8_E4M3_BLOCKS", "DA_DTYPE_INT8_BLOCKS", "TableArgs", "AppendArgs", "GatherArgs", "make_args",
     "make_table_args", "make_append_args", "make_gather_args", "decode_attn_build_tables",
     "decode_attn_append", "decode_attn_gather", "NormArgs", "make_norm_args", "decode_attn_append_normed",
+    "VerifyArgs", "make_verify_args", "decode_attn_verify",
 ]
 
 DA_OK, DA_ERR_INVALID_ARG, DA_ERR_UNSUPPORTED, DA_ERR_CUDA = 0, 1, 2, 3
@@ -36,6 +37,7 @@ DA_DTYPE_BF16, DA_DTYPE_FP8_E4M3, DA_DTYPE_FP8_E4M3_TOKEN_SCALE, DA_DTYPE_INT4_G
 DA_DTYPE_FP4_E2M1_BLOCKS, DA_DTYPE_FP8_E4M3_BLOCKS, DA_DTYPE_INT8_BLOCKS = 4, 5, 6
 DA_DEVERR_PAGE_INDEX, DA_DEVERR_SPARSE_INDEX, DA_DEVERR_SEQ_LEN, DA_DEVERR_TIMEOUT = 1, 2, 4, 8
 DA_DEVERR_NO_PAGES, DA_DEVERR_SLOT, DA_DEVERR_POSITION = 16, 32, 64
+DA_DEVERR_TOKEN, DA_DEVERR_PROBS = 128, 256
 
 
 class DecodeAttnError(RuntimeError):
@@ -106,6 +108,14 @@ class GatherArgs(ctypes.Structure):
         "v_out")] + [("num_tokens", ctypes.c_int32)]
 
 
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "target_probs", "draft_probs", "target_tokens", "draft_tokens", "num_draft", "uniforms", "tokens_out",
+        "num_accepted", "seq_lens", "seq_lens_out", "block_table", "free_pages", "num_free", "num_free_out")] + [
+        ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)] + [
+        (n, ctypes.c_int32) for n in ("q_len", "vocab", "free_capacity")]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "kv_tile", "chunk_tokens", "num_splits", "num_units", "rows_per_unit", "grid_x", "grid_y",
@@ -150,6 +160,7 @@ def load(build_if_missing: bool = False):
         "decode_attn_append_normed": (st, [vp, ctypes.POINTER(AppendArgs), ctypes.POINTER(NormArgs), vp,
                                            ctypes.c_size_t, vp]),
         "decode_attn_gather": (st, [vp, ctypes.POINTER(GatherArgs), vp, ctypes.c_size_t, vp]),
+        "decode_attn_verify": (st, [vp, ctypes.POINTER(VerifyArgs), vp, ctypes.c_size_t, vp]),
         "decode_attn_destroy": (None, [vp]),
         "decode_attn_status_string": (ctypes.c_char_p, [st]),
         # test hooks (include/decode_attn_testing.h)
@@ -406,6 +417,47 @@ def make_gather_args(tensors: dict) -> GatherArgs:
     return a
 
 
+def _prob_rows(t, name: str, rows: int, vocab: int):
+    """Pointer and row stride of [batch, tokens, vocab] probabilities: a vocabulary's are contiguous, the
+    rows evenly apart (a column range of wider rows is fine)."""
+    if not t.is_cuda:
+        raise ValueError("tensor arguments must be in device memory (got a host tensor)")
+    if t.dtype != torch.float32 or t.dim() != 3 or t.shape[0] * t.shape[1] != rows or t.shape[2] != vocab:
+        raise ValueError(f"{name} must be float32 [batch, tokens, {vocab}], {rows} rows in all")
+    if rows == 0:
+        return None, vocab
+    if (vocab > 1 and t.stride(2) != 1) or (t.shape[0] > 1 and t.shape[1] > 1 and t.stride(0) != t.shape[1] * t.stride(1)):
+        raise ValueError(f"the rows of {name} must be contiguous and evenly apart")
+    stride = t.stride(1) if t.shape[1] > 1 else t.stride(0) if t.shape[0] > 1 else vocab
+    return ctypes.c_void_p(t.data_ptr()), stride
+
+
+def make_verify_args(tensors: dict, vocab: int = 0) -> VerifyArgs:
+    """Arguments of ``decode_attn_verify`` from a dict with the names of the C struct. ``target_probs`` is
+    [batch, Q, vocab], ``draft_probs`` [batch, Q - 1, vocab]; with ``target_tokens`` [batch, Q] instead, ``vocab``
+    is given here (0: any token)."""
+    a = VerifyArgs()
+    target, greedy = tensors.get("target_probs"), tensors.get("target_tokens")
+    if (target is None) == (greedy is None):
+        raise ValueError("either target_probs or target_tokens must be given")
+    b, q = (target if target is not None else greedy).shape[:2]
+    a.q_len = q
+    if target is not None:
+        a.vocab = target.shape[2]
+        a.target_probs, a.target_stride = _prob_rows(target, "target_probs", b * q, a.vocab)
+        if tensors.get("draft_probs") is not None:
+            a.draft_probs, a.draft_stride = _prob_rows(tensors["draft_probs"], "draft_probs", b * (q - 1), a.vocab)
+    else:
+        a.vocab = int(vocab) or 1 << 21
+    for name, n in (("target_tokens", b * q), ("draft_tokens", b * (q - 1)), ("num_draft", b), ("tokens_out", b * q),
+                    ("num_accepted", b), ("seq_lens", b), ("seq_lens_out", b), ("block_table", None),
+                    ("free_pages", None), ("num_free", 1), ("num_free_out", 1)):
+        setattr(a, name, _typed_ptr(tensors, name, torch.int32, n))
+    a.uniforms = _typed_ptr(tensors, "uniforms", torch.float32, b * q)
+    a.free_capacity = tensors["free_pages"].numel() if tensors.get("free_pages") is not None else 0
+    return a
+
+
 def _enqueue(fn, name: str, ctx, args, workspace, stream, *more):
     """One call of an entry point that enqueues on a stream. Decode steps make a few of these a
     token, so the arguments go over as plain integers (no ctypes objects are made here)."""
@@ -438,6 +490,11 @@ def decode_attn_append_normed(ctx, args: AppendArgs, norm: NormArgs, workspace: 
 def decode_attn_gather(ctx, args: GatherArgs, workspace: torch.Tensor, stream=None):
     """Reads cache rows back as bf16 (one kernel)."""
     _enqueue(load().decode_attn_gather, "decode_attn_gather", ctx, args, workspace, stream)
+
+
+def decode_attn_verify(ctx, args: VerifyArgs, workspace: torch.Tensor, stream=None):
+    """Drafted tokens verified, the token after them drawn, lengths and pages taken back (one kernel)."""
+    _enqueue(load().decode_attn_verify, "decode_attn_verify", ctx, args, workspace, stream)
 
 
 def decode_attn_get_error(ctx, workspace: torch.Tensor, stream=None) -> int:
@@ -567,6 +624,21 @@ class DecodeAttention:
                 raise ValueError(f"{name} must have {n * row} elements")
         decode_attn_gather(self.ctx, make_gather_args(tensors), self.workspace, stream)
         return tensors["k_out"], tensors["v_out"]
+
+    def verify(self, tensors: dict, vocab=0, stream=None):
+        """``decode_attn_verify`` with the sizes checked against the problem."""
+        p = self.problem
+        first = tensors["target_probs"] if tensors.get("target_probs") is not None else tensors["target_tokens"]
+        if first.shape[0] != p.batch:
+            raise ValueError(f"the problem has {p.batch} rows, got {first.shape[0]}")
+        for name in ("tokens_out", "num_accepted"):
+            if tensors.get(name) is None:
+                raise ValueError(f"{name} must be given")
+        table = tensors.get("block_table")
+        if table is not None and table.numel() != p.batch * p.max_pages_per_seq:
+            raise ValueError(f"block_table must be [{p.batch}, {p.max_pages_per_seq}]")
+        decode_attn_verify(self.ctx, make_verify_args(tensors, vocab), self.workspace, stream)
+        return tensors["tokens_out"], tensors["num_accepted"]
 
     def errors(self, stream=None) -> int:
         return decode_attn_get_error(self.ctx, self.workspace, stream)

@@ -1,5 +1,5 @@
 // cache_api.cpp -- the C entry points around the decode: block tables and slots from
-// lengths, rows appended to the cache, rows read back. Argument checks and launches
+// lengths, rows appended to the cache, rows read back, drafts verified. Argument checks and launches
 // only; nothing here allocates or synchronises.
 #include <algorithm>
 #include <cstring>
@@ -18,7 +18,7 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-// Checks that the three calls share.
+// Checks that the calls share.
 da_status check_call(const da_ctx *ctx, const void *args, const void *ws, size_t bytes) {
   if (!ctx || !args) return DA_ERR_INVALID_ARG;
   if (!da::ctx_planned(ctx)) return DA_ERR_NOT_PLANNED;
@@ -233,6 +233,57 @@ da_status decode_attn_gather(da_ctx *ctx, const da_gather_args *a, void *workspa
   return da::launch_gather(c, kind_of(p), da::ctx_num_sms(ctx), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
              ? DA_OK
              : DA_ERR_CUDA;
+}
+
+da_status decode_attn_verify(da_ctx *ctx, const da_verify_args *a, void *workspace, size_t workspace_bytes,
+                             da_stream_t stream) {
+  da_status st = check_call(ctx, a, workspace, workspace_bytes);
+  if (st != DA_OK) return st;
+  const da_problem &p = da::ctx_problem(ctx);
+  const bool paged = p.kv_layout == DA_KV_PAGED, greedy = a->target_tokens != nullptr;
+  if (a->q_len < 1 || a->vocab < 1 || !a->tokens_out || !a->num_accepted) return DA_ERR_INVALID_ARG;
+  if (greedy == (a->target_probs != nullptr) || (greedy && (a->draft_probs || a->uniforms))) return DA_ERR_INVALID_ARG;
+  if (a->q_len > 1 && !a->draft_tokens) return DA_ERR_INVALID_ARG;
+  if (!greedy && (!a->uniforms || a->target_stride < a->vocab)) return DA_ERR_INVALID_ARG;
+  if (a->draft_probs && a->q_len > 1 && a->draft_stride < a->vocab) return DA_ERR_INVALID_ARG;
+  if ((a->seq_lens != nullptr) != (a->seq_lens_out != nullptr)) return DA_ERR_INVALID_ARG;
+  const bool gives = a->free_pages != nullptr;
+  if (gives && (!paged || !a->seq_lens || !a->block_table || !a->num_free || !a->num_free_out || a->free_capacity < 0))
+    return DA_ERR_INVALID_ARG;
+  if (!gives && (a->block_table || a->num_free || a->num_free_out)) return DA_ERR_INVALID_ARG;
+  // (the segments' sums of a row are in shared memory; CTAs are counted in 31 bits)
+  if (a->vocab > (1 << 21) || a->q_len > (1 << 20) || p.batch > (1 << 27)) return DA_ERR_UNSUPPORTED;
+  const int64_t capacity = paged ? (int64_t)p.max_pages_per_seq * p.page_size : (int64_t)p.max_seq_len;
+  if (capacity >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
+  da::VerifyParams v;
+  std::memset(&v, 0, sizeof v);
+  v.target = a->target_probs;
+  v.draft = a->draft_probs;
+  v.target_stride = a->target_stride;
+  v.draft_stride = a->draft_stride;
+  v.target_tokens = a->target_tokens;
+  v.draft_tokens = a->draft_tokens;
+  v.num_draft = a->num_draft;
+  v.uniforms = a->uniforms;
+  v.tokens_out = a->tokens_out;
+  v.num_accepted = a->num_accepted;
+  v.seq_lens = a->seq_lens;
+  v.seq_lens_out = a->seq_lens_out;
+  v.block_table = a->block_table;
+  v.free_pages = a->free_pages;
+  v.num_free = a->num_free;
+  v.num_free_out = a->num_free_out;
+  v.err = reinterpret_cast<uint32_t *>(workspace);
+  v.ticket = reinterpret_cast<uint32_t *>(reinterpret_cast<uint8_t *>(workspace) + da::kVerifyTicketOffset);
+  v.capacity = capacity;
+  v.batch = p.batch;
+  v.q_len = a->q_len;
+  v.vocab = a->vocab;
+  v.free_capacity = a->free_capacity;
+  v.page_size = paged ? p.page_size : 1;
+  v.max_pages = p.max_pages_per_seq;
+  v.num_pages = p.num_pages;
+  return da::launch_verify(v, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -9,6 +9,7 @@ namespace da {
 // The workspace's header (kWorkspaceHeader bytes) is the error word at byte 0 and, in what the
 // decode kernels know as its padding, build_tables' block counter here, zero between calls.
 constexpr int64_t kTicketOffset = 64;
+constexpr int64_t kVerifyTicketOffset = 128;  // and that of decode_attn_verify
 
 // Decode over a cache in granules of 16 rows, read through their addresses (stream_split.cuh):
 // 4-bit floats (fp4_split.cu, 1152 bytes each) or 8-bit blocks (block8_split.cu, 2048 bytes);
@@ -74,6 +75,25 @@ struct TableParams {
   int32_t paged, in_place;     // in_place: an output overlaps an input that every block reads
 };
 
+// decode_attn_verify, verify.cu.
+struct VerifyParams {
+  const float *target, *draft;         // [B][Q][V], [B][Q - 1][V], rows *_stride on; draft null: certain drafts
+  int64_t target_stride, draft_stride;
+  const int32_t *target_tokens;        // [B][Q] instead of probabilities
+  const int32_t *draft_tokens, *num_draft;
+  const float *uniforms;               // [B][Q]
+  int32_t *tokens_out, *num_accepted;
+  const int32_t *seq_lens;             // optional
+  int32_t *seq_lens_out;
+  const int32_t *block_table;          // with free_pages
+  int32_t *free_pages;                 // optional
+  const int32_t *num_free;
+  int32_t *num_free_out;
+  uint32_t *err, *ticket;
+  int64_t capacity;                    // positions a row can hold
+  int32_t batch, q_len, vocab, free_capacity, page_size, max_pages, num_pages;
+};
+
 // Launches a kernel that begins with wait_for_previous_kernel (cache_ptx.cuh), so that its
 // blocks may take their places while the stream's previous kernel drains: a
 // launch after another one of ours costs about 1.5 us less. Ordering is that of the
@@ -120,6 +140,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
 cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream);
 
 }  // namespace da

@@ -107,7 +107,9 @@ enum {
                                   is outside [0, free_capacity]                            */
   DA_DEVERR_SLOT = 32u,        /* a slot outside the cache (token skipped), or more new
                                   tokens than slot_map holds (left out)                    */
-  DA_DEVERR_POSITION = 64u     /* a position outside the cosine table: token skipped       */
+  DA_DEVERR_POSITION = 64u,    /* a position outside the cosine table: token skipped       */
+  DA_DEVERR_TOKEN = 128u,      /* a drafted token past the vocabulary: the drafts end there */
+  DA_DEVERR_PROBS = 256u       /* a row whose target gives no token a probability: token -1 */
 };
 
 /*
@@ -582,6 +584,69 @@ typedef struct {
  */
 da_status decode_attn_gather(da_ctx *ctx, const da_gather_args *args, void *workspace,
                              size_t workspace_bytes, da_stream_t stream);
+
+/*
+ * Arguments of decode_attn_verify: device pointers, caller-owned. Q = q_len query tokens a row were
+ * run: the row's last known token and up to Q - 1 drafted ones.
+ *
+ *   target_probs   fp32, the target's distribution over the vocabulary after query token i of row b in
+ *                  row b Q + i, rows target_stride elements on (at least vocab); NULL: target_tokens
+ *   target_tokens  int32 [B][Q], the target's one token after each query token (greedy): a draft is
+ *                  accepted where it is the same. NULL with target_probs
+ *   draft_probs    fp32, what drafted token i of row b was drawn from in row b (Q - 1) + i, rows draft_stride
+ *                  elements on; NULL: drafts that were not drawn (each had probability 1)
+ *   draft_tokens   int32 [B][Q - 1]; a negative one ends the row's drafts (padding). NULL if Q is 1
+ *   num_draft      int32 [B], how many drafted tokens each row has (at most Q - 1); negative: the row takes
+ *                  no part (it accepts 0, its tokens are -1, its length stays); NULL: Q - 1 each
+ *   uniforms       fp32 [B][Q], random numbers in [0, 1): those of the drafted tokens, then, at Q - 1, that
+ *                  of the token drawn after them. NULL with target_tokens
+ *   tokens_out     int32 [B][Q]: the accepted tokens, the one after them, then -1
+ *   num_accepted   int32 [B]
+ *   seq_lens       int32 [B], lengths with the row's num_draft tokens in (NULL: no lengths)
+ *   seq_lens_out   int32 [B], may be seq_lens: less the tokens that were not accepted
+ *   block_table    int32 [B][max_pages_per_seq], with free_pages: the pages that only those had are put
+ *   free_pages     back on the stack int32 [free_capacity] of num_free[0] entries (as
+ *                  decode_attn_build_tables takes them): the last row's first, each row's from its end.
+ *                  NULL: no pages are given back. The table keeps its entries
+ *   num_free, num_free_out  int32 [1], may be the same; NULL without free_pages
+ */
+typedef struct {
+  const float *target_probs;
+  const float *draft_probs;
+  const int32_t *target_tokens;
+  const int32_t *draft_tokens;
+  const int32_t *num_draft;
+  const float *uniforms;
+  int32_t *tokens_out;
+  int32_t *num_accepted;
+  const int32_t *seq_lens;
+  int32_t *seq_lens_out;
+  const int32_t *block_table;
+  int32_t *free_pages;
+  const int32_t *num_free;
+  int32_t *num_free_out;
+  int64_t target_stride;
+  int64_t draft_stride;
+  int32_t q_len;
+  int32_t vocab;
+  int32_t free_capacity;
+} da_verify_args;
+
+/*
+ * Speculative decoding's last step: with p_i, q_i the target's and the draft's probabilities and u the random
+ * numbers, drafted token x_i is accepted while u_i q_i(x_i) < p_i(x_i) (the product exact). The token after the
+ * accepted ones is drawn from max(p_i - q_i, 0) where token i was rejected (from p_i where that is 0 everywhere),
+ * else from the target after the last draft: the first token whose running sum of weights, from token 0 on,
+ * passes u_{Q-1} times the sum of all. So tokens are distributed as the target's own. Sums are good to
+ * 2^-40 of themselves; weights need not sum to 1; NaN and negative ones count as 0. Lengths out of
+ * range stay as they are (DA_DEVERR_SEQ_LEN); ids outside the pool are not given back
+ * (DA_DEVERR_PAGE_INDEX), nor pages that the stack has no room for (DA_DEVERR_NO_PAGES). One kernel; it takes
+ * the workspace as the cache calls do, two that give pages back not at once. The context gives batch and the cache's
+ * layout. No output may overlap an input except where said. vocab at most 2^21.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, NOT_PLANNED, CUDA.
+ */
+da_status decode_attn_verify(da_ctx *ctx, const da_verify_args *args, void *workspace, size_t workspace_bytes,
+                             da_stream_t stream);
 
 /* Releases the context (NULL is allowed). */
 void decode_attn_destroy(da_ctx *ctx);
