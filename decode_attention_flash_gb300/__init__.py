@@ -458,7 +458,7 @@ def make_verify_args(tensors: dict, vocab: int = 0) -> VerifyArgs:
     return a
 
 
-def _enqueue(fn, name: str, ctx, args, workspace, stream, *more):
+def _enqueue(fn, name: str, ctx, args, workspace, stream):
     """One call of an entry point that enqueues on a stream. Decode steps make a few of these a
     token, so the arguments go over as plain integers (no ctypes objects are made here)."""
     if not workspace.is_cuda or not workspace.is_contiguous():
@@ -467,7 +467,7 @@ def _enqueue(fn, name: str, ctx, args, workspace, stream, *more):
         stream = torch._C._cuda_getCurrentRawStream(workspace.get_device())
     else:
         stream = _stream(stream)
-    status = fn(ctx, args, *more, workspace.data_ptr(), workspace.nbytes, stream)
+    status = fn(ctx, args, workspace.data_ptr(), workspace.nbytes, stream)
     if status != DA_OK:
         raise DecodeAttnError(status, name)
 
@@ -484,7 +484,8 @@ def decode_attn_append(ctx, args: AppendArgs, workspace: torch.Tensor, stream=No
 
 def decode_attn_append_normed(ctx, args: AppendArgs, norm: NormArgs, workspace: torch.Tensor, stream=None):
     """``decode_attn_append`` with queries and keys normed head by head first (one kernel)."""
-    _enqueue(load().decode_attn_append_normed, "decode_attn_append_normed", ctx, args, workspace, stream, norm)
+    fn = load().decode_attn_append_normed
+    _enqueue(lambda c, a, *rest: fn(c, a, norm, *rest), "decode_attn_append_normed", ctx, args, workspace, stream)
 
 
 def decode_attn_gather(ctx, args: GatherArgs, workspace: torch.Tensor, stream=None):

@@ -58,22 +58,25 @@ struct Block8Format {
 
   const uint8_t *k_lane, *v_lane;
   const float *scale;  // lane 0: K's, lane 1: V's
-  int lane, shift, dst, k0, k1, v0, v1;
+  int lane, shift, k0, k1, v0, v1;
+  uint32_t even, turn;  // where the lane's 16 bytes of rows 0 .. 3 go, and how much further those of rows 4 .. 7
   __device__ __forceinline__ Block8Format(const StreamParams &fp, int l)
       : k_lane(fp.k + l * 16), v_lane(fp.v + l * 16), scale(l == 0 ? fp.g.k_scale : fp.g.v_scale), lane(l),
         shift(fp.scale_shift) {
     const int q4 = l & 3, r8 = l >> 2;
-    dst = (l >> 3) * 128 + (((l & 7) ^ (l >> 3)) << 4);  // rows 0 .. 3; rows 4 .. 7: chunks ^ 4
+    even = (l >> 3) * 128 + (((l & 7) ^ (l >> 3)) << 4);
+    turn = (even ^ 64) - even;
     k0 = r8 * 128 + (((2 * q4) ^ r8) << 4);
     k1 = r8 * 128 + (((2 * q4 + 1) ^ r8) << 4);
     v0 = 2 * q4 * 128 + ((r8 ^ (2 * q4)) << 4);
     v1 = (2 * q4 + 1) * 128 + ((r8 ^ (2 * q4 + 1)) << 4);
   }
+  __device__ __forceinline__ uint32_t lane_at() const { return even; }
   __device__ __forceinline__ void copy(uint32_t k, uint32_t v, int64_t off, uint8_t *scales, int gi) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      cp_async_16(k + j * 512 + (dst ^ ((j & 1) << 6)), k_lane + off + j * 512);
-      cp_async_16(v + j * 512 + (dst ^ ((j & 1) << 6)), v_lane + off + j * 512);
+      cp_async_16(k + j * 512 + (j & 1 ? turn : 0u), k_lane + off + j * 512);
+      cp_async_16(v + j * 512 + (j & 1 ? turn : 0u), v_lane + off + j * 512);
     }
     if (lane < 2) cp_async_4(scales + 4 * (lane * kH + gi), scale + (off >> shift));
   }

@@ -283,7 +283,7 @@ da_status decode_attn_verify(da_ctx *ctx, const da_verify_args *a, void *workspa
   v.page_size = paged ? p.page_size : 1;
   v.max_pages = p.max_pages_per_seq;
   v.num_pages = p.num_pages;
-  return da::launch_verify(v, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
+  return da::launch_verify(v, da::ctx_num_sms(ctx), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? DA_OK : DA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -140,7 +140,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream);
+cudaError_t launch_verify(const VerifyParams &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream);
 
 }  // namespace da

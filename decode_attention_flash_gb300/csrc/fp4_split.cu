@@ -105,9 +105,10 @@ struct Fp4Format {
     cp_async_16(dst + 512, src + 512);
     if (lane < 8) cp_async_16(dst + 1024, src + 1024);
   }
+  __device__ __forceinline__ uint32_t lane_at() const { return lane * 16; }
   __device__ __forceinline__ void copy(uint32_t k, uint32_t v, int64_t off, uint8_t *, int) const {
-    copy_one(k + lane * 16, k_lane + off);
-    copy_one(v + lane * 16, v_lane + off);
+    copy_one(k, k_lane + off);
+    copy_one(v, v_lane + off);
   }
   template <int NT>
   __device__ __forceinline__ void scores(const uint8_t *stage, const uint8_t *, const uint32_t (&qf)[NT][8][2],

@@ -519,7 +519,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
     // commit group. False when the walker stays away.
     uint32_t ready = 0;
     const F fmt(fp, lane);
-    const uint32_t ring_at = smem_u32(ring);
+    const uint32_t ring_at = smem_u32(ring) + fmt.lane_at();
     uint8_t *side = smem + C::oSide + warp * C::kSideBytes;
     auto issue = [&](int i, int to) -> bool {
       if ((int)ready <= i) {

@@ -4,16 +4,23 @@
 // the target's p_0 .. p_n. Token i is accepted while u_i q_i(x_i) < p_i(x_i). At the first that is not,
 // the next token is drawn from max(p_i - q_i, 0) (rejection sampling: the tokens are then distributed
 // as the target's own), else from p_n. A draw takes the first token whose running sum of weights passes
-// r times their sum. Running sums meet borders, so they are kept far beyond fp32: a lane adds its
-// weights as pairs of floats (the rounding error of every difference and sum is carried along: 2^-45
-// or so of the sum after some hundred terms), and pairs meet as doubles. Comparisons of a draft are of
-// exact products of two floats in 64 bits.
+// r times their sum. Running sums meet borders, so they are kept far beyond fp32, as unevaluated pairs of
+// floats: the rounding error of every difference, sum and product is computed exactly (Knuth's two-sum,
+// the product's by a fused multiply) and carried along, which leaves 2^-44 or so of the sum. (Doubles
+// instead: 16 cycles of an SM for a warp's one addition; 82.7, 33.0 and 16.0 us for the three below.)
+// Two such sums side by side take the packed adds.
+// A drafted token's product is compared exactly, in 64 bits.
 //
 // What bounds it. One row of p and one of q a batch row, read once: HBM, and latency for few rows.
 // A cluster of CTAs takes a batch row. Every CTA finds the row's first rejection itself (a lane a
-// drafted token), sums its share of the vocabulary in segments of 512, and reads the other
+// drafted token), sums its share of the vocabulary in segments of 256, and reads the other
 // CTAs' sums through the cluster; the one whose share holds the border finds its segment and looks at
 // that again, from L2.
+// Measured: 256 rows of 128000 with a draft's distribution each: 45 us (floor 38.7, 85 % of the copy
+// rate); 64 rows of 151937, no draft's: 19 us (floor 5.8; the clusters of eight leave SMs without a CTA, and
+// each row takes 7 us beside its stream); 4 rows of 32000: 9 us, latency (2.4 of them the pages' return:
+// a count of the rows, then lengths, then table entries). Segments of 512: 10.1, 15.9 and 45.0 us where these take
+// 8.5, 15.7 and 44.6 (captured, from L2); of 128: 8.2, 18.1 and 58.0. Eight segments' loads at once instead of four: spills.
 #include <algorithm>
 
 #include "cache_ops.h"
@@ -24,8 +31,10 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPer = 16;          // elements of a segment a lane
+constexpr int kPer = 8;           // tokens of a segment a lane
+constexpr int kTogether = 4;      // segments that a warp loads at once (of two rows half as many)
 constexpr int kSeg = 32 * kPer;
+constexpr int kMaxCtas = 8;       // of a cluster
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -39,15 +48,8 @@ __device__ __forceinline__ uint32_t cluster_ctas() {
 }
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ double load_remote(const double *p, uint32_t rank) {
-  uint32_t at;
-  double v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(at) : "memory");
-  return v;
-}
 
-// A sum as a pair of floats.
+// An unevaluated sum of two floats.
 struct Two {
   float hi = 0.f, lo = 0.f;
   __device__ __forceinline__ void add(float x) {
@@ -55,64 +57,244 @@ struct Two {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
     hi = s;
   }
-  // max(p - q, 0), its rounding error with it; NaN counts as 0
+  __device__ __forceinline__ void add(const Two &x) {
+    add(x.hi);
+    lo = __fadd_rn(lo, x.lo);
+  }
+  // max(p - q, 0), with its rounding error; NaN counts as 0
   __device__ __forceinline__ void add_rest(float p, float q) {
-    if (!(p > q)) return;
     const float d = __fsub_rn(p, q), b = __fsub_rn(d, p);
-    lo = __fadd_rn(lo, __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b)));
-    add(d);
+    const float e = __fsub_rn(__fsub_rn(p, __fsub_rn(d, b)), __fadd_rn(q, b));
+    const bool on = p > q;
+    lo = __fadd_rn(lo, on ? e : 0.f);
+    add(on ? d : 0.f);
+  }
+  __device__ __forceinline__ bool above(const Two &x) const {
+    return __fadd_rn(__fsub_rn(hi, x.hi), __fsub_rn(lo, x.lo)) > 0.f;
+  }
+  __device__ __forceinline__ bool positive() const { return __fadd_rn(hi, lo) > 0.f; }
+  __device__ __forceinline__ bool negative() const { return __fadd_rn(hi, lo) < 0.f; }
+  __device__ __forceinline__ Two minus(const Two &x) const {
+    Two r = *this;
+    r.add(-x.hi);
+    r.lo = __fsub_rn(r.lo, x.lo);
+    return r;
+  }
+  __device__ __forceinline__ Two times(float x) const {
+    Two r;
+    r.hi = __fmul_rn(hi, x);
+    r.lo = fmaf(lo, x, fmaf(hi, x, -r.hi));
+    return r;
   }
 };
-
-// The rest of one token: `q` is the draft's row, or null, and then 1 for token `only` (-1: none).
-struct Weights {
-  const float *p, *q;
-  int only, vocab;
-  __device__ __forceinline__ float less(int i) const { return q ? q[i] : i == only ? 1.f : 0.f; }
-};
-
-__device__ __forceinline__ double inclusive(double v, int lane) {
+__device__ __forceinline__ Two load_remote(const float2 *p, uint32_t rank) {
+  uint32_t at;
+  Two v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.hi), "=f"(v.lo) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ Two shuffle(const Two &v, int lane) {
+  Two r;
+  r.hi = __shfl_sync(0xffffffffu, v.hi, lane);
+  r.lo = __shfl_sync(0xffffffffu, v.lo, lane);
+  return r;
+}
+// Sums up to this lane, itself included, of the first LANES lanes.
+template <int LANES>
+__device__ __forceinline__ Two inclusive(Two v, int lane) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const double u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
+  for (int o = 1; o < LANES; o <<= 1) {
+    Two u;
+    u.hi = __shfl_up_sync(0xffffffffu, v.hi, o);
+    u.lo = __shfl_up_sync(0xffffffffu, v.lo, o);
+    if (lane >= o) v.add(u);
   }
   return v;
 }
 // The first lane whose sum passes `border`, else the last with a weight; -1: none has one.
-__device__ __forceinline__ int pick_lane(double sum, double own, double border) {
-  const uint32_t past = __ballot_sync(0xffffffffu, sum > border && own > 0.0);
-  if (past) return __ffs(past) - 1;
-  const uint32_t some = __ballot_sync(0xffffffffu, own > 0.0);
-  return some ? 31 - __clz(some) : -1;
+__device__ __forceinline__ int pick_lane(const Two &sum, const Two &own, const Two &border) {
+  const uint32_t some = __ballot_sync(0xffffffffu, own.positive());
+  const uint32_t past = __ballot_sync(0xffffffffu, sum.above(border)) & some;
+  return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;
+}
+
+// Two floats at once (the packed adds of sm_100 and later), for two sums side by side.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pack(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack(Pair v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair sub2(Pair a, Pair b) {
+  Pair r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+struct TwoPairs {
+  Pair hi = 0, lo = 0;
+  __device__ __forceinline__ void add(Pair x) {
+    const Pair s = add2(hi, x), b = sub2(s, hi);
+    lo = add2(lo, add2(sub2(hi, sub2(s, b)), sub2(x, b)));
+    hi = s;
+  }
+  __device__ __forceinline__ void add_rest(float p0, float p1, float q0, float q1) {  // as Two::add_rest
+    const Pair p = pack(p0, p1), q = pack(q0, q1);
+    const Pair d = sub2(p, q), b = sub2(d, p), e = sub2(sub2(p, sub2(d, b)), add2(q, b));
+    float d0, d1, e0, e1;
+    unpack(d, d0, d1);
+    unpack(e, e0, e1);
+    lo = add2(lo, pack(d0 > 0.f ? e0 : 0.f, d1 > 0.f ? e1 : 0.f));
+    add(pack(fmaxf(d0, 0.f), fmaxf(d1, 0.f)));
+  }
+  __device__ __forceinline__ Two both() const {
+    Two a, b;
+    unpack(hi, a.hi, b.hi);
+    unpack(lo, a.lo, b.lo);
+    a.add(b);
+    return a;
+  }
+};
+
+// A vocabulary's weights max(p - q, 0): q is a row of the draft's, or (null) 1 for token `only` and else 0.
+// Segments begin `shift` elements before the row, where p is 16-byte aligned.
+struct Rows {
+  const float *p, *q;
+  int only, vocab, shift;
+};
+// Tokens 128 k + 4 lane + j (VEC: 16-byte loads) or 128 k + 32 j + lane of a row's segment: in any order, for
+// sums; outside the vocabulary 0.
+template <bool VEC>
+__device__ __forceinline__ void load_segment(const float *row, int first, int vocab, int lane, float (&x)[kPer]) {
+  if (first >= 0 && first + kSeg <= vocab) {
+#pragma unroll
+    for (int k = 0; k < kPer / 4; ++k) {
+      if (VEC) {
+        const float4 a = reinterpret_cast<const float4 *>(row + first)[32 * k + lane];
+        x[4 * k] = a.x, x[4 * k + 1] = a.y, x[4 * k + 2] = a.z, x[4 * k + 3] = a.w;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[4 * k + j] = row[first + 128 * k + 32 * j + lane];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = first + 128 * (k >> 2) + (VEC ? 4 * lane + (k & 3) : 32 * (k & 3) + lane);
+      x[k] = i >= 0 && i < vocab ? row[i] : 0.f;
+    }
+  }
+}
+// The certain draft's token, where a segment that begins at `first` has it: 1 less (above 0 only past 1,
+// where it is exact).
+__device__ __forceinline__ void less_certain(const Rows &w, int first, int lane, float (&x)[kPer]) {
+  const int i = w.only - first;
+  if (w.only < 0 || i < 0 || i >= kSeg) return;  // (the same for every lane)
+  const int at = (i >> 2 & 31) == lane ? (i >> 7) * 4 + (i & 3) : -1;
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) x[k] = k == at ? x[k] - 1.f : x[k];
+}
+// A CTA's segments, a warp each in turn: their sums, kAt segments at a time. DRAFT: q is a row; VEC: and
+// aligned where p is.
+template <bool DRAFT, bool VEC>
+__device__ __forceinline__ void sum_segments(const Rows &w, int g0, int ng, int warp, int lane, float2 *sums) {
+  constexpr int kAt = DRAFT ? kTogether / 2 : kTogether;
+#pragma unroll 1
+  for (int g = warp; g < ng; g += kAt * kWarps) {
+    float x[kAt][kPer], y[kAt][kPer];
+#pragma unroll
+    for (int a = 0; a < kAt; ++a) {
+      // (past the CTA's share: loaded as a segment past the vocabulary, zeros)
+      const int first = g + a * kWarps < ng ? (g0 + g + a * kWarps) * kSeg - w.shift : w.vocab;
+      load_segment<VEC>(w.p, first, w.vocab, lane, x[a]);
+      if (DRAFT) load_segment<VEC>(w.q, first, w.vocab, lane, y[a]);
+    }
+    Two s[kAt];
+#pragma unroll
+    for (int a = 0; a < kAt; ++a) {
+      TwoPairs s2;
+      if (!DRAFT) less_certain(w, (g0 + g + a * kWarps) * kSeg - w.shift, lane, x[a]);
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2) {
+        if (DRAFT) s2.add_rest(x[a][k], x[a][k + 1], y[a][k], y[a][k + 1]);
+        else s2.add(pack(fmaxf(x[a][k], 0.f), fmaxf(x[a][k + 1], 0.f)));  // (NaN counts as 0)
+      }
+      s[a] = s2.both();
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+      for (int a = 0; a < kAt; ++a) {
+        Two u;
+        u.hi = __shfl_xor_sync(0xffffffffu, s[a].hi, o);
+        u.lo = __shfl_xor_sync(0xffffffffu, s[a].lo, o);
+        s[a].add(u);
+      }
+#pragma unroll
+    for (int a = 0; a < kAt; ++a)
+      if (lane == 0 && g + a * kWarps < ng) sums[g + a * kWarps] = make_float2(s[a].hi, s[a].lo);
+  }
 }
 
 // The token of a segment, by one warp: the first whose running sum passes `border`, else the last that
-// has a weight.
-__device__ int pick_token(const Weights &w, int seg, double border, int lane) {
-  const int first = seg * kSeg + lane * kPer;
-  double x[kPer], own = 0.0;
+// has a weight; -1: none has. Lane by lane four tokens of each 128.
+__device__ __forceinline__ int pick_token(const Rows &w, int seg, Two border, int lane) {
+  const int first = seg * kSeg - w.shift;
+  float x[kPer], y[kPer];
+  load_segment<true>(w.p, first, w.vocab, lane, x);
+  if (!w.q) {
+    less_certain(w, first, lane, x);
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    const int i = first + k;
-    x[k] = 0.0;
-    if (i < w.vocab) {
-      const float a = w.p[i], b = w.less(i);
-      if (a > b) x[k] = (double)a - (double)b;
+    for (int k = 0; k < kPer; ++k) y[k] = 0.f;
+  } else {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      const int i = first + 128 * (k >> 2) + 4 * lane + (k & 3);
+      y[k] = i >= 0 && i < w.vocab ? w.q[i] : 0.f;
     }
-    own += x[k];
   }
-  const double sum = inclusive(own, lane);
-  const int l = pick_lane(sum, own, border);
-  if (l < 0) return -1;
-  int token = -1;
-  double at = sum - own;
+  constexpr int kGroups = kPer / 4;
+  Two own[kGroups], sum[kGroups];
 #pragma unroll
-  for (int k = 0; k < kPer; ++k) {
-    if (x[k] > 0.0 && (token < 0 || at <= border)) token = first + k;
-    at += x[k];
+  for (int g = 0; g < kGroups; ++g) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) own[g].add_rest(x[4 * g + j], y[4 * g + j]);
+    sum[g] = own[g];
   }
-  return __shfl_sync(0xffffffffu, token, l);
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) {
+      Two u;
+      u.hi = __shfl_up_sync(0xffffffffu, sum[g].hi, o);
+      u.lo = __shfl_up_sync(0xffffffffu, sum[g].lo, o);
+      if (lane >= o) sum[g].add(u);
+    }
+  // the group: the last with a weight whose tokens begin at or below the border
+  int token = -1;
+#pragma unroll
+  for (int g = 0; g < kGroups; ++g) {
+    const Two all = shuffle(sum[g], 31);
+    if (all.positive() && (token < 0 || !border.negative())) {
+      const int l = pick_lane(sum[g], own[g], border);
+      Two at = sum[g].minus(own[g]);
+      int mine = -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (x[4 * g + j] > y[4 * g + j] && (mine < 0 || !at.above(border))) mine = first + 128 * g + 4 * lane + j;
+        at.add_rest(x[4 * g + j], y[4 * g + j]);
+      }
+      token = __shfl_sync(0xffffffffu, mine, l);
+    }
+    border = border.minus(all);
+  }
+  return token;
 }
 
 __device__ __forceinline__ int drafts_of(const VerifyParams &p, int b) {
@@ -182,29 +364,30 @@ __device__ void release(const VerifyParams &p, int *scan) {
   if (err) atomicOr(p.err, err);
 }
 
-__global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant__ VerifyParams p) {
-  extern __shared__ double seg_sum[];  // of this CTA's segments
-  __shared__ double s_total;
-  __shared__ int s_accepted, s_rejected, s_token, s_last, s_scan[kWarps];
+__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p) {
+  extern __shared__ float2 seg_sum[];  // of this CTA's segments
+  __shared__ float2 s_total;
+  __shared__ int s_accepted, s_rejected, s_token, s_home, s_last, s_scan[kWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)cta_rank(), ctas = (int)cluster_ctas();
   const int b = blockIdx.x / ctas, Q = p.q_len;
   begin_dependent();
-  const int n = drafts_of(p, b);
   const int32_t *draft = p.draft_tokens + (int64_t)b * (Q - 1);
+  const int n = drafts_of(p, b);
   uint32_t err = 0;
 
-  // ---- the first drafted token that is not accepted, a lane each
+  // ---- the first drafted token that is not accepted, a lane each (the lanes do not wait for n to load
+  // their token's probabilities)
   if (warp == 0) {
     int kept = max(n, 0);
     bool rejected = false;
-    for (int base = 0; base < n; base += 32) {
+    for (int base = 0; base < Q - 1; base += 32) {
       const int i = base + lane;
-      bool ok = false, real = false;
-      if (i < n) {
+      bool ok = false, real = false, past = false;
+      if (i < Q - 1) {
         const int x = draft[i];
-        real = x >= 0 && x < p.vocab;
-        if (x >= p.vocab) err |= DA_DEVERR_TOKEN;
+        past = x >= p.vocab;
+        real = x >= 0 && !past;
         if (real && p.target_tokens) {
           ok = p.target_tokens[(int64_t)b * Q + i] == x;
         } else if (real) {
@@ -218,9 +401,10 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
         const int l = __ffs(no) - 1;
         kept = base + l;
         rejected = __shfl_sync(0xffffffffu, (int)real, l) != 0;  // (padding ends the drafts, rejecting none)
-        if (lane > l) err = 0;  // (tokens behind it do not matter)
+        if (lane == l && past) err |= DA_DEVERR_TOKEN;
         break;
       }
+      if (base + 32 >= n) break;
     }
     if (lane == 0) {
       s_accepted = kept;
@@ -235,82 +419,72 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
     if (threadIdx.x == 0) s_token = p.target_tokens[(int64_t)b * Q + a];
   } else if (n >= 0) {
     // ---- the next token
-    Weights w;
+    Rows w;
     w.vocab = p.vocab;
     w.p = p.target + ((int64_t)b * Q + a) * p.target_stride;
     w.q = s_rejected && p.draft ? p.draft + ((int64_t)b * (Q - 1) + a) * p.draft_stride : nullptr;
     w.only = s_rejected && !p.draft ? draft[a] : -1;
-    const int segs = (p.vocab + kSeg - 1) / kSeg;
+    w.shift = (int)(reinterpret_cast<uintptr_t>(w.p) >> 2) & 3;
+    const int segs = (p.vocab + w.shift + kSeg - 1) / kSeg;
     const int g0 = (int)((int64_t)segs * rank / ctas), ng = (int)((int64_t)segs * (rank + 1) / ctas) - g0;
     const float r = p.uniforms[(int64_t)b * Q + Q - 1];
     while (true) {
-      for (int g = warp; g < ng; g += kWarps) {
-        const int first = (g0 + g) * kSeg + lane;
-        float x[kPer], y[kPer];
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          const int i = first + 32 * k;
-          x[k] = i < p.vocab ? w.p[i] : 0.f;
-          y[k] = i < p.vocab ? w.less(i) : 0.f;
-        }
-        Two s;
-#pragma unroll
-        for (int k = 0; k < kPer; ++k) s.add_rest(x[k], y[k]);
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float hi = __shfl_xor_sync(0xffffffffu, s.hi, o), lo = __shfl_xor_sync(0xffffffffu, s.lo, o);
-          s.add(hi);
-          s.lo = __fadd_rn(s.lo, lo);
-        }
-        if (lane == 0) seg_sum[g] = (double)s.hi + (double)s.lo;
-      }
+      if (!w.q) sum_segments<false, true>(w, g0, ng, warp, lane, seg_sum);
+      else if ((((reinterpret_cast<uintptr_t>(w.p) ^ reinterpret_cast<uintptr_t>(w.q)) >> 2) & 3) == 0)
+        sum_segments<true, true>(w, g0, ng, warp, lane, seg_sum);
+      else sum_segments<true, false>(w, g0, ng, warp, lane, seg_sum);
       __syncthreads();
       // a lane's segments of the CTA's, and the CTA's of the cluster's
       const int per = (ng + 31) / 32, s0 = min(lane * per, ng), s1 = min(s0 + per, ng);
-      double own = 0.0, sum = 0.0;
+      Two own, sum;
       if (warp == 0) {
-        for (int g = s0; g < s1; ++g) own += seg_sum[g];
-        sum = inclusive(own, lane);
-        if (lane == 31) s_total = sum;
+        for (int g = s0; g < s1; ++g) {
+          Two x;
+          x.hi = seg_sum[g].x, x.lo = seg_sum[g].y;
+          own.add(x);
+        }
+        sum = inclusive<32>(own, lane);
+        if (lane == 31) s_total = make_float2(sum.hi, sum.lo);
       }
       cluster_arrive();
       cluster_wait();
-      const double part = lane < ctas ? load_remote(&s_total, (uint32_t)lane) : 0.0;
-      cluster_arrive();  // (nobody's sum is written again, and nobody leaves, before all have read)
-      const double upto = inclusive(part, lane);
-      const double total = __shfl_sync(0xffffffffu, upto, 31);
-      if (!(total > 0.0 && total < 1e300)) {
-        cluster_wait();
-        if (w.q || w.only >= 0) {  // target and draft alike everywhere, up to rounding: the target's own
-          w.q = nullptr;
-          w.only = -1;
-          continue;
-        }
-        err |= DA_DEVERR_PROBS;  // no token has a probability
-        break;
-      }
-      const double border = (double)(r > 0.f ? r : 0.f) * total;
-      const int home = pick_lane(upto, part, border);
-      winner = rank == home;
-      if (winner && warp == 0) {
-        const double rest = border - __shfl_sync(0xffffffffu, upto - part, home);
-        const int l = pick_lane(sum, own, rest);
-        double at = sum - own;
-        int seg = -1;
-        double before = 0.0;
-        for (int g = s0; g < s1; ++g) {
-          if (seg_sum[g] > 0.0 && (seg < 0 || at <= rest)) {
-            seg = g;
-            before = at;
+      if (warp == 0) {
+        Two part;
+        if (lane < ctas) part = load_remote(&s_total, (uint32_t)lane);
+        const Two upto = inclusive<kMaxCtas>(part, lane), total = shuffle(upto, ctas - 1);
+        const Two border = total.times(r > 0.f ? r : 0.f);
+        const bool some = total.hi > 0.f && total.hi < __int_as_float(0x7f800000);
+        const int home = some ? pick_lane(upto, part, border) : -1;
+        if (home == rank) {
+          const Two rest = border.minus(shuffle(upto.minus(part), home));
+          const int l = pick_lane(sum, own, rest);
+          Two at = sum.minus(own), before;
+          int seg = -1;
+          for (int g = s0; g < s1; ++g) {
+            Two x;
+            x.hi = seg_sum[g].x, x.lo = seg_sum[g].y;
+            if (x.positive() && (seg < 0 || !at.above(rest))) {
+              seg = g;
+              before = at;
+            }
+            at.add(x);
           }
-          at += seg_sum[g];
+          seg = __shfl_sync(0xffffffffu, seg, l);
+          const int token = pick_token(w, g0 + seg, rest.minus(shuffle(before, l)), lane);
+          if (lane == 0) s_token = token;
         }
-        seg = __shfl_sync(0xffffffffu, seg, l);
-        before = __shfl_sync(0xffffffffu, before, l);
-        const int token = pick_token(w, g0 + seg, rest - before, lane);
-        if (lane == 0) s_token = token;
+        if (lane == 0) s_home = home;
       }
+      cluster_arrive();  // (nobody's sum is written again, and nobody leaves, before all have read)
       cluster_wait();
+      const int home = s_home;
+      winner = rank == max(home, 0);
+      if (home < 0 && (w.q || w.only >= 0)) {  // target and draft alike everywhere, up to rounding: the target's own
+        w.q = nullptr;
+        w.only = -1;
+        continue;
+      }
+      if (home < 0) err |= DA_DEVERR_PROBS;  // no token has a probability
       break;
     }
   }
@@ -342,21 +516,23 @@ __global__ void __launch_bounds__(kThreads) verify_kernel(const __grid_constant_
 
 }  // namespace
 
-// CTAs of a cluster: as many as leave each a segment a warp.
-static int verify_ctas(const VerifyParams &p) {
+// CTAs of a cluster: as many as the SMs hold at once (four each) and as leave each a segment a warp.
+// 256 rows of 128000: 8 CTAs a row 59.3 us, 4 48.1, 2 42.6; 64 of 151937: 8 18.0, 4 18.2, 2 21.5
+// (with segments of 512).
+static int verify_ctas(const VerifyParams &p, int num_sms) {
   if (p.target_tokens) return 1;
-  int c = 8;
-  while (c > 1 && (int64_t)p.vocab < (int64_t)c * kSeg * kWarps) c /= 2;
+  int c = kMaxCtas;
+  while (c > 1 && ((int64_t)p.batch * c > num_sms * 4 || (int64_t)p.vocab < (int64_t)c * kSeg * kWarps / 2)) c /= 2;
   return c;
 }
 
-cudaError_t launch_verify(const VerifyParams &p, cudaStream_t stream) {
-  const int ctas = verify_ctas(p);
-  const int segs = (p.vocab + kSeg - 1) / kSeg;
+cudaError_t launch_verify(const VerifyParams &p, int num_sms, cudaStream_t stream) {
+  const int ctas = verify_ctas(p, num_sms);
+  const int segs = (p.vocab + 3 + kSeg - 1) / kSeg;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)p.batch * ctas);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.target_tokens ? 0 : (size_t)((segs + ctas - 1) / ctas) * sizeof(double);
+  cfg.dynamicSmemBytes = p.target_tokens ? 0 : (size_t)((segs + ctas - 1) / ctas) * sizeof(float2);
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
