@@ -5,7 +5,11 @@
 // integer code, exact in f16. A granule of 16 positions lies in one block, so
 //   S^T = (K codes) Q^T * kscale,   O^T += vscale * (V codes)^T P^T
 // with the products on f16 operands with fp32 sums and the scales applied to them in fp32: any
-// fp32 scale serves, and 16 positions cost 4 + 32 multiplies a lane beside their 16 products.
+// fp32 scale serves. With sixteen rows a unit, where the scheduler's issue is what bounds the kernel, the V
+// scale joins the weights instead, over a power of two that O is in units of (but where it is far below
+// that, or not finite), and integers meet Q as u 2^-24, u the code plus 128, the f16 whose bits are u: what
+// the 128 adds is the same for every token and is taken off the score in fp32. (With eight rows, which HBM
+// bounds, both cost more than they save: one row of 131072 tokens, 64 heads, integers: 56.6 -> 59.0 us.)
 //
 // What bounds it. 16 positions of one kv head are 4096 bytes, 732 cycles of a scheduler at the
 // measured copy bandwidth; their conversions, products and weights take about 250. So HBM does.
@@ -36,6 +40,11 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
     hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
   }
 }
+// The same with the bytes u as f16 of those bits, u 2^-24.
+__device__ __forceinline__ void bits_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
+  lo = prmt(w, 0u, 0x4140);
+  hi = prmt(w, 0u, 0x4342);
+}
 template <bool INT>
 __device__ __forceinline__ uint32_t biased(uint32_t w) {
   return INT ? w ^ 0x80808080u : w;
@@ -44,17 +53,23 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int c) {
   return c == 0 ? v.x : c == 1 ? v.y : c == 2 ? v.z : v.w;
 }
 
-template <bool INT>
+// Up to eight rows a unit: 32 tokens a stage, seven streaming warps, Q in registers. Sixteen, whose O takes
+// 64 registers: 16 tokens a stage, eleven warps in 168 registers, Q in shared memory (16 rows of 1000..20000
+// tokens, 4 query tokens: 95.7 us; as for eight rows, in 255 registers, 102; fifteen warps in 128: 106).
+template <bool INT, int ROWS>
 struct Block8Format {
-  static constexpr int kT = 32;
+  static constexpr int kT = ROWS == 1 ? 32 : 16;
   static constexpr int kH = kT / 16;
   static constexpr int kGranBytes = 2048;
   static constexpr int kSideBytes = 16;  // K's scales, then V's
   static constexpr bool kHeadScales = false;
   static constexpr bool kCareful = true;
-  static constexpr int kWarps(int) { return 7; }
+  static constexpr bool kBlockScales = true;
+  static constexpr bool kFoldsV = ROWS == 2;
+  static constexpr bool kBiased = INT && ROWS == 2;
+  static constexpr int kWarps(int nt) { return nt == 1 ? 7 : 11; }
   static constexpr int kStages(int) { return 3; }
-  static constexpr bool kQShared(int) { return false; }
+  static constexpr bool kQShared(int nt) { return nt == 2; }
 
   const uint8_t *k_lane, *v_lane;
   const float *scale;  // lane 0: K's, lane 1: V's
@@ -80,9 +95,38 @@ struct Block8Format {
     }
     if (lane < 2) cp_async_4(scales + 4 * (lane * kH + gi), scale + (off >> shift));
   }
+  __device__ static __forceinline__ float v_scale(const uint8_t *scales, int gi) {
+    return reinterpret_cast<const float *>(scales)[kH + gi];
+  }
+  // 128 times the sum of a query's elements (this lane: a quarter of row r8's), for the lane's score columns.
+  template <int NT>
+  __device__ static __forceinline__ void bias(const uint32_t (&qf)[NT][8][2], const uint4 *qs, int lane, float (&qbias)[NT][2]) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float sum = 0.f;
+#pragma unroll
+      for (int s = 0; s < 8; ++s)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t w;
+          if constexpr (kQShared(NT)) {
+            const uint4 q = qs[s * 32];
+            w = nt ? (k ? q.w : q.z) : (k ? q.y : q.x);
+          } else {
+            w = qf[nt][s][k];
+          }
+          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+          sum += f.x + f.y;
+        }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) qbias[nt][e] = 128.f * __shfl_sync(0xffffffffu, sum, (2 * (lane & 3) + e) * 4);
+    }
+  }
   template <int NT>
   __device__ __forceinline__ void scores(const uint8_t *stage, const uint8_t *scales, const uint32_t (&qf)[NT][8][2],
-                                         const uint4 *, float (&s)[NT][kH][4]) const {
+                                         const uint4 *qs, const float (&qbias)[NT][2], float (&s)[NT][kH][4]) const {
     const float *ks = reinterpret_cast<const float *>(scales);
 #pragma unroll
     for (int gi = 0; gi < kH; ++gi) {
@@ -97,15 +141,29 @@ struct Block8Format {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         uint32_t a0, a1, a2, a3;
-        codes_to_f16<INT>(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
-        codes_to_f16<INT>(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
+        if (kBiased) {
+          bits_to_f16(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
+          bits_to_f16(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
+        } else {
+          codes_to_f16<INT>(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
+          codes_to_f16<INT>(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
+        }
+        if constexpr (kQShared(NT)) {
+          const uint4 q = qs[c * 32];
+          mma_f16_16816(s[0][gi], a0, a1, a2, a3, q.x, q.y);
+          mma_f16_16816(s[NT - 1][gi], a0, a1, a2, a3, q.z, q.w);
+        } else {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][gi], a0, a1, a2, a3, qf[nt][c][0], qf[nt][c][1]);
+          for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][gi], a0, a1, a2, a3, qf[nt][c][0], qf[nt][c][1]);
+        }
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][gi][e] *= ks[gi];
+        for (int e = 0; e < 4; ++e) {
+          if (kBiased) s[nt][gi][e] = fmaf(s[nt][gi][e], 0x1p24f, -qbias[nt][e & 1]);
+          s[nt][gi][e] *= ks[gi];
+        }
     }
   }
   // Masked tokens weigh 0: their rows must not hold NaN codes, nor a granule that was not copied
@@ -119,12 +177,17 @@ struct Block8Format {
     if (lane < kH && ((valid >> (16 * lane)) & 0xFFFFu) == 0) reinterpret_cast<float *>(scales)[kH + lane] = 0.f;
   }
   template <int NT>
-  __device__ __forceinline__ void values(const uint8_t *v, const uint8_t *scales, const uint32_t (&pb)[NT][kH][2],
-                                         float (&oacc)[NT][8][4]) const {
+  __device__ __forceinline__ void values(const uint8_t *v, const float (&vmul)[kH], bool fold,
+                                         const uint32_t (&pb)[NT][kH][2], float (&oacc)[NT][8][4]) const {
+    if (kFoldsV && fold) products<NT, true>(v, vmul, pb, oacc);
+    else products<NT, false>(v, vmul, pb, oacc);
+  }
+  template <int NT, bool FOLD>
+  __device__ __forceinline__ void products(const uint8_t *v, const float (&vmul)[kH], const uint32_t (&pb)[NT][kH][2],
+                                           float (&oacc)[NT][8][4]) const {
 #pragma unroll
     for (int gi = 0; gi < kH; ++gi) {
       const uint8_t *gv = v + gi * kGranBytes;
-      const float vs = reinterpret_cast<const float *>(scales)[kH + gi];
       // tokens 2 q4, 2 q4 + 1 and the same + 8, dims 16 r8 .. 16 r8 + 15 of each
       const uint4 w0 = *reinterpret_cast<const uint4 *>(gv + v0), w1 = *reinterpret_cast<const uint4 *>(gv + v1);
       const uint4 w8 = *reinterpret_cast<const uint4 *>(gv + v0 + 1024);
@@ -140,10 +203,14 @@ struct Block8Format {
           codes_to_f16<INT>(prmt(x8, x9, k ? 0x7362 : 0x5140), a2, a3);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float o[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16_16816(o, a0, a1, a2, a3, pb[nt][gi][0], pb[nt][gi][1]);
+            if (FOLD) {
+              mma_f16_16816(oacc[nt][2 * c + k], a0, a1, a2, a3, pb[nt][gi][0], pb[nt][gi][1]);
+            } else {
+              float o[4] = {0.f, 0.f, 0.f, 0.f};
+              mma_f16_16816(o, a0, a1, a2, a3, pb[nt][gi][0], pb[nt][gi][1]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) oacc[nt][2 * c + k][e] = fmaf(o[e], vs, oacc[nt][2 * c + k][e]);
+              for (int e = 0; e < 4; ++e) oacc[nt][2 * c + k][e] = fmaf(o[e], vmul[gi], oacc[nt][2 * c + k][e]);
+            }
           }
         }
       }
@@ -166,14 +233,14 @@ struct Block8Format {
   }
   // values() token by token, leaving out what a row's mask leaves out.
   template <int NT>
-  __device__ __forceinline__ void values_kept(const uint8_t *v, const uint8_t *scales, uint32_t valid,
+  __device__ __forceinline__ void values_kept(const uint8_t *v, const float (&vmul)[kH], uint32_t valid,
                                               const float (&s)[NT][kH][4], const float (&y)[NT][2][2 * kH],
                                               float (&oacc)[NT][8][4]) const {
     const int q4 = lane & 3, r8 = lane >> 2;
     const float ninf = -__int_as_float(0x7f800000);
 #pragma unroll
     for (int k = 0; k < 2 * kH; ++k) {
-      const float vs = reinterpret_cast<const float *>(scales)[kH + (k >> 1)];
+      const float vs = vmul[k >> 1];
       for (int r = 0; r < 8; ++r) {  // token 8 k + r, whose weights lane (r, q4) has
         float w[NT][2];
 #pragma unroll
@@ -208,16 +275,16 @@ struct Block8Format {
 };
 
 template <bool INT, int NT, int MOD>
-__global__ void __launch_bounds__(StreamLayout<Block8Format<INT>, NT>::kThreads, 1)
+__global__ void __launch_bounds__(StreamLayout<Block8Format<INT, NT>, NT>::kThreads, 1)
     block8_split_kernel(const StreamParams fp) {
   begin_dependent();
-  stream_split<Block8Format<INT>, NT, MOD>(fp);
+  stream_split<Block8Format<INT, NT>, NT, MOD>(fp);
 }
 
 template <bool INT, int NT, int MOD>
 cudaError_t block8_attr() {
   return cudaFuncSetAttribute(block8_split_kernel<INT, NT, MOD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              StreamLayout<Block8Format<INT>, NT>::kTotal);
+                              StreamLayout<Block8Format<INT, NT>, NT>::kTotal);
 }
 template <bool INT>
 cudaError_t block8_attrs() {
@@ -235,7 +302,7 @@ cudaError_t launch(const StreamParams &p, int ctas, cudaStream_t stream) {
   const int mod = gqa_mod(p.g);
 #define DA_B8(NT, M)                                                                                          \
   return launch_dependent(block8_split_kernel<INT, NT, M>, (unsigned)ctas,                                     \
-                          StreamLayout<Block8Format<INT>, NT>::kThreads, StreamLayout<Block8Format<INT>, NT>::kTotal, \
+                          StreamLayout<Block8Format<INT, NT>, NT>::kThreads, StreamLayout<Block8Format<INT, NT>, NT>::kTotal, \
                           stream, p)
   if (p.g.group <= 8) {
     if (mod == 0) DA_B8(1, 0);
@@ -251,11 +318,12 @@ cudaError_t launch(const StreamParams &p, int ctas, cudaStream_t stream) {
 
 }  // namespace
 
-int block8_tile() { return Block8Format<false>::kT; }
-int block8_warps(int group) { return Block8Format<false>::kWarps(group <= 8 ? 1 : 2); }
+int block8_tile(int group) { return group <= 8 ? Block8Format<false, 1>::kT : Block8Format<false, 2>::kT; }
+int block8_warps(int group) { return Block8Format<false, 1>::kWarps(group <= 8 ? 1 : 2); }
 
 cudaError_t block8_prepare() {
-  const cudaError_t e = block8_attrs<false>();
+  cudaError_t e = append_blocks_prepare();
+  if (e == cudaSuccess) e = block8_attrs<false>();
   return e != cudaSuccess ? e : block8_attrs<true>();
 }
 

@@ -11,12 +11,12 @@
 // loses half a bit on average.
 //
 // The layout. The tokens of one block (a run, neighbours in slot_map) are the work of a group of
-// n / 16 warps, for one head and K or V: a warp holds 16 of their rows in registers (two rows of 16 lanes at a
-// time, as in cache_rows.cu), normed and turned; the greatest |x| of the group's warps meets in shared
-// memory; then the rows go out as codes. So a row is read once. Only where the scale grew the
-// group reads the block's other rows, 16 a warp, and writes them rounded again. Runs are found by the warps
-// themselves: a group looks through a window of tokens for those whose predecessor is in another block.
-// Queries are the other blocks of the grid, as in cache_rows.cu.
+// n / 16 warps, for one head and K or V: a warp stages 16 of their rows in shared memory by asynchronous
+// copies and turns them in place (two rows of 16 lanes at a time, as in cache_rows.cu); the greatest |x| of
+// the group's warps meets in shared memory; then the rows go out as codes. So a row is read once. Only where
+// the scale grew the group reads the block's other rows, 16 a warp, and writes them rounded again. Runs are
+// found by the warps themselves: a group looks through a window of tokens for those whose predecessor is in
+// another block. Queries are the other blocks of the grid, as in cache_rows.cu.
 #include <algorithm>
 
 #include "cache_rows.cuh"
@@ -27,10 +27,19 @@ namespace {
 constexpr int kRows = 16;      // rows of a run, and of a block, that a warp has
 constexpr int kMinWarps = 4;   // of a CTA
 constexpr int kMaxWarps = 16;
+constexpr int kPerSm = 5;      // CTAs of kMinWarps an SM
 
+// The greater of two; NaN wins for integers (an e4m3 code can be NaN by itself).
 template <bool INT>
 __device__ __forceinline__ float max_of(float a, float b) {
-  return INT ? max_nan(a, b) : fmaxf(a, b);  // (an e4m3 code can be NaN by itself)
+  return INT ? max_nan(a, b) : fmaxf(a, b);
+}
+template <bool INT>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t w) {  // of bf16 pairs; a is not negative
+  w &= 0x7FFF7FFFu;
+  const __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162 *>(&a), y = *reinterpret_cast<__nv_bfloat162 *>(&w);
+  const __nv_bfloat162 r = INT ? __hmax2_nan(x, y) : __hmax2(x, y);
+  return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 // The least power of two that brings |x| <= a into the codes' range: 448 = 1.75 2^8, 127 = 1.984375 2^6.
@@ -51,6 +60,27 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
     return code(a) | (code(b) << 8) | (code(c) << 16) | (code(d) << 24);
   }
   return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
+}
+// A row's eight elements over the scale, as codes. Integers of finite rows (nothing past 127) by adding
+// 1.5 2^23, after which the low byte of a float is its nearest integer, ties to even.
+template <bool INT>
+__device__ __forceinline__ uint2 codes8(const uint4 &row, float inv, bool finite) {
+  Eight x = times(values8(row), inv);
+  float e[8];
+  if (INT && finite) {
+    const Pair m = pack(12582912.f, 12582912.f);
+    uint32_t w[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) unpack(add2(x.v[i], m), e[2 * i], e[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = prmt(prmt(__float_as_uint(e[4 * i]), __float_as_uint(e[4 * i + 1]), 0x0040),
+                  prmt(__float_as_uint(e[4 * i + 2]), __float_as_uint(e[4 * i + 3]), 0x0040), 0x5410);
+    return make_uint2(w[0], w[1]);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) unpack(x.v[i], e[2 * i], e[2 * i + 1]);
+  return make_uint2(codes4<INT>(e[0], e[1], e[2], e[3]), codes4<INT>(e[4], e[5], e[6], e[7]));
 }
 // Four codes times `ratio`, as codes.
 template <bool INT>
@@ -73,45 +103,46 @@ __device__ __forceinline__ uint32_t again4(uint32_t w, float ratio) {
 // Whether every position that turns a pair of token t is in the table.
 __device__ __forceinline__ bool positions_ok(const CacheRowParams &p, int64_t t) {
   bool ok = true;
-  int last = -1;
-  for (int i = 0; i < p.rope_pairs; ++i) {
-    const int a = p.pair_axis[i];
-    if (a == last) continue;
-    last = a;
-    const int pos = p.positions[(int64_t)a * p.position_stride + t];
+  for (int i = 0; i < p.num_axes; ++i) {
+    const int pos = p.positions[(int64_t)p.axes[i] * p.position_stride + t];
     ok = ok && pos >= 0 && pos < p.max_position;
   }
   return ok;
 }
 
-// The first kv_blocks CTAs have the keys and values, the others the queries (a warp a part of a token).
-template <bool INT, bool NORM>
-__global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __grid_constant__ CacheRowParams p,
+// kv_blocks CTAs have the keys and values, the others the queries (a warp a part of a token).
+// WARPS: of a CTA, at most.
+template <bool INT, bool NORM, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) append_blocks_kernel(const __grid_constant__ CacheRowParams p,
                                                                        const int kv_blocks) {
-  __shared__ uint32_t written_all[kMinWarps][8];  // rows of the block that the run writes, per group
+  extern __shared__ uint4 staged_all[];  // [warp][row][16]
+  __shared__ uint32_t written_all[kMinWarps][256 / 32];  // rows of the block that the run writes, per group
   __shared__ float amax_all[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   begin_dependent();
-  if ((int)blockIdx.x >= kv_blocks) {
-    const int64_t item = (int64_t)((int)blockIdx.x - kv_blocks) * warps + warp;
-    const int64_t t = item / p.parts;
+  // The two kinds alternate as long as there are both: keys and values wait for memory, queries stream.
+  const int both = 2 * min(kv_blocks, (int)gridDim.x - kv_blocks), b = (int)blockIdx.x;
+  const bool queries = b < both ? (b & 1) != 0 : 2 * kv_blocks < (int)gridDim.x;
+  const uint32_t block = b < both ? b >> 1 : b - both / 2;  // of its kind
+  if (queries) {
+    const uint32_t item = block * warps + warp;
+    const uint32_t t = item / (uint32_t)p.parts;
     const int part = (int)(item - t * p.parts);
-    if (t >= p.num_tokens) return;
+    if (t >= (uint32_t)p.num_tokens) return;
     const int nq = (p.num_q_heads + 3) / 4;
     const QueryLane<128> ql(p, lane);
     int64_t slot;
     float c[8], s[8];
-    append_queries<128, NORM>(p, t, lane, ql, (int)((int64_t)part * nq / p.parts),
-                              (int)((int64_t)(part + 1) * nq / p.parts), p.num_q_heads, slot, c, s);
+    append_queries<128, NORM>(p, t, lane, ql, (int)((uint32_t)(part * nq) / (uint32_t)p.parts),
+                              (int)((uint32_t)((part + 1) * nq) / (uint32_t)p.parts), p.num_q_heads, slot, c, s);
     return;
   }
   const int n = p.kv_groups, shift = 31 - __clz(n), gw = n / kRows;  // a block's rows, a group's warps
   const int group = warp / gw, gwarp = warp - group * gw, HK = p.num_kv_heads;
-  const int64_t windows = ((int64_t)p.num_tokens + p.window - 1) / p.window;
-  const int64_t item = (int64_t)blockIdx.x * (warps / gw) + group;
-  if (item >= windows * HK * 2) return;
-  const int64_t w0 = item / (2 * HK) * p.window;
-  const int h = (int)(item % (2 * HK)) >> 1, side = (int)(item & 1);  // side 0: K
+  const uint32_t item = block * (uint32_t)(warps / gw) + group, at = item / (uint32_t)(2 * HK);
+  const int64_t w0 = (int64_t)at * p.window;
+  if (w0 >= p.num_tokens) return;
+  const int h = (int)(item - at * (2 * HK)) >> 1, side = (int)(item & 1);  // side 0: K
   uint32_t *written = written_all[group];
   float *amax = amax_all + group * gw;
   auto meet = [&]() {
@@ -129,11 +160,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __g
   const bool turned = kl < 2 * r, second = turned && !p.rope_adjacent && kl >= r;
   const int partner = lane - kl + (turned && !p.rope_adjacent ? (second ? kl - r : kl + r) : kl);
   const bool norm = NORM && side == 0 && p.k_weight != nullptr;
-  float wo[8], wp[8];
-  if (norm) {
-    load8(p.k_weight + 8 * kl, wo);
-    load8(p.k_weight + 8 * (partner & 15), wp);
-  }
+  uint4 *mine_at = staged_all + (warp * kRows + sub) * 16 + kl;  // this lane's part of every second row
 
   auto block_of = [&](int64_t t) -> int64_t {  // -1: padding or outside the cache
     const int64_t s = p.slot_map[t];
@@ -150,14 +177,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __g
   }
   for (; leads != 0; leads &= leads - 1) {
     const int64_t t0 = w0 + __ffs(leads) - 1, blk = block_of(t0);
-    const int64_t unit = blk / (p.rows_per_page >> shift), j = blk - unit * (p.rows_per_page >> shift);  // page, block in it
-    const int64_t row0 = (unit * HK + h) * p.rows_per_page + j * n;
-    float *scale = scales + (unit * HK + h) * (p.rows_per_page >> shift) + j;
+    const uint32_t per = (uint32_t)p.rows_per_page >> shift;  // blocks of a page
+    const int64_t page = (blk >> 32) == 0 ? (int64_t)((uint32_t)blk / per) : blk / per, j = blk - page * per;
+    const int64_t row0 = (page * HK + h) * p.rows_per_page + j * n;
+    float *scale = scales + (page * HK + h) * per + j;
     const float was = *scale;
     // ---- which tokens, and which rows they write
     bool fresh = false;
-    uint32_t mine = 0;  // of the warp's 16 tokens, those that are written
-    int my_off = 0;     // lane i < 16: the row of the i-th
+    uint32_t mine = 0;  // of the warp's kRows tokens, those that are written
+    int my_off = 0;     // lane i < kRows: the row of the i-th
+    const int in32 = gwarp * kRows & 31;  // where those are among 32
     for (int base = 0; base < n; base += 32) {
       const int64_t t = t0 + base + lane;
       const bool in = base + lane < n && t < p.num_tokens;
@@ -172,10 +201,10 @@ __global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __g
       const int off = use ? (int)(p.slot_map[t] & (n - 1)) : -1;
       fresh = fresh || __any_sync(0xffffffffu, off == 0);
       const uint32_t used = __ballot_sync(0xffffffffu, use);
-      const int o16 = __shfl_sync(0xffffffffu, off, (gwarp & 1) * 16 + (lane & 15));
-      if (base / 32 == gwarp / 2) {
-        mine = (used >> ((gwarp & 1) * 16)) & 0xFFFFu;
-        my_off = o16;
+      const int o = __shfl_sync(0xffffffffu, off, in32 + lane % kRows);
+      if (base / 32 == gwarp * kRows / 32) {
+        mine = (used >> in32) & ((1u << kRows) - 1u);
+        my_off = o;
       }
       if (gwarp == 0) {  // (a run of one block: every row once)
         if (base == 0 && lane < 8) written[lane] = 0;
@@ -185,35 +214,40 @@ __global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __g
       if (m < 32) break;
     }
     // ---- the warp's rows: read, normed, turned, in bf16
-    uint4 x[kRows / 2];
-    float top = 0.f;
+    const int64_t t1 = t0 + gwarp * kRows + sub;
 #pragma unroll
-    for (int i = 0; i < kRows / 2; ++i) {
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if ((mine >> (2 * i + sub)) & 1u) x[i] = src[(t0 + gwarp * kRows + 2 * i + sub) * stride + kl];
-    }
+    for (int i = 0; i < kRows / 2; ++i)
+      if ((mine >> (2 * i + sub)) & 1u) cp_async_16(smem_u32(mine_at + 32 * i), src + (t1 + 2 * i) * stride + kl);
+    cp_async_commit();
+    uint32_t top2 = 0;
+    const int pair0 = p.rope_adjacent ? 4 * kl : 8 * (second ? kl - r : kl);
+    cp_async_wait_group<0>();  // (a lane reads what it copied itself)
 #pragma unroll 2
     for (int i = 0; i < kRows / 2; ++i) {
       if (((mine >> (2 * i)) & 3u) == 0) continue;
       const bool on = (mine >> (2 * i + sub)) & 1u;
-      const int64_t t = t0 + gwarp * kRows + 2 * i + sub;
+      uint4 x = on ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
       if (r > 0 || norm) {
         float c[8], s[8];
         if (on && turned) {
-          if (p.rope_adjacent) load_turn<4>(p, t, 4 * kl, c, s);
-          else load_turn<8>(p, t, 8 * (second ? kl - r : kl), c, s);
+          if (p.rope_adjacent) load_turn<4>(p, t1 + 2 * i, pair0, c, s);
+          else load_turn<8>(p, t1 + 2 * i, pair0, c, s);
+        }
+        if (norm) {
+          norm_key(p, x, kl, partner, turned, second, c, s);
+        } else {
           if (second)  // (b c + a s) is (x c - u s) with s of the other sign
 #pragma unroll
             for (int k = 0; k < 8; ++k) s[k] = -s[k];
+          turn_key(p, x, partner, turned, c, s);
         }
-        if (norm) norm_key(p, x[i], kl, partner, turned, c, s, wo, wp);
-        else turn_key(p, x[i], partner, turned, c, s);
+        if (on) mine_at[32 * i] = x;
+        else x = make_uint4(0u, 0u, 0u, 0u);
       }
-      float e[8];
-      values8(x[i], e);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) top = on ? max_of<INT>(top, fabsf(e[k])) : top;
+      top2 = max_abs2<INT>(max_abs2<INT>(top2, x.x), x.y);
+      top2 = max_abs2<INT>(max_abs2<INT>(top2, x.z), x.w);
     }
+    float top = max_of<INT>(bf_lo(top2), bf_hi(top2));
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) top = max_of<INT>(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) amax[gwarp] = top;
@@ -223,24 +257,21 @@ __global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __g
     const float old = fresh ? 0.f : was, need = least_scale<INT>(top);
     const float now = old == old ? (need > old || need != need ? need : old) : old;
     const float inv = now != 0.f ? __frcp_rn(now) : 0.f;
-#pragma unroll
+    const bool finite = top < __int_as_float(0x7f800000);
+    uint8_t *out = cache + row0 * 128 + kl * 8;
+#pragma unroll 2
     for (int i = 0; i < kRows / 2; ++i) {
+      if (((mine >> (2 * i)) & 3u) == 0) continue;
       const int off = __shfl_sync(0xffffffffu, my_off, 2 * i + sub);
-      if ((mine >> (2 * i + sub)) & 1u) {
-        float e[8];
-        values8(x[i], e);
-        *reinterpret_cast<uint2 *>(cache + (row0 + off) * 128 + kl * 8) =
-            make_uint2(codes4<INT>(e[0] * inv, e[1] * inv, e[2] * inv, e[3] * inv),
-                       codes4<INT>(e[4] * inv, e[5] * inv, e[6] * inv, e[7] * inv));
-      }
+      if ((mine >> (2 * i + sub)) & 1u) *reinterpret_cast<uint2 *>(out + off * 128) = codes8<INT>(mine_at[32 * i], inv, finite);
     }
     // ---- rows that stay, rounded again
     if (!fresh && now > old) {
       const float ratio = old * inv;
-      const uint32_t keep = ~(written[gwarp >> 1] >> ((gwarp & 1) * 16));
+      const uint32_t keep = ~(written[gwarp * kRows >> 5] >> in32);
       uint4 *rows = reinterpret_cast<uint4 *>(cache + (row0 + gwarp * kRows) * 128) + lane;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)  // four rows of 8 lanes
+#pragma unroll 1
+      for (int i = 0; i < kRows / 4; ++i)  // four rows of 8 lanes
         if ((keep >> (4 * i + (lane >> 3))) & 1u) {
           const uint4 a = rows[32 * i];
           rows[32 * i] = make_uint4(again4<INT>(a.x, ratio), again4<INT>(a.y, ratio), again4<INT>(a.z, ratio),
@@ -255,14 +286,26 @@ __global__ void __launch_bounds__(kMaxWarps * 32) append_blocks_kernel(const __g
 
 }  // namespace
 
+static int blocks_smem(int warps) { return warps * kRows * 256; }
+
+cudaError_t append_blocks_prepare() {
+  const int most = blocks_smem(kMaxWarps);
+  const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(append_blocks_kernel<false, false, kMaxWarps>, a, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(append_blocks_kernel<false, true, kMaxWarps>, a, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(append_blocks_kernel<true, false, kMaxWarps>, a, most);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(append_blocks_kernel<true, true, kMaxWarps>, a, most);
+  return e;
+}
+
 cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
   const int gw = p.kv_groups / kRows, warps = std::max(kMinWarps, gw);
   // Windows of one token while that makes few warps (a decode step: every token a run of its own), else
-  // wider ones, up to half a block: most groups then find no run and end, or one.
+  // wider ones, up to a block or the lanes of a warp: few groups then find no run.
   const int64_t one = (int64_t)p.num_tokens * p.num_kv_heads * 2 * gw;
   int window = 1;
-  while (window < 32 && window * 2 <= p.kv_groups && one / window > (int64_t)num_sms * 64) window *= 2;
+  while (window < 32 && window < p.kv_groups && one / window > (int64_t)num_sms * 16) window *= 2;
   p.window = window;
   const int64_t items = ((int64_t)p.num_tokens + window - 1) / window * p.num_kv_heads * 2;
   const int64_t kv_blocks = (items + warps / gw - 1) / (warps / gw);
@@ -273,11 +316,14 @@ cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, c
     p.parts = (int32_t)std::max<int64_t>(1, std::min<int64_t>(groups, (int64_t)num_sms * 32 / p.num_tokens));
     q_blocks = ((int64_t)p.num_tokens * p.parts + warps - 1) / warps;
   }
-  if (kv_blocks + q_blocks > INT32_MAX) return cudaErrorInvalidConfiguration;
+  if (kv_blocks + q_blocks > INT32_MAX / kMaxWarps) return cudaErrorInvalidConfiguration;  // (items in 32 bits)
   const unsigned grid = (unsigned)(kv_blocks + q_blocks), threads = (unsigned)warps * 32;
   const bool norm = p.q_weight || p.k_weight;
   const int kv = (int)kv_blocks;
-#define DA_BLOCKS(I, N) return launch_dependent(append_blocks_kernel<I, N>, grid, threads, 0, stream, p, kv)
+  const size_t smem = (size_t)blocks_smem(warps);
+#define DA_BLOCKS(I, N)                                                                                               \
+  return warps == kMinWarps ? launch_dependent(append_blocks_kernel<I, N, kMinWarps>, grid, threads, smem, stream, p, kv) \
+                            : launch_dependent(append_blocks_kernel<I, N, kMaxWarps>, grid, threads, smem, stream, p, kv)
   if (integers) {
     if (norm) DA_BLOCKS(true, true);
     else DA_BLOCKS(true, false);

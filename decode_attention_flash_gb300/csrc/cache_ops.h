@@ -57,6 +57,8 @@ struct CacheRowParams {
   const float *q_weight, *k_weight;  // the norm's weights of a head (latent: k_weight of 512); null: no norm
   float norm_eps;
   float *k_block_scale, *v_block_scale;  // 8-bit blocks: [pages][HKV][rows_per_page / kv_groups]
+  int32_t num_axes;            // 8-bit blocks: the distinct axes in pair_axis, and those
+  uint8_t axes[64];
   int32_t window;              // 8-bit blocks: tokens that one group of warps looks through (the launcher's)
   uint8_t pair_axis[64];
 };
@@ -122,10 +124,10 @@ inline bool is_stream(const da_problem &p) { return p.kv_dtype == DA_DTYPE_FP4_E
 cudaError_t fp4_prepare();
 cudaError_t block8_prepare();
 int fp4_tile();                // tokens per stage
-int block8_tile();
+int block8_tile(int group);
 int fp4_warps(int group);      // warps of a CTA for `group` rows per unit
 int block8_warps(int group);
-inline int stream_tile(const da_problem &p) { return is_block8(p) ? block8_tile() : fp4_tile(); }
+inline int stream_tile(const da_problem &p, int group) { return is_block8(p) ? block8_tile(group) : fp4_tile(); }
 inline int stream_warps(const da_problem &p, int group) { return is_block8(p) ? block8_warps(group) : fp4_warps(group); }
 // log2 of the units that a kv head's queries are split into, so that each has at most 16 rows
 // (one query token, dense); -1: no such split.
@@ -138,6 +140,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
                 int32_t num_splits_override, int32_t *few_tiles, int32_t *few_ctas);
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
+cudaError_t append_blocks_prepare();  // sets shared-memory attributes
 cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyParams &p, int num_sms, cudaStream_t stream);

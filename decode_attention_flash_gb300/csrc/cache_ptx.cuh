@@ -32,6 +32,38 @@ __device__ __forceinline__ void begin_dependent() {
   let_next_kernel_start();
 }
 
+// ---------------------------------------------------------------- packed fp32
+
+// Two floats in a register pair, added or multiplied by one instruction (sm_100 and later), each
+// result rounded by itself as by __fadd_rn, __fsub_rn, __fmul_rn.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pack(float a, float b) {
+  Pair r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack(Pair v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  Pair r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair sub2(Pair a, Pair b) {
+  Pair r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 // ---------------------------------------------------------------- cp.async
 
 // 16 bytes to the shared address `smem_dst` (both sides 16-byte aligned), past L1.

@@ -210,7 +210,7 @@ __device__ __forceinline__ void put_row(const CacheRowParams &p, bool on, uint8_
 // NORM: heads over their root mean square first (p.q_weight, p.k_weight); its weights take
 // registers, so fewer blocks an SM.
 template <int KIND, int HEAD, bool NORM>
-__global__ void __launch_bounds__(kWarps * 32, NORM ? 5 : 8) append_kernel(const __grid_constant__ CacheRowParams p) {
+__global__ void __launch_bounds__(kWarps * 32, NORM ? 7 : 8) append_kernel(const __grid_constant__ CacheRowParams p) {
   constexpr int kLanes = HEAD / 16;        // lanes of a query head
   constexpr int kHeads = 32 / kLanes;      // query heads a warp takes at once
   const int lane = threadIdx.x & 31;
@@ -243,9 +243,10 @@ __global__ void __launch_bounds__(kWarps * 32, NORM ? 5 : 8) append_kernel(const
     uint4 u, v;
     if (lane < kLanes) u = rope[ca], v = rope[cb];
     if (NORM && p.k_weight) {
-      const float n = head_rsqrt<32>(x, y, p.norm_eps);
-      x = normed(x, n, p.k_weight + 8 * lane);
-      y = normed(y, n, p.k_weight + 256 + 8 * lane);
+      const Eight a = values8(x), b = values8(y);
+      const float n = head_rsqrt<32, 16>(squares(a) + squares(b), p.norm_eps);
+      x = pack8(times(times(a, n), load8(p.k_weight + 8 * lane)));
+      y = pack8(times(times(b, n), load8(p.k_weight + 256 + 8 * lane)));
     }
     dst[0] = x;
     dst[32] = y;
@@ -274,14 +275,9 @@ __global__ void __launch_bounds__(kWarps * 32, NORM ? 5 : 8) append_kernel(const
         if (p.rope_adjacent) load_turn<4>(p, t, 4 * kl, c, s);
         else load_turn<8>(p, t, 8 * (second ? kl - r : kl), c, s);
       }
-      if (second)  // (b c + a s) is (x c - u s) with s of the other sign
+      if (second && !(NORM && p.k_weight))  // (b c + a s) is (x c - u s) with s of the other sign
 #pragma unroll
         for (int i = 0; i < 8; ++i) s[i] = -s[i];
-    }
-    float wo[8], wp[8];  // the norm's weights of the lane's elements and of its partner's
-    if (NORM && p.k_weight) {
-      load8(p.k_weight + 8 * kl, wo);
-      load8(p.k_weight + 8 * (partner & 15), wp);
     }
     int h = 2 * (first - nq) + ksub;
     const uint4 *ksrc = reinterpret_cast<const uint4 *>(p.k_new + t * p.k_stride) + h * 16 + kl;
@@ -308,7 +304,7 @@ __global__ void __launch_bounds__(kWarps * 32, NORM ? 5 : 8) append_kernel(const
       for (int i = 0; i < kSide; ++i) {
         if (g + i >= g1) break;
         if (NORM && p.k_weight) {
-          norm_key(p, w[i], kl, partner, kturned, c, s, wo, wp);
+          norm_key(p, w[i], kl, partner, kturned, second, c, s);
         } else if (r > 0) {
           turn_key(p, w[i], partner, kturned, c, s);
         }

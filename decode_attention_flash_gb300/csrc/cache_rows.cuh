@@ -32,6 +32,19 @@ __device__ __forceinline__ int64_t load_slot(const CacheRowParams &p, int64_t t,
   return s;
 }
 
+// The cosines and sines of pairs pair0 .. pair0 + 7 (or + 3: kPairs) at a position of the table.
+template <int kPairs>
+__device__ __forceinline__ void load_angles(const CacheRowParams &p, int pos, int pair0, float (&c)[8], float (&s)[8]) {
+  const int n = p.rope_pairs;
+  const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + pair0);
+  const float4 *row2 = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + n + pair0);
+#pragma unroll
+  for (int j = 0; j < kPairs / 4; ++j) {
+    const float4 a = __ldg(row + j), b = __ldg(row2 + j);
+    c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
+    s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
+  }
+}
 // The cosines and sines of pairs pair0 .. pair0 + 7 (or + 3: kPairs) of token t;
 // false when a position is outside the table.
 template <int kPairs>
@@ -40,14 +53,7 @@ __device__ __forceinline__ bool load_turn(const CacheRowParams &p, int64_t t, in
   if (p.rope_whole) {  // they share an axis: vector loads
     const int pos = p.positions[(int64_t)p.pair_axis[pair0] * p.position_stride + t];
     if (pos < 0 || pos >= p.max_position) return false;
-    const float4 *row = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + pair0);
-    const float4 *row2 = reinterpret_cast<const float4 *>(p.cos_sin + (int64_t)pos * 2 * n + n + pair0);
-#pragma unroll
-    for (int j = 0; j < kPairs / 4; ++j) {
-      const float4 a = __ldg(row + j), b = __ldg(row2 + j);
-      c[4 * j] = a.x, c[4 * j + 1] = a.y, c[4 * j + 2] = a.z, c[4 * j + 3] = a.w;
-      s[4 * j] = b.x, s[4 * j + 1] = b.y, s[4 * j + 2] = b.z, s[4 * j + 3] = b.w;
-    }
+    load_angles<kPairs>(p, pos, pair0, c, s);
     return true;
   }
   bool ok = true;
@@ -116,69 +122,87 @@ __device__ __forceinline__ void turn_key(const CacheRowParams &p, uint4 &v, int 
 
 // ---------------------------------------------------------------- the norm of a head
 
-// Eight consecutive weights (ordinary loads; 16-byte aligned).
-__device__ __forceinline__ void load8(const float *src, float (&w)[8]) {
-  const float4 a = reinterpret_cast<const float4 *>(src)[0], b = reinterpret_cast<const float4 *>(src)[1];
-  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
-  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+// Eight bf16 elements, or eight consecutive floats (ordinary loads; 16-byte aligned), as pairs.
+struct Eight {
+  Pair v[4];
+};
+__device__ __forceinline__ Eight values8(const uint4 &w) {
+  return {{pack(bf_lo(w.x), bf_hi(w.x)), pack(bf_lo(w.y), bf_hi(w.y)), pack(bf_lo(w.z), bf_hi(w.z)),
+           pack(bf_lo(w.w), bf_hi(w.w))}};
 }
-__device__ __forceinline__ void values8(const uint4 &v, float (&x)[8]) {
-  x[0] = bf_lo(v.x), x[1] = bf_hi(v.x), x[2] = bf_lo(v.y), x[3] = bf_hi(v.y);
-  x[4] = bf_lo(v.z), x[5] = bf_hi(v.z), x[6] = bf_lo(v.w), x[7] = bf_hi(v.w);
+__device__ __forceinline__ Eight load8(const float *src) {
+  const ulonglong2 a = reinterpret_cast<const ulonglong2 *>(src)[0], b = reinterpret_cast<const ulonglong2 *>(src)[1];
+  return {{a.x, a.y, b.x, b.y}};
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ uint32_t bf16x2_of(Pair v) {
+  float a, b;
+  unpack(v, a, b);
+  return pack_bf16(a, b);
 }
-__device__ __forceinline__ float squares(const uint4 &v) {
-  float x[8], sum = 0.f;
-  values8(v, x);
+__device__ __forceinline__ uint4 pack8(const Eight &x) {
+  return make_uint4(bf16x2_of(x.v[0]), bf16x2_of(x.v[1]), bf16x2_of(x.v[2]), bf16x2_of(x.v[3]));
+}
+__device__ __forceinline__ Eight times(const Eight &x, const Eight &y) {
+  return {{mul2(x.v[0], y.v[0]), mul2(x.v[1], y.v[1]), mul2(x.v[2], y.v[2]), mul2(x.v[3], y.v[3])}};
+}
+__device__ __forceinline__ Eight times(const Eight &x, float n) {
+  const Pair m = pack(n, n);
+  return {{mul2(x.v[0], m), mul2(x.v[1], m), mul2(x.v[2], m), mul2(x.v[3], m)}};
+}
+__device__ __forceinline__ Eight plus(const Eight &x, const Eight &y) {
+  return {{add2(x.v[0], y.v[0]), add2(x.v[1], y.v[1]), add2(x.v[2], y.v[2]), add2(x.v[3], y.v[3])}};
+}
+__device__ __forceinline__ Eight minus(const Eight &x, const Eight &y) {
+  return {{sub2(x.v[0], y.v[0]), sub2(x.v[1], y.v[1]), sub2(x.v[2], y.v[2]), sub2(x.v[3], y.v[3])}};
+}
+__device__ __forceinline__ Eight pairs8(const float (&x)[8]) {
+  return {{pack(x[0], x[1]), pack(x[2], x[3]), pack(x[4], x[5]), pack(x[6], x[7])}};
+}
+__device__ __forceinline__ float squares(const Eight &x) {
+  Pair sum = mul2(x.v[0], x.v[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sum = fmaf(x[i], x[i], sum);
-  return sum;
+  for (int i = 1; i < 4; ++i) sum = fma2(x.v[i], x.v[i], sum);
+  float a, b;
+  unpack(sum, a, b);
+  return a + b;
 }
-// 1 / sqrt(mean x^2 + eps) of a head of LANES lanes with two chunks each; every lane of the warp calls it.
-template <int LANES>
-__device__ __forceinline__ float head_rsqrt(const uint4 &a, const uint4 &b, float eps) {
-  float sum = squares(a) + squares(b);
+// 1 / sqrt(mean x^2 + eps) of a head of LANES lanes with ELEMENTS each and these sums of squares; every
+// lane of the warp calls it.
+template <int LANES, int ELEMENTS>
+__device__ __forceinline__ float head_rsqrt(float sum, float eps) {
 #pragma unroll
   for (int o = 1; o < LANES; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return rsqrtf(fmaf(sum, 1.f / (16 * LANES), eps));
+  return rsqrtf(fmaf(sum, 1.f / (LANES * ELEMENTS), eps));
 }
-// (x n) w, rounded to bf16
-__device__ __forceinline__ uint4 normed(const uint4 &v, float n, const float *weight) {
-  float x[8], w[8];
-  values8(v, x);
-  load8(weight, w);
+// Neighbours as pairs: elements 2i, 2i + 1 with cosines c[at + i].
+__device__ __forceinline__ void turn_neighbours(Eight &x, const float (&c)[8], const float (&s)[8], int at) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] * n * w[i];
-  return pack8(x);
+  for (int i = 0; i < 4; ++i) {
+    float a, b, u, v;
+    unpack(x.v[i], a, b);
+    turn(a, b, c[at + i], s[at + i], u, v);
+    x.v[i] = pack(u, v);
+  }
 }
 
 // A key of 16 lanes, 8 elements each: normed, then turned (lanes with `turned`); the partner of a
-// half-split pair is in lane `partner`, c and s are signed for the lane's half. wo, wp: the weights of
-// the lane's elements and of its partner's. Every lane of the warp calls it.
-__device__ __forceinline__ void norm_key(const CacheRowParams &p, uint4 &v, int kl, int partner, bool turned,
-                                         const float (&c)[8], const float (&s)[8], const float (&wo)[8],
-                                         const float (&wp)[8]) {
-  float sum = squares(v);
-#pragma unroll
-  for (int o = 1; o < 16; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  const float n = rsqrtf(fmaf(sum, 1.f / 128, p.norm_eps));
+// half-split pair is in lane `partner`, c and s are its angle's (`second`: the lane has the pair's second
+// elements). Every lane of the warp calls it. (The weights come from L1 for each key: 32 registers held
+// for them cost more warps than they save.)
+__device__ __forceinline__ void norm_key(const CacheRowParams &p, uint4 &v, int kl, int partner, bool turned, bool second,
+                                         const float (&c)[8], const float (&s)[8]) {
+  Eight x = values8(v);
+  const float n = head_rsqrt<16, 8>(squares(x), p.norm_eps);
   const uint4 z = make_uint4(__shfl_sync(0xffffffffu, v.x, partner), __shfl_sync(0xffffffffu, v.y, partner),
                              __shfl_sync(0xffffffffu, v.z, partner), __shfl_sync(0xffffffffu, v.w, partner));
-  float x[8];
-  values8(v, x);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = x[i] * n * wo[i];
+  x = times(times(x, n), load8(p.k_weight + 8 * kl));
   if (turned) {
     if (p.rope_adjacent) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) turn(x[2 * i], x[2 * i + 1], c[i], s[i], x[2 * i], x[2 * i + 1]);
+      turn_neighbours(x, c, s, 0);
     } else {
-      float y[8];
-      values8(z, y);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(__fmul_rn(x[i], c[i]), __fmul_rn(y[i] * n * wp[i], s[i]));
+      // (b c + a s) is (x c - y s) with y of the other sign
+      const Eight y = times(times(values8(z), second ? -n : n), load8(p.k_weight + 8 * (partner & 15)));
+      x = minus(times(x, pairs8(c)), times(y, pairs8(s)));
     }
   }
   v = pack8(x);
@@ -241,11 +265,6 @@ __device__ __forceinline__ bool append_queries(const CacheRowParams &p, int64_t 
   if (err && lane == 0) atomicOr(p.err, err);
   if (bad || padding) return false;
   const bool norm = NORM && p.q_weight != nullptr;
-  float wa[8], wb[8];
-  if (norm && g0 < gq1) {
-    load8(p.q_weight + 8 * ca, wa);
-    load8(p.q_weight + 8 * cb, wb);
-  }
   {
     const bool many = p.q_len > 1;
     const int64_t row0 = many ? (t / p.q_len * p.num_q_heads) * p.q_len + t % p.q_len : t * p.num_q_heads;
@@ -258,24 +277,17 @@ __device__ __forceinline__ bool append_queries(const CacheRowParams &p, int64_t 
         const int hd = (g + k) * kHeads + sub;
         if (g + k >= gq1 || (!NORM && hd >= HQ)) continue;
         if (norm) {
-          const float n = head_rsqrt<kLanes>(a[k], b[k], p.norm_eps);
-          float x[8], y[8];
-          values8(a[k], x);
-          values8(b[k], y);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x[i] = x[i] * n * wa[i];
-            y[i] = y[i] * n * wb[i];
-          }
+          Eight x = values8(a[k]), y = values8(b[k]);
+          const float n = head_rsqrt<kLanes, 16>(squares(x) + squares(y), p.norm_eps);
+          x = times(times(x, n), load8(p.q_weight + 8 * ca));
+          y = times(times(y, n), load8(p.q_weight + 8 * cb));
           if (split) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) turn(x[i], y[i], c[i], s[i], x[i], y[i]);
+            const Eight cc = pairs8(c), ss = pairs8(s), u = minus(times(x, cc), times(y, ss));
+            y = plus(times(y, cc), times(x, ss));
+            x = u;
           } else if (turned) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              turn(x[2 * i], x[2 * i + 1], c[i], s[i], x[2 * i], x[2 * i + 1]);
-              turn(y[2 * i], y[2 * i + 1], c[4 + i], s[4 + i], y[2 * i], y[2 * i + 1]);
-            }
+            turn_neighbours(x, c, s, 0);
+            turn_neighbours(y, c, s, 4);
           }
           a[k] = pack8(x);
           b[k] = pack8(y);

@@ -103,7 +103,8 @@ da_status validate_problem(const da_problem *p) {
     const int64_t list = (int64_t)p->sparse_block_size * p->max_sparse_blocks * 2;
     if (cap >= (1ll << 31) || list >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
     const int64_t units = ((int64_t)p->batch * p->num_kv_heads) << stream_kv_shift(*p);
-    const int64_t tiles = units * ((std::max(cap, list) + 31) / 32);
+    const int64_t tile = is_block8(*p) ? 16 : 32;  // (block8: at least)
+    const int64_t tiles = units * ((std::max(cap, list) + tile - 1) / tile);
     if (units >= (1ll << 31) || tiles >= (1ll << 31)) return DA_ERR_UNSUPPORTED;
     return DA_OK;
   }
@@ -178,8 +179,6 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
   const bool sparse = !mla && p->sparse_block_size > 0;
   const bool paged = p->kv_layout == DA_KV_PAGED;
   const bool stream = is_stream(*p);
-  const int tile = mla ? kMlaTile : stream ? stream_tile(*p) : kGqaTile;
-  const int align = sparse ? p->sparse_block_size : tile;
   // units: GQA (row, kv head); MLA (row, query token), whose heads share the latent cache
   const int Q = p->q_len > 1 ? p->q_len : 1;
   const int shift = stream ? stream_kv_shift(*p) : 0;
@@ -190,6 +189,7 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
   // rows per unit: the G query heads (times the query tokens) of a kv head; MLA: all heads
   const int rows = mla ? p->num_q_heads : (p->num_q_heads / p->num_kv_heads * Q) >> shift;
   const int dv = p->head_dim_v;
+  const int tile = mla ? kMlaTile : stream ? stream_tile(*p, rows) : kGqaTile;
 
   // positions per unit the split kernel walks (sparse: the compacted list)
   std::vector<int64_t> unit_len((size_t)units);

@@ -39,7 +39,8 @@ constexpr float kRaise = 32768.f;    // a sum of weights past this raises the re
 
 // A format F of the cache is a struct of constants (tokens of a stage, granule bytes, streaming
 // warps, stages of a ring, bytes of scales beside a stage) and of what a lane does: copy a half
-// of a stage, S^T = K Q^T, drop what masked tokens hold, O^T += V^T P^T.
+// of a stage, S^T = K Q^T, drop what masked tokens hold, O^T += V^T P^T. kHeadScales: K and V have
+// a scale a head; kBlockScales: a scale a granule, which kFoldsV joins to the weights; kBiased: K codes meet Q with a bias added.
 template <class F, int NT>
 struct StreamLayout {
   static constexpr int kT = F::kT;                               // tokens per stage
@@ -565,6 +566,9 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
         trow[nt][e] = (nt * 8 + 2 * q4 + e) % p.q_len;
         mword[nt][e] = (2u << trow[nt][e]) - 1u;
       }
+    // (kFoldsV) O is in units of vref, a power of two not below any V scale of the segment so far
+    float vref = 0x1p-126f;
+    float qbias[NT][2];       // (kBiased) what the codes' bias adds to a score
     bool from_start = false;  // the segment holds its unit's first tile
     bool fresh = false;       // no reference for the segment's weights yet
     int unit = 0;
@@ -636,6 +640,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
             }
           }
         }
+        if constexpr (F::kBiased) F::template bias<NT>(qf, qs, lane, qbias);
         sscale = p.score_scale * (F::kHeadScales ? p.k_scale[h >> fp.kv_shift] : 1.f) * pow2f(-qexp);
         // a zero factor (uniform weights) as 2^-100: a finite score still weighs 1, and
         // an infinite one (a masked token's) 0
@@ -653,6 +658,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
           for (int mt = 0; mt < 8; ++mt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) oacc[nt][mt][e] = 0.f;
+          if (F::kFoldsV) vref = 0x1p-126f;
           m_neg[nt][0] = m_neg[nt][1] = 0.f;
           no_ref[nt][0] = no_ref[nt][1] = true;
           l_part[nt][0] = l_part[nt][1] = 0.f;
@@ -673,7 +679,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
         // keep their instructions apart; what a half that was not copied holds is masked below)
         float s[NT][H][4];
         const uint8_t *scales = side + st * F::kSideBytes;
-        fmt.template scores<NT>(stage, scales, qf, qs, s);
+        fmt.template scores<NT>(stage, scales, qf, qs, qbias, s);
         // ---------------- masks and the online softmax (log2 units)
         const bool part = valid != kAll;
         float f = sscale;  // log2 units of a score in s
@@ -781,6 +787,39 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
           }
           weights();
         }
+        // The V scales over vref join the weights (16 multiplies, not 128, for 32 tokens of 16 rows). One below
+        // 2^-4 of it would cost small weights their bits in f16, one that is not finite is no factor of f16:
+        // such a stage's products are scaled in fp32.
+        float vmul[H];
+        bool fold = true;
+        if constexpr (F::kFoldsV) {
+          float most = 0.f;
+#pragma unroll
+          for (int gi = 0; gi < H; ++gi) {
+            vmul[gi] = F::v_scale(scales, gi);
+            if (vmul[gi] < __int_as_float(0x7f800000)) most = fmaxf(most, vmul[gi]);
+          }
+          if (__builtin_expect(most > vref && vref < 0x1p126f, 0)) {  // (the same in every lane)
+            const float up = fminf(__uint_as_float((__float_as_uint(most) + 0x7FFFFFu) & 0x7F800000u), 0x1p126f);
+            const float alpha = vref / up;
+            vref = up;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oacc[nt][mt][e] *= alpha;
+          }
+          const float vinv = __uint_as_float(0x7F000000u - __float_as_uint(vref));
+#pragma unroll
+          for (int gi = 0; gi < H; ++gi) {
+            vmul[gi] *= vinv;
+            fold = fold && (vmul[gi] == 0.f || (vmul[gi] >= 0x1p-4f && vmul[gi] <= 1.f));
+          }
+        } else if constexpr (F::kBlockScales) {
+#pragma unroll
+          for (int gi = 0; gi < H; ++gi) vmul[gi] = F::v_scale(scales, gi);
+        }
         // P^T fragments: weights as f16, the row sums from the fp32 ones
         uint32_t pb[NT][H][2];
 #pragma unroll
@@ -789,7 +828,9 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
           l_part[nt][1] += sum[nt][1];
 #pragma unroll
           for (int k = 0; k < 2 * H; ++k)
-            pb[nt][k >> 1][k & 1] = movmatrix_trans(pack_f16(y[nt][0][k], y[nt][1][k]));
+            pb[nt][k >> 1][k & 1] = movmatrix_trans(
+                F::kFoldsV ? pack_f16(y[nt][0][k] * (fold ? vmul[k >> 1] : 1.f), y[nt][1][k] * (fold ? vmul[k >> 1] : 1.f))
+                           : pack_f16(y[nt][0][k], y[nt][1][k]));
         }
         // ---------------- O^T += V^T P^T
         // (a weight of 0 times NaN is no 0: a token that some query rows see and others do not
@@ -809,9 +850,9 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
           }
         }
         if constexpr (MOD >= 1 && F::kCareful) {
-          if (__builtin_expect(careful, 0)) fmt.template values_kept<NT>(stage + H * kGranBytes, scales, valid, s, y, oacc);
+          if (__builtin_expect(careful, 0)) fmt.template values_kept<NT>(stage + H * kGranBytes, vmul, valid, s, y, oacc);
         }
-        if (!careful) fmt.template values<NT>(stage + H * kGranBytes, scales, pb, oacc);
+        if (!careful) fmt.template values<NT>(stage + H * kGranBytes, vmul, fold, pb, oacc);
       }
       int seg_P = 0, seg_tiles = 0;
       if (fl & kLast) {
@@ -832,6 +873,14 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
       float *piece = nullptr;
       if (!whole) {
         float *stat = stat_all + (warp * 2 + (tail ? 0 : 1)) * 32;
+        if constexpr (F::kFoldsV) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) oacc[nt][mt][e] *= vref;
+        }
         piece = tail ? reinterpret_cast<float *>(ring)
                      : fp.o_head + ((int64_t)cta * W + warp) * G * kD;
         // the unit's first warp here names the group (a head alone is warp 0's)
@@ -889,7 +938,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
             const int g = nt * 8 + 2 * q4 + e;
             if (g < G) {
               const int64_t row = (int64_t)b * p.num_q_heads + h * G + g;
-              const float mul = l == 0.f ? 0.f : (F::kHeadScales ? p.v_scale[h >> fp.kv_shift] : 1.f) / l;  // no valid token: 0; NaN goes through
+              const float mul = l == 0.f ? 0.f : (F::kHeadScales ? p.v_scale[h >> fp.kv_shift] : F::kFoldsV ? vref : 1.f) / l;  // no valid token: 0; NaN goes through
               uint4 *dst = reinterpret_cast<uint4 *>(p.out + row * kD + 16 * r8);
 #pragma unroll
               for (int k = 0; k < 2; ++k)

@@ -119,24 +119,7 @@ __device__ __forceinline__ int pick_lane(const Two &sum, const Two &own, const T
   return past ? __ffs(past) - 1 : some ? 31 - __clz(some) : -1;
 }
 
-// Two floats at once (the packed adds of sm_100 and later), for two sums side by side.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pack(float a, float b) {
-  Pair r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-  return r;
-}
-__device__ __forceinline__ void unpack(Pair v, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ Pair sub2(Pair a, Pair b) {
-  Pair r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
+// Two such sums side by side.
 struct TwoPairs {
   Pair hi = 0, lo = 0;
   __device__ __forceinline__ void add(Pair x) {
@@ -518,11 +501,12 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 
 // CTAs of a cluster: as many as the SMs hold at once (four each) and as leave each a segment a warp.
 // 256 rows of 128000: 8 CTAs a row 59.3 us, 4 48.1, 2 42.6; 64 of 151937: 8 18.0, 4 18.2, 2 21.5
-// (with segments of 512).
+// (with segments of 512). The sums of a CTA's segments fit 40 KB.
 static int verify_ctas(const VerifyParams &p, int num_sms) {
   if (p.target_tokens) return 1;
   int c = kMaxCtas;
-  while (c > 1 && ((int64_t)p.batch * c > num_sms * 4 || (int64_t)p.vocab < (int64_t)c * kSeg * kWarps / 2)) c /= 2;
+  const int segs = (p.vocab + 3 + kSeg - 1) / kSeg;
+  while (c > 1 && segs / (c / 2) < 5000 && ((int64_t)p.batch * c > num_sms * 4 || (int64_t)p.vocab < (int64_t)c * kSeg * kWarps / 2)) c /= 2;
   return c;
 }
 

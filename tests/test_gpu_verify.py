@@ -135,6 +135,19 @@ def test_the_largest_vocabulary():
     assert e.value.status == da.DA_ERR_UNSUPPORTED
 
 
+def test_many_rows_of_the_largest_vocabulary():
+    """More rows than clusters of several CTAs are made for: a share's sums still fit."""
+    b, v = 700, 1 << 21
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    p = torch.rand(b, 1, v, generator=gen, device="cuda")
+    t = dict(target_probs=p, draft_tokens=torch.zeros(b, 0, dtype=torch.int32), uniforms=torch.rand(b, 1, generator=gen, device="cuda"))
+    dev = run(eng := engine(b, pages=16, cols=1), t)
+    assert eng.errors() == 0
+    for i in range(0, b, 70):
+        cum = p[i, 0].double().cumsum(0)
+        assert int(dev["tokens_out"][i, 0]) == int((cum <= t["uniforms"][i, 0].double() * cum[-1]).sum())
+
+
 @pytest.mark.parametrize("b", [1, 3, 300, 700])
 def test_batches(b):
     check(make(b, 4, 1000, ragged=True, near=0.5, seed=b))
