@@ -27,7 +27,7 @@ namespace {
 constexpr int kRows = 16;      // rows of a run, and of a block, that a warp has
 constexpr int kMinWarps = 4;   // of a CTA
 constexpr int kMaxWarps = 16;
-constexpr int kPerSm = 5;      // CTAs of kMinWarps an SM
+constexpr int kPerSm = 4;      // CTAs of kMinWarps an SM
 
 // The greater of two; NaN wins for integers (an e4m3 code can be NaN by itself).
 template <bool INT>
@@ -120,10 +120,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
   __shared__ float amax_all[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   begin_dependent();
-  // The two kinds alternate as long as there are both: keys and values wait for memory, queries stream.
-  const int both = 2 * min(kv_blocks, (int)gridDim.x - kv_blocks), b = (int)blockIdx.x;
-  const bool queries = b < both ? (b & 1) != 0 : 2 * kv_blocks < (int)gridDim.x;
-  const uint32_t block = b < both ? b >> 1 : b - both / 2;  // of its kind
+  // Keys first, which take longest, then values and queries in turn as long as there are both (the one waits
+  // for memory, the other streams).
+  const int half = kv_blocks / 2, q_blocks = (int)gridDim.x - kv_blocks, b = (int)blockIdx.x - half;
+  const int both = 2 * min(half, q_blocks);
+  const bool queries = b >= 0 && (b < both ? (b & 1) != 0 : half < q_blocks);
+  const uint32_t block = b < 0 ? b + half : (b < both ? b >> 1 : b - both / 2) + (queries ? 0 : half);  // of its kind
   if (queries) {
     const uint32_t item = block * warps + warp;
     const uint32_t t = item / (uint32_t)p.parts;
@@ -139,10 +141,11 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
   }
   const int n = p.kv_groups, shift = 31 - __clz(n), gw = n / kRows;  // a block's rows, a group's warps
   const int group = warp / gw, gwarp = warp - group * gw, HK = p.num_kv_heads;
-  const uint32_t item = block * (uint32_t)(warps / gw) + group, at = item / (uint32_t)(2 * HK);
+  const int side = (int)block >= half ? 1 : 0;  // 0: K
+  const uint32_t item = (block - side * half) * (uint32_t)(warps / gw) + group, at = item / (uint32_t)HK;
   const int64_t w0 = (int64_t)at * p.window;
   if (w0 >= p.num_tokens) return;
-  const int h = (int)(item - at * (2 * HK)) >> 1, side = (int)(item & 1);  // side 0: K
+  const int h = (int)(item - at * HK);
   uint32_t *written = written_all[group];
   float *amax = amax_all + group * gw;
   auto meet = [&]() {
@@ -162,21 +165,23 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
   const bool norm = NORM && side == 0 && p.k_weight != nullptr;
   uint4 *mine_at = staged_all + (warp * kRows + sub) * 16 + kl;  // this lane's part of every second row
 
-  auto block_of = [&](int64_t t) -> int64_t {  // -1: padding or outside the cache
-    const int64_t s = p.slot_map[t];
-    return s < 0 || s >= p.num_slots ? -1 : s >> shift;
-  };
+  auto block_of = [&](int64_t slot) -> int64_t { return slot < 0 || slot >= p.num_slots ? -1 : slot >> shift; };
   uint32_t err = 0;
-  uint32_t leads;  // tokens of the window whose run starts there
+  uint32_t leads, alone;  // tokens of the window whose run starts there, and those whose run is one token
   {
-    const int64_t t = w0 + lane;
-    const bool in = lane < p.window && t < p.num_tokens;
-    const int64_t b = in ? block_of(t) : -1;
-    if (in && b < 0 && p.slot_map[t] != -1) err |= DA_DEVERR_SLOT;
-    leads = __ballot_sync(0xffffffffu, b >= 0 && (t == 0 || block_of(t - 1) != b));
+    // lane i: the slot of token w0 + i; the last lane that of the token before (a window is at most 30 tokens)
+    const int64_t t = lane == 31 ? w0 - 1 : w0 + lane;
+    const bool in = t >= 0 && t < p.num_tokens && (lane <= p.window || lane == 31);
+    const int64_t slot = in ? p.slot_map[t] : -1, blk = block_of(slot);
+    if (lane < p.window && blk < 0 && slot != -1) err |= DA_DEVERR_SLOT;
+    const int64_t before = __shfl_sync(0xffffffffu, blk, (lane + 31) & 31), after = __shfl_sync(0xffffffffu, blk, (lane + 1) & 31);
+    leads = __ballot_sync(0xffffffffu, lane < p.window && blk >= 0 && before != blk);
+    alone = __ballot_sync(0xffffffffu, after != blk);
   }
   for (; leads != 0; leads &= leads - 1) {
-    const int64_t t0 = w0 + __ffs(leads) - 1, blk = block_of(t0);
+    const int first = __ffs(leads) - 1;
+    const int64_t t0 = w0 + first, blk = block_of(p.slot_map[t0]);
+    const int run_most = (alone >> first) & 1u ? 1 : n;  // (a decode step: the tokens after it are not looked at)
     const uint32_t per = (uint32_t)p.rows_per_page >> shift;  // blocks of a page
     const int64_t page = (blk >> 32) == 0 ? (int64_t)((uint32_t)blk / per) : blk / per, j = blk - page * per;
     const int64_t row0 = (page * HK + h) * p.rows_per_page + j * n;
@@ -189,8 +194,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
     const int in32 = gwarp * kRows & 31;  // where those are among 32
     for (int base = 0; base < n; base += 32) {
       const int64_t t = t0 + base + lane;
-      const bool in = base + lane < n && t < p.num_tokens;
-      const bool same = in && block_of(t) == blk;
+      const bool in = base + lane < run_most && t < p.num_tokens;
+      const int64_t slot = in ? p.slot_map[t] : -1;
+      const bool same = in && block_of(slot) == blk;
       const uint32_t run = __ballot_sync(0xffffffffu, same);
       const int m = run == 0xffffffffu ? 32 : __ffs(~run) - 1;  // up to the first of another block
       bool use = lane < m;
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
         err |= DA_DEVERR_POSITION;
         use = false;
       }
-      const int off = use ? (int)(p.slot_map[t] & (n - 1)) : -1;
+      const int off = use ? (int)(slot & (n - 1)) : -1;
       fresh = fresh || __any_sync(0xffffffffu, off == 0);
       const uint32_t used = __ballot_sync(0xffffffffu, use);
       const int o = __shfl_sync(0xffffffffu, off, in32 + lane % kRows);
@@ -222,17 +228,16 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
     uint32_t top2 = 0;
     const int pair0 = p.rope_adjacent ? 4 * kl : 8 * (second ? kl - r : kl);
     cp_async_wait_group<0>();  // (a lane reads what it copied itself)
-#pragma unroll 2
-    for (int i = 0; i < kRows / 2; ++i) {
-      if (((mine >> (2 * i)) & 3u) == 0) continue;
+    // (the next rows' angles are in flight while these are turned)
+    auto angles = [&](int i, float (&c)[8], float (&s)[8]) {
+      if (!turned || !((mine >> (2 * i + sub)) & 1u)) return;
+      if (p.rope_adjacent) load_turn<4>(p, t1 + 2 * i, pair0, c, s);
+      else load_turn<8>(p, t1 + 2 * i, pair0, c, s);
+    };
+    auto turn_rows = [&](int i, float (&c)[8], float (&s)[8]) {
       const bool on = (mine >> (2 * i + sub)) & 1u;
       uint4 x = on ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
       if (r > 0 || norm) {
-        float c[8], s[8];
-        if (on && turned) {
-          if (p.rope_adjacent) load_turn<4>(p, t1 + 2 * i, pair0, c, s);
-          else load_turn<8>(p, t1 + 2 * i, pair0, c, s);
-        }
         if (norm) {
           norm_key(p, x, kl, partner, turned, second, c, s);
         } else {
@@ -246,6 +251,25 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
       }
       top2 = max_abs2<INT>(max_abs2<INT>(top2, x.x), x.y);
       top2 = max_abs2<INT>(max_abs2<INT>(top2, x.z), x.w);
+    };
+    const int pairs = (32 - __clz(mine) + 1) / 2;  // of rows, up to the warp's last
+    if (side == 0) {
+      float c[8], s[8], c2[8], s2[8];
+      angles(0, c, s);
+#pragma unroll 1
+      for (int i = 0; i < pairs; i += 2) {
+        angles(i + 1, c2, s2);
+        turn_rows(i, c, s);
+        angles(i + 2, c, s);
+        turn_rows(i + 1, c2, s2);
+      }
+    } else {
+#pragma unroll 2
+      for (int i = 0; i < pairs; ++i) {
+        const uint4 x = (mine >> (2 * i + sub)) & 1u ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
+        top2 = max_abs2<INT>(max_abs2<INT>(top2, x.x), x.y);
+        top2 = max_abs2<INT>(max_abs2<INT>(top2, x.z), x.w);
+      }
     }
     float top = max_of<INT>(bf_lo(top2), bf_hi(top2));
 #pragma unroll
@@ -260,8 +284,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
     const bool finite = top < __int_as_float(0x7f800000);
     uint8_t *out = cache + row0 * 128 + kl * 8;
 #pragma unroll 2
-    for (int i = 0; i < kRows / 2; ++i) {
-      if (((mine >> (2 * i)) & 3u) == 0) continue;
+    for (int i = 0; i < pairs; ++i) {
       const int off = __shfl_sync(0xffffffffu, my_off, 2 * i + sub);
       if ((mine >> (2 * i + sub)) & 1u) *reinterpret_cast<uint2 *>(out + off * 128) = codes8<INT>(mine_at[32 * i], inv, finite);
     }
@@ -305,10 +328,10 @@ cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, c
   // wider ones, up to a block or the lanes of a warp: few groups then find no run.
   const int64_t one = (int64_t)p.num_tokens * p.num_kv_heads * 2 * gw;
   int window = 1;
-  while (window < 32 && window < p.kv_groups && one / window > (int64_t)num_sms * 16) window *= 2;
+  while (window < 30 && window < p.kv_groups && one / window > (int64_t)num_sms * 16) window = std::min(2 * window, 30);
   p.window = window;
-  const int64_t items = ((int64_t)p.num_tokens + window - 1) / window * p.num_kv_heads * 2;
-  const int64_t kv_blocks = (items + warps / gw - 1) / (warps / gw);
+  const int64_t items = ((int64_t)p.num_tokens + window - 1) / window * p.num_kv_heads;  // of K, and of V
+  const int64_t kv_blocks = 2 * ((items + warps / gw - 1) / (warps / gw));
   int64_t q_blocks = 0;
   p.parts = 1;
   if (p.q) {
