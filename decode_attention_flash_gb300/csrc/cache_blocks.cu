@@ -17,6 +17,13 @@
 // the scale grew the group reads the block's other rows, 16 a warp, and writes them rounded again. Runs are
 // found by the warps themselves: a group looks through a window of tokens for those whose predecessor is in
 // another block. Queries are the other blocks of the grid, as in cache_rows.cu.
+//
+// What bounds it. A decode step is latency: 64 tokens of 32 + 16 heads, blocks of 64: 4.7 us (queries alone
+// 2.5); four warps a group there, most with nothing to do, made two waves of blocks: 7.3. A prefill of 4096 such
+// tokens into blocks of 32 takes 27 us against a floor of 13.6: keys wait for their angles (5 of the 10 us that a
+// group takes, now loaded a step ahead), rows of one head and one block are little work for the slots,
+// positions and scales that have to be looked up first, and a scheduler has five warps at most. Measured and not
+// kept: rows in registers (32 us then); eight rows a warp (the same); more blocks an SM with spills (32 -> 38).
 #include <algorithm>
 
 #include "cache_rows.cuh"
@@ -24,7 +31,9 @@
 namespace da {
 namespace {
 
-constexpr int kRows = 16;      // rows of a run, and of a block, that a warp has
+constexpr int kRows = 16;      // rows of a run, and of a block, that a warp has (of few tokens up to kFewRows)
+constexpr int kFewRows = 64;
+constexpr int kLook = 30;      // tokens that a group looks at together for runs that start there
 constexpr int kMinWarps = 4;   // of a CTA
 constexpr int kMaxWarps = 16;
 constexpr int kPerSm = 4;      // CTAs of kMinWarps an SM
@@ -113,7 +122,7 @@ __device__ __forceinline__ bool positions_ok(const CacheRowParams &p, int64_t t)
 // kv_blocks CTAs have the keys and values, the others the queries (a warp a part of a token).
 // WARPS: of a CTA, at most.
 template <bool INT, bool NORM, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) append_blocks_kernel(const __grid_constant__ CacheRowParams p,
+__global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) append_blocks_kernel(const __grid_constant__ CacheRowParams p,
                                                                        const int kv_blocks) {
   extern __shared__ uint4 staged_all[];  // [warp][row][16]
   __shared__ uint32_t written_all[kMinWarps][256 / 32];  // rows of the block that the run writes, per group
@@ -139,7 +148,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
                               (int)((uint32_t)((part + 1) * nq) / (uint32_t)p.parts), p.num_q_heads, slot, c, s);
     return;
   }
-  const int n = p.kv_groups, shift = 31 - __clz(n), gw = n / kRows;  // a block's rows, a group's warps
+  const int n = p.kv_groups, shift = 31 - __clz(n), R = p.warp_rows, gw = n / R;  // a block's rows, a warp's, a group's warps
   const int group = warp / gw, gwarp = warp - group * gw, HK = p.num_kv_heads;
   const int side = (int)block >= half ? 1 : 0;  // 0: K
   const uint32_t item = (block - side * half) * (uint32_t)(warps / gw) + group, at = item / (uint32_t)HK;
@@ -163,24 +172,28 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
   const bool turned = kl < 2 * r, second = turned && !p.rope_adjacent && kl >= r;
   const int partner = lane - kl + (turned && !p.rope_adjacent ? (second ? kl - r : kl + r) : kl);
   const bool norm = NORM && side == 0 && p.k_weight != nullptr;
-  uint4 *mine_at = staged_all + (warp * kRows + sub) * 16 + kl;  // this lane's part of every second row
+  uint4 *mine_at = staged_all + (warp * R + sub) * 16 + kl;  // this lane's part of every second row
 
   auto block_of = [&](int64_t slot) -> int64_t { return slot < 0 || slot >= p.num_slots ? -1 : slot >> shift; };
   uint32_t err = 0;
-  uint32_t leads, alone;  // tokens of the window whose run starts there, and those whose run is one token
-  {
-    // lane i: the slot of token w0 + i; the last lane that of the token before (a window is at most 30 tokens)
-    const int64_t t = lane == 31 ? w0 - 1 : w0 + lane;
-    const bool in = t >= 0 && t < p.num_tokens && (lane <= p.window || lane == 31);
-    const int64_t slot = in ? p.slot_map[t] : -1, blk = block_of(slot);
-    if (lane < p.window && blk < 0 && slot != -1) err |= DA_DEVERR_SLOT;
-    const int64_t before = __shfl_sync(0xffffffffu, blk, (lane + 31) & 31), after = __shfl_sync(0xffffffffu, blk, (lane + 1) & 31);
-    leads = __ballot_sync(0xffffffffu, lane < p.window && blk >= 0 && before != blk);
-    alone = __ballot_sync(0xffffffffu, after != blk);
-  }
-  for (; leads != 0; leads &= leads - 1) {
+  const int64_t w1 = min(w0 + p.window, (int64_t)p.num_tokens);
+  uint32_t leads = 0, alone = 0;  // of kLook tokens, those whose run starts there, and those whose run is one token
+  int64_t from = w0 - kLook;
+  while (true) {
+    while (leads == 0 && (from += kLook) < w1) {
+      // lane i: the slot of token from + i; the last lane that of the token before
+      const int64_t t = lane == 31 ? from - 1 : from + lane;
+      const bool mine = lane < kLook && t < w1;
+      const int64_t slot = t >= 0 && t < p.num_tokens ? p.slot_map[t] : -1, blk = block_of(slot);
+      if (mine && blk < 0 && slot != -1) err |= DA_DEVERR_SLOT;
+      const int64_t before = __shfl_sync(0xffffffffu, blk, (lane + 31) & 31), after = __shfl_sync(0xffffffffu, blk, (lane + 1) & 31);
+      leads = __ballot_sync(0xffffffffu, mine && blk >= 0 && before != blk);
+      alone = __ballot_sync(0xffffffffu, after != blk);
+    }
+    if (leads == 0) break;
     const int first = __ffs(leads) - 1;
-    const int64_t t0 = w0 + first, blk = block_of(p.slot_map[t0]);
+    leads &= leads - 1;
+    const int64_t t0 = from + first, blk = block_of(p.slot_map[t0]);
     const int run_most = (alone >> first) & 1u ? 1 : n;  // (a decode step: the tokens after it are not looked at)
     const uint32_t per = (uint32_t)p.rows_per_page >> shift;  // blocks of a page
     const int64_t page = (blk >> 32) == 0 ? (int64_t)((uint32_t)blk / per) : blk / per, j = blk - page * per;
@@ -189,9 +202,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
     const float was = *scale;
     // ---- which tokens, and which rows they write
     bool fresh = false;
-    uint32_t mine = 0;  // of the warp's kRows tokens, those that are written
-    int my_off = 0;     // lane i < kRows: the row of the i-th
-    const int in32 = gwarp * kRows & 31;  // where those are among 32
+    uint64_t mine = 0;            // of the warp's R tokens, those that are written
+    int off_lo = 0, off_hi = 0;   // lane i: the rows of tokens i and 32 + i of those
+    const int in32 = gwarp * R & 31;  // where they begin among 32
     for (int base = 0; base < n; base += 32) {
       const int64_t t = t0 + base + lane;
       const bool in = base + lane < run_most && t < p.num_tokens;
@@ -207,10 +220,13 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
       const int off = use ? (int)(slot & (n - 1)) : -1;
       fresh = fresh || __any_sync(0xffffffffu, off == 0);
       const uint32_t used = __ballot_sync(0xffffffffu, use);
-      const int o = __shfl_sync(0xffffffffu, off, in32 + lane % kRows);
-      if (base / 32 == gwarp * kRows / 32) {
-        mine = (used >> in32) & ((1u << kRows) - 1u);
-        my_off = o;
+      const int o = __shfl_sync(0xffffffffu, off, (in32 + lane) & 31), at = base - (gwarp * R & ~31);
+      if (at == 0) {
+        mine |= (used >> in32) & (R < 32 ? 0xFFFFu : 0xFFFFFFFFu);
+        off_lo = o;
+      } else if (at == 32 && R == 64) {
+        mine |= (uint64_t)used << 32;
+        off_hi = o;
       }
       if (gwarp == 0) {  // (a run of one block: every row once)
         if (base == 0 && lane < 8) written[lane] = 0;
@@ -220,9 +236,10 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
       if (m < 32) break;
     }
     // ---- the warp's rows: read, normed, turned, in bf16
-    const int64_t t1 = t0 + gwarp * kRows + sub;
-#pragma unroll
-    for (int i = 0; i < kRows / 2; ++i)
+    const int64_t t1 = t0 + gwarp * R + sub;
+    const int pairs = (64 - __clzll((long long)mine) + 1) / 2;  // of rows, up to the warp's last
+#pragma unroll 8
+    for (int i = 0; i < pairs; ++i)
       if ((mine >> (2 * i + sub)) & 1u) cp_async_16(smem_u32(mine_at + 32 * i), src + (t1 + 2 * i) * stride + kl);
     cp_async_commit();
     uint32_t top2 = 0;
@@ -230,11 +247,12 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
     cp_async_wait_group<0>();  // (a lane reads what it copied itself)
     // (the next rows' angles are in flight while these are turned)
     auto angles = [&](int i, float (&c)[8], float (&s)[8]) {
-      if (!turned || !((mine >> (2 * i + sub)) & 1u)) return;
+      if (!turned || i >= pairs || !((mine >> (2 * i + sub)) & 1u)) return;
       if (p.rope_adjacent) load_turn<4>(p, t1 + 2 * i, pair0, c, s);
       else load_turn<8>(p, t1 + 2 * i, pair0, c, s);
     };
     auto turn_rows = [&](int i, float (&c)[8], float (&s)[8]) {
+      if (i >= pairs) return;
       const bool on = (mine >> (2 * i + sub)) & 1u;
       uint4 x = on ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
       if (r > 0 || norm) {
@@ -252,7 +270,6 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
       top2 = max_abs2<INT>(max_abs2<INT>(top2, x.x), x.y);
       top2 = max_abs2<INT>(max_abs2<INT>(top2, x.z), x.w);
     };
-    const int pairs = (32 - __clz(mine) + 1) / 2;  // of rows, up to the warp's last
     if (side == 0) {
       float c[8], s[8], c2[8], s2[8];
       angles(0, c, s);
@@ -285,17 +302,16 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
     uint8_t *out = cache + row0 * 128 + kl * 8;
 #pragma unroll 2
     for (int i = 0; i < pairs; ++i) {
-      const int off = __shfl_sync(0xffffffffu, my_off, 2 * i + sub);
+      const int off = __shfl_sync(0xffffffffu, 2 * i < 32 ? off_lo : off_hi, (2 * i + sub) & 31);
       if ((mine >> (2 * i + sub)) & 1u) *reinterpret_cast<uint2 *>(out + off * 128) = codes8<INT>(mine_at[32 * i], inv, finite);
     }
     // ---- rows that stay, rounded again
     if (!fresh && now > old) {
       const float ratio = old * inv;
-      const uint32_t keep = ~(written[gwarp * kRows >> 5] >> in32);
-      uint4 *rows = reinterpret_cast<uint4 *>(cache + (row0 + gwarp * kRows) * 128) + lane;
-#pragma unroll 1
-      for (int i = 0; i < kRows / 4; ++i)  // four rows of 8 lanes
-        if ((keep >> (4 * i + (lane >> 3))) & 1u) {
+      uint4 *rows = reinterpret_cast<uint4 *>(cache + (row0 + gwarp * R) * 128) + lane;
+#pragma unroll 4
+      for (int i = 0; i < R / 4; ++i)  // four rows of 8 lanes
+        if (!((written[(gwarp * R + 4 * i) >> 5] >> ((gwarp * R + 4 * i + (lane >> 3)) & 31)) & 1u)) {
           const uint4 a = rows[32 * i];
           rows[32 * i] = make_uint4(again4<INT>(a.x, ratio), again4<INT>(a.y, ratio), again4<INT>(a.z, ratio),
                                     again4<INT>(a.w, ratio));
@@ -309,26 +325,32 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 2) a
 
 }  // namespace
 
-static int blocks_smem(int warps) { return warps * kRows * 256; }
-
-cudaError_t append_blocks_prepare() {
-  const int most = blocks_smem(kMaxWarps);
+template <bool INT, bool NORM>
+static cudaError_t prepare_blocks() {
   const cudaFuncAttribute a = cudaFuncAttributeMaxDynamicSharedMemorySize;
-  cudaError_t e = cudaFuncSetAttribute(append_blocks_kernel<false, false, kMaxWarps>, a, most);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(append_blocks_kernel<false, true, kMaxWarps>, a, most);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(append_blocks_kernel<true, false, kMaxWarps>, a, most);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(append_blocks_kernel<true, true, kMaxWarps>, a, most);
-  return e;
+  const cudaError_t e = cudaFuncSetAttribute(append_blocks_kernel<INT, NORM, kMinWarps>, a, kMinWarps * kFewRows * 256);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(append_blocks_kernel<INT, NORM, kMaxWarps>, a, kMaxWarps * kRows * 256);
+}
+cudaError_t append_blocks_prepare() {
+  cudaError_t e = prepare_blocks<false, false>();
+  if (e == cudaSuccess) e = prepare_blocks<false, true>();
+  if (e == cudaSuccess) e = prepare_blocks<true, false>();
+  return e != cudaSuccess ? e : prepare_blocks<true, true>();
 }
 
 cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  const int gw = p.kv_groups / kRows, warps = std::max(kMinWarps, gw);
-  // Windows of one token while that makes few warps (a decode step: every token a run of its own), else
-  // wider ones, up to a block or the lanes of a warp: few groups then find no run.
+  // Few tokens (a decode step: every token, or every few, a run of its own) take a warp for up to 64 rows of
+  // a block, most of which have nothing to write: 64 tokens of 8 heads, blocks of 64: 7.3 -> 4.7 us.
+  const bool few = p.num_tokens <= 256;
+  p.warp_rows = std::min<int>(p.kv_groups, few ? kFewRows : kRows);
+  const int gw = p.kv_groups / p.warp_rows, warps = std::max(kMinWarps, gw);
+  // Windows of one token while that makes few warps, else wider ones, up to a block (less a sixteenth): few groups
+  // then find no run.
   const int64_t one = (int64_t)p.num_tokens * p.num_kv_heads * 2 * gw;
   int window = 1;
-  while (window < 30 && window < p.kv_groups && one / window > (int64_t)num_sms * 16) window = std::min(2 * window, 30);
+  while (!few && window < p.kv_groups * 15 / 16 && one / window > (int64_t)num_sms * 16)
+    window = window < 16 ? 2 * window : window < kLook ? kLook : 2 * window;
   p.window = window;
   const int64_t items = ((int64_t)p.num_tokens + window - 1) / window * p.num_kv_heads;  // of K, and of V
   const int64_t kv_blocks = 2 * ((items + warps / gw - 1) / (warps / gw));
@@ -343,7 +365,7 @@ cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, c
   const unsigned grid = (unsigned)(kv_blocks + q_blocks), threads = (unsigned)warps * 32;
   const bool norm = p.q_weight || p.k_weight;
   const int kv = (int)kv_blocks;
-  const size_t smem = (size_t)blocks_smem(warps);
+  const size_t smem = (size_t)warps * p.warp_rows * 256;
 #define DA_BLOCKS(I, N)                                                                                               \
   return warps == kMinWarps ? launch_dependent(append_blocks_kernel<I, N, kMinWarps>, grid, threads, smem, stream, p, kv) \
                             : launch_dependent(append_blocks_kernel<I, N, kMaxWarps>, grid, threads, smem, stream, p, kv)

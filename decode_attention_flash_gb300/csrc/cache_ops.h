@@ -59,6 +59,7 @@ struct CacheRowParams {
   float *k_block_scale, *v_block_scale;  // 8-bit blocks: [pages][HKV][rows_per_page / kv_groups]
   int32_t num_axes;            // 8-bit blocks: the distinct axes in pair_axis, and those
   uint8_t axes[64];
+  int32_t warp_rows;           // 8-bit blocks: rows of a block that a warp has (the launcher's)
   int32_t window;              // 8-bit blocks: tokens that one group of warps looks through (the launcher's)
   uint8_t pair_axis[64];
 };
