@@ -149,7 +149,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
   const int64_t pieces = info.rows_per_unit <= 8 ? 28 : 16;
   const int64_t most = longest > 0 ? std::max<int64_t>(pieces * sum / longest, 1) : pieces * info.num_units;
   *few_ctas = (int32_t)std::min<int64_t>(most, info.grid_x);
-  *few_tiles = (int32_t)std::min<int64_t>(most * 4 * stream_warps(p, info.rows_per_unit), INT32_MAX);
+  *few_tiles = (int32_t)std::min<int64_t>(most * 4 * 32 / info.kv_tile * stream_warps(p, info.rows_per_unit), INT32_MAX);
 }
 
 // Resident CTAs of the split kernel per SM, from its shared-memory footprint.
@@ -233,12 +233,14 @@ da_status plan_compute(const da_problem *p, int32_t num_sms, int32_t smem_per_sm
       // about 3 us (6 of 16 rows a unit), and costs the time by which the longest unit
       // passes an equal share: about 0.09 us a tile (8 heads of one 700-token row: 11.7
       // against 13.1 us; of a 3000-token row: 20 against 13; two heads of 16 rows in three
-      // rows of 1500 tokens: 17.6 against 21.9; of 3000: 25.1 against 22.3).
+      // rows of 1500 tokens: 17.6 against 21.9; of 3000: 25.1 against 22.3). Blocks of 8 bits likewise: 700 tokens
+      // 9.7 against 11.3, 1500 13.6 against 11.9; 16 rows a unit, 1500 tokens, 19.0 against 21.7, 3000 28.8
+      // against 24.0 (the limits are in tiles of 32 tokens).
       int64_t longest = 0;
       for (int64_t len : unit_len) longest = std::max(longest, ceil_div(len, tile));
       whole = num_splits_override > 0
                   ? num_splits_override == 1 && units <= 65535
-                  : seq_lens_host && units <= num_sms && longest - tiles / num_sms <= (rows <= 8 ? 32 : 48);
+                  : seq_lens_host && units <= num_sms && longest - tiles / num_sms <= (rows <= 8 ? 32 : 48) * 32 / tile;
       // (a unit's pieces, at most one a CTA, are merged in two levels of at most 32)
       ctas = whole ? units : std::min<int64_t>(ctas, 1024);
     }
