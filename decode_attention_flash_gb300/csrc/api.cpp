@@ -218,6 +218,7 @@ da_status run_gqa(da_ctx *ctx, const da_args *a, uint8_t *ws, cudaStream_t strea
   if ((a->kv_full_num_blks != nullptr) != (a->kv_full_idx != nullptr)) return DA_ERR_INVALID_ARG;
   if (a->kv_full_num_blks && !sparse) return DA_ERR_INVALID_ARG;
   if (fp8 && !token_scale && !int4 && (!a->k_scale || !a->v_scale)) return DA_ERR_INVALID_ARG;
+  if (da::is_block8(p) && (!aligned(a->k_scale, 4) || !aligned(a->v_scale, 4))) return DA_ERR_INVALID_ARG;
   if (token_scale && (!a->k_scale_shift || !a->v_scale_shift || !aligned(a->k_scale_shift, 16) ||
                       !aligned(a->v_scale_shift, 16)))
     return DA_ERR_INVALID_ARG;

@@ -245,6 +245,7 @@ da_status decode_attn_verify(da_ctx *ctx, const da_verify_args *a, void *workspa
   if (a->q_len < 1 || a->vocab < 1 || !a->tokens_out || !a->num_accepted) return DA_ERR_INVALID_ARG;
   if (greedy == (a->target_probs != nullptr) || (greedy && (a->draft_probs || a->uniforms))) return DA_ERR_INVALID_ARG;
   if (a->q_len > 1 && !a->draft_tokens) return DA_ERR_INVALID_ARG;
+  if (!aligned(a->target_probs, 4) || !aligned(a->draft_probs, 4) || !aligned(a->uniforms, 4)) return DA_ERR_INVALID_ARG;
   if (!greedy && (!a->uniforms || a->target_stride < a->vocab)) return DA_ERR_INVALID_ARG;
   if (a->draft_probs && a->q_len > 1 && a->draft_stride < a->vocab) return DA_ERR_INVALID_ARG;
   if ((a->seq_lens != nullptr) != (a->seq_lens_out != nullptr)) return DA_ERR_INVALID_ARG;

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
   extern __shared__ uint4 staged_all[];  // [warp][row][16]
   __shared__ uint32_t written_all[kMinWarps][256 / 32];  // rows of the block that the run writes, per group
   __shared__ float amax_all[kMaxWarps];
+  __shared__ uint32_t leads_all[kMinWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   begin_dependent();
   // Keys first, which take longest, then values and queries in turn as long as there are both (the one waits
@@ -189,6 +190,13 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
       const int64_t before = __shfl_sync(0xffffffffu, blk, (lane + 31) & 31), after = __shfl_sync(0xffffffffu, blk, (lane + 1) & 31);
       leads = __ballot_sync(0xffffffffu, mine && blk >= 0 && before != blk);
       alone = __ballot_sync(0xffffffffu, after != blk);
+      if (gw > 1) {  // (the group's warps meet below: what its first one saw holds for all)
+        if (gwarp == 0 && lane == 0) leads_all[group][0] = leads, leads_all[group][1] = alone;
+        meet();
+        leads = leads_all[group][0];
+        alone = leads_all[group][1];
+        meet();
+      }
     }
     if (leads == 0) break;
     const int first = __ffs(leads) - 1;

@@ -797,7 +797,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
 #pragma unroll
           for (int gi = 0; gi < H; ++gi) {
             vmul[gi] = F::v_scale(scales, gi);
-            if (vmul[gi] < __int_as_float(0x7f800000)) most = fmaxf(most, vmul[gi]);
+            if (fabsf(vmul[gi]) < __int_as_float(0x7f800000)) most = fmaxf(most, fabsf(vmul[gi]));
           }
           if (__builtin_expect(most > vref && vref < 0x1p126f, 0)) {  // (the same in every lane)
             const float up = fminf(__uint_as_float((__float_as_uint(most) + 0x7FFFFFu) & 0x7F800000u), 0x1p126f);

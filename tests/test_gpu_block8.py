@@ -200,6 +200,40 @@ def test_scales_of_any_size():
 
 
 @both
+@pytest.mark.parametrize("group", [4, 12])
+def test_scales_that_differ_and_negative_ones(kind, group):
+    """Value scales from 2^-40 to 2^6 of one another, some negative: a block far below the largest keeps its
+    weights' bits."""
+    t = B.make(lens=[700, 90], hq=group, hkv=1, kind=kind, block=16, page=64, seed=23)
+    gen = torch.Generator().manual_seed(24)
+    n = t["v_scale"].numel()
+    f = torch.exp2(torch.randint(-40, 7, (n,), generator=gen).float()) * (torch.randint(0, 2, (n,), generator=gen) * 2 - 1)
+    t["v_scale"] = (t["v_scale"].flatten() * f).reshape(t["v_scale"].shape)
+    check(t, hq=group, hkv=1, kind=kind, block=16, page=64)
+    t["v_scale"] = t["v_scale"].abs() * -1
+    check(t, hq=group, hkv=1, kind=kind, block=16, page=64)
+    t["v_scale"] *= 2.0 ** 100
+    check(t, hq=group, hkv=1, kind=kind, block=16, page=64)
+
+
+def test_misaligned_scales_are_refused():
+    t = B.make(lens=[20], hq=4, hkv=1, kind="e4m3", block=16, page=16, seed=25)
+    eng = engine(t, hq=4, hkv=1, kind="e4m3", block=16, page=16)
+    dev = {k: v.cuda() for k, v in t.items()}
+    out = torch.zeros_like(dev["q"])
+    for name in ("k_scale", "v_scale"):
+        a = da.make_args(dev, SCALE, out)
+        setattr(a, name, getattr(a, name) + 2)
+        with pytest.raises(da.DecodeAttnError) as e:
+            da.decode_attn_run(eng.ctx, a, eng.workspace)
+        assert e.value.status == da.DA_ERR_INVALID_ARG
+        setattr(a, name, None)
+        with pytest.raises(da.DecodeAttnError) as e:
+            da.decode_attn_run(eng.ctx, a, eng.workspace)
+        assert e.value.status == da.DA_ERR_INVALID_ARG
+
+
+@both
 def test_nan_reaches_the_rows_that_read_it(kind):
     t = B.make(lens=[90, 90], hq=4, hkv=2, kind=kind, block=16, page=16, seed=13)
     p = int(t["block_table"][1, 3])
