@@ -16,11 +16,14 @@
 // drafted token), sums its share of the vocabulary in segments of 256, and reads the other
 // CTAs' sums through the cluster; the one whose share holds the border finds its segment and looks at
 // that again, from L2.
-// Measured: 256 rows of 128000 with a draft's distribution each: 45 us (floor 38.7, 85 % of the copy
-// rate); 64 rows of 151937, no draft's: 19 us (floor 5.8; the clusters of eight leave SMs without a CTA, and
-// each row takes 7 us beside its stream); 4 rows of 32000: 9 us, latency (2.4 of them the pages' return:
-// a count of the rows, then lengths, then table entries). Segments of 512: 10.1, 15.9 and 45.0 us where these take
-// 8.5, 15.7 and 44.6 (captured, from L2); of 128: 8.2, 18.1 and 58.0. Eight segments' loads at once instead of four: spills.
+// Measured: 256 rows of 128000, four drafts each: 41 us. A row that keeps all its drafts reads no draft's
+// distribution, so 175 MB there, 4.2 TB/s: rows of one distribution and of two lie side by side, and an SM that
+// has more of the second ends later (CTAs of 256 threads, half as many: 43). 64 rows of 151937, no draft's: 14 us
+// from L2 (floor 5.8): 7 us a row has beside its stream (drafts, then their probabilities, then the sums' way
+// through the cluster and back). 4 rows of 32000: 8.9 us, latency, 2.4 of them the pages' return (a count of the
+// rows, then lengths, then table entries). Segments of 512 instead of 256: 9.5, 15.2 and 44.1 us where these took
+// 8.5, 15.3 and 43.4; of 128: 8.2, 15.5 and 51.2. A warp's reduction for each segment's sum alone, not four at
+// once: 16.9 and 45.
 #include <algorithm>
 
 #include "cache_ops.h"
@@ -29,12 +32,13 @@
 namespace da {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kPer = 8;           // tokens of a segment a lane
 constexpr int kTogether = 4;      // segments that a warp loads at once (of two rows half as many)
 constexpr int kSeg = 32 * kPer;
 constexpr int kMaxCtas = 8;       // of a cluster
+constexpr int kGive = 2;          // rows of a thread that takes pages back
 
 __device__ __forceinline__ uint32_t cta_rank() {
   uint32_t r;
@@ -304,7 +308,7 @@ __device__ __forceinline__ int drafts_of(const VerifyParams &p, int b) {
 
 // Rows' lengths without their rejected tokens, and the pages that only those had back on the stack: the
 // last row's first, each row's from its end. By the threads of one CTA.
-__device__ void release(const VerifyParams &p, int *scan) {
+__device__ __forceinline__ void release(const VerifyParams &p, int *scan) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t err = 0;
   int64_t top = p.num_free[0];
@@ -312,30 +316,33 @@ __device__ void release(const VerifyParams &p, int *scan) {
     err |= DA_DEVERR_NO_PAGES;
     top = top < 0 ? 0 : p.free_capacity;
   }
-  for (int base = 0; base < p.batch; base += kThreads) {
-    const int b = p.batch - 1 - base - (int)threadIdx.x;
-    int give = 0;
-    int64_t old_pages = 0, new_pages = 0;
-    const int32_t *table = nullptr;
-    if (b >= 0) {
-      const int n = drafts_of(p, b);
-      int64_t len = p.seq_lens[b];
-      int64_t less = n < 0 ? 0 : n - __ldcg(p.num_accepted + b);
+  // a thread has up to kGive rows that follow one another, whose loads are in flight together
+  const int per = min((p.batch + kThreads - 1) / kThreads, kGive);
+  for (int base = 0; base < p.batch; base += kThreads * per) {
+    int give = 0, before[kGive], after[kGive], row[kGive];  // pages of a row with and without its rejected tokens
+#pragma unroll
+    for (int j = 0; j < kGive; ++j) {
+      const int b = p.batch - 1 - base - (int)threadIdx.x * per - j;
+      row[j] = j < per && b >= 0 ? b : -1;
+      before[j] = after[j] = 0;
+      if (row[j] < 0) continue;
+      const int n = drafts_of(p, b), len = p.seq_lens[b];
+      int less = n < 0 ? 0 : n - __ldcg(p.num_accepted + b);
       if (len < less || len > p.capacity) {
         err |= DA_DEVERR_SEQ_LEN;
         less = 0;
-        old_pages = new_pages = 0;
       } else {
-        old_pages = (len + p.page_size - 1) / p.page_size;
-        new_pages = (len - less + p.page_size - 1) / p.page_size;
+        before[j] = (int)(((int64_t)len + p.page_size - 1) / p.page_size);
+        after[j] = (int)(((int64_t)len - less + p.page_size - 1) / p.page_size);
       }
-      p.seq_lens_out[b] = (int32_t)(len - less);
-      table = p.block_table + (int64_t)b * p.max_pages;
-      for (int64_t c = new_pages; c < old_pages; ++c) {
-        if ((uint32_t)table[c] < (uint32_t)p.num_pages) ++give;
+      p.seq_lens_out[b] = len - less;
+    }
+#pragma unroll
+    for (int j = 0; j < kGive; ++j)
+      for (int c = after[j]; c < before[j]; ++c) {
+        if ((uint32_t)p.block_table[(int64_t)row[j] * p.max_pages + c] < (uint32_t)p.num_pages) ++give;
         else err |= DA_DEVERR_PAGE_INDEX;
       }
-    }
     int sum = give;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -350,13 +357,15 @@ __device__ void release(const VerifyParams &p, int *scan) {
       all += scan[k];
     }
     int64_t at = top + sum - give;
-    for (int64_t c = old_pages - 1; c >= new_pages; --c) {
-      const int32_t id = table[c];
-      if ((uint32_t)id >= (uint32_t)p.num_pages) continue;
-      if (at < p.free_capacity) p.free_pages[at] = id;
-      else err |= DA_DEVERR_NO_PAGES;
-      ++at;
-    }
+#pragma unroll
+    for (int j = 0; j < kGive; ++j)
+      for (int c = before[j] - 1; c >= after[j]; --c) {
+        const int32_t id = p.block_table[(int64_t)row[j] * p.max_pages + c];
+        if ((uint32_t)id >= (uint32_t)p.num_pages) continue;
+        if (at < p.free_capacity) p.free_pages[at] = id;
+        else err |= DA_DEVERR_NO_PAGES;
+        ++at;
+      }
     top += all;
     __syncthreads();
   }
@@ -364,7 +373,7 @@ __device__ void release(const VerifyParams &p, int *scan) {
   if (err) atomicOr(p.err, err);
 }
 
-__global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_constant__ VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 8) verify_kernel(const __grid_constant__ VerifyParams p) {
   extern __shared__ float2 seg_sum[];  // of this CTA's segments
   __shared__ float2 s_total;
   __shared__ int s_accepted, s_rejected, s_token, s_home, s_last, s_scan[kWarps];
@@ -516,14 +525,13 @@ __global__ void __launch_bounds__(kThreads, 4) verify_kernel(const __grid_consta
 
 }  // namespace
 
-// CTAs of a cluster: as many as the SMs hold at once (four each) and as leave each a segment a warp.
-// 256 rows of 128000: 8 CTAs a row 59.3 us, 4 48.1, 2 42.6; 64 of 151937: 8 18.0, 4 18.2, 2 21.5
-// (with segments of 512). The sums of a CTA's segments fit 40 KB.
+// CTAs of a cluster: as many as the SMs hold at once (eight each) and as leave each half a segment a warp.
+// 256 rows of 128000: four CTAs a row 41 us, two 52, eight 44. The sums of a CTA's segments fit 40 KB.
 static int verify_ctas(const VerifyParams &p, int num_sms) {
   if (p.target_tokens) return 1;
   int c = kMaxCtas;
   const int segs = (p.vocab + 3 + kSeg - 1) / kSeg;
-  while (c > 1 && segs / (c / 2) < 5000 && ((int64_t)p.batch * c > num_sms * 4 || (int64_t)p.vocab < (int64_t)c * kSeg * kWarps / 2)) c /= 2;
+  while (c > 1 && segs / (c / 2) < 5000 && ((int64_t)p.batch * c > num_sms * 8 || (int64_t)p.vocab < (int64_t)c * kSeg * kWarps / 2)) c /= 2;
   return c;
 }
 
