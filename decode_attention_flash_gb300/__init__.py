@@ -484,8 +484,12 @@ def decode_attn_append(ctx, args: AppendArgs, workspace: torch.Tensor, stream=No
 
 def decode_attn_append_normed(ctx, args: AppendArgs, norm: NormArgs, workspace: torch.Tensor, stream=None):
     """``decode_attn_append`` with queries and keys normed head by head first (one kernel)."""
-    fn = load().decode_attn_append_normed
-    _enqueue(lambda c, a, *rest: fn(c, a, norm, *rest), "decode_attn_append_normed", ctx, args, workspace, stream)
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        _ptr(workspace)  # raises
+    stream = torch._C._cuda_getCurrentRawStream(workspace.get_device()) if stream is None else _stream(stream)
+    status = load().decode_attn_append_normed(ctx, args, norm, workspace.data_ptr(), workspace.nbytes, stream)
+    if status != DA_OK:
+        raise DecodeAttnError(status, "decode_attn_append_normed")
 
 
 def decode_attn_gather(ctx, args: GatherArgs, workspace: torch.Tensor, stream=None):

@@ -125,7 +125,6 @@ da_status append(da_ctx *ctx, const da_append_args *a, const da_norm_args *norm,
       if (ax >= a->rope_axes) return DA_ERR_INVALID_ARG;
       c.pair_axis[i] = (uint8_t)ax;
       if (ax != c.pair_axis[i / group * group]) c.rope_whole = 0;
-      if (std::memchr(c.axes, ax, (size_t)c.num_axes) == nullptr) c.axes[c.num_axes++] = (uint8_t)ax;
     }
   }
   c.q = reinterpret_cast<const __nv_bfloat16 *>(a->q);

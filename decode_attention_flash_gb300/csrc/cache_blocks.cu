@@ -25,6 +25,7 @@
 // positions and scales that have to be looked up first, and a scheduler has five warps at most. Measured and not
 // kept: rows in registers (32 us then); eight rows a warp (the same); more blocks an SM with spills (32 -> 38).
 #include <algorithm>
+#include <cstring>
 
 #include "cache_rows.cuh"
 
@@ -110,7 +111,7 @@ __device__ __forceinline__ uint32_t again4(uint32_t w, float ratio) {
 }
 
 // Whether every position that turns a pair of token t is in the table.
-__device__ __forceinline__ bool positions_ok(const CacheRowParams &p, int64_t t) {
+__device__ __forceinline__ bool positions_ok(const BlockRowParams &p, int64_t t) {
   bool ok = true;
   for (int i = 0; i < p.num_axes; ++i) {
     const int pos = p.positions[(int64_t)p.axes[i] * p.position_stride + t];
@@ -122,7 +123,7 @@ __device__ __forceinline__ bool positions_ok(const CacheRowParams &p, int64_t t)
 // kv_blocks CTAs have the keys and values, the others the queries (a warp a part of a token).
 // WARPS: of a CTA, at most.
 template <bool INT, bool NORM, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) append_blocks_kernel(const __grid_constant__ CacheRowParams p,
+__global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) append_blocks_kernel(const __grid_constant__ BlockRowParams p,
                                                                        const int kv_blocks) {
   extern __shared__ uint4 staged_all[];  // [warp][row][16]
   __shared__ uint32_t written_all[kMinWarps][256 / 32];  // rows of the block that the run writes, per group
@@ -346,8 +347,15 @@ cudaError_t append_blocks_prepare() {
   return e != cudaSuccess ? e : prepare_blocks<true, true>();
 }
 
-cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream) {
-  if (p.num_tokens == 0) return cudaSuccess;
+cudaError_t launch_append_blocks(const CacheRowParams &rows, bool integers, int num_sms, cudaStream_t stream) {
+  if (rows.num_tokens == 0) return cudaSuccess;
+  BlockRowParams p;
+  std::memset(&p, 0, sizeof p);
+  static_cast<CacheRowParams &>(p) = rows;
+  for (int i = 0; i < p.rope_pairs; ++i) {
+    const int a = p.pair_axis[i];
+    if (std::memchr(p.axes, a, (size_t)p.num_axes) == nullptr) p.axes[p.num_axes++] = (uint8_t)a;
+  }
   // Few tokens (a decode step: every token, or every few, a run of its own) take a warp for up to 64 rows of
   // a block, most of which have nothing to write: 64 tokens of 8 heads, blocks of 64: 7.3 -> 4.7 us.
   const bool few = p.num_tokens <= 256;

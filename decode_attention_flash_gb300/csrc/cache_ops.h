@@ -57,11 +57,14 @@ struct CacheRowParams {
   const float *q_weight, *k_weight;  // the norm's weights of a head (latent: k_weight of 512); null: no norm
   float norm_eps;
   float *k_block_scale, *v_block_scale;  // 8-bit blocks: [pages][HKV][rows_per_page / kv_groups]
-  int32_t num_axes;            // 8-bit blocks: the distinct axes in pair_axis, and those
-  uint8_t axes[64];
-  int32_t warp_rows;           // 8-bit blocks: rows of a block that a warp has (the launcher's)
-  int32_t window;              // 8-bit blocks: tokens that one group of warps looks through (the launcher's)
   uint8_t pair_axis[64];
+};
+// The append of 8-bit blocks: the launcher's choices.
+struct BlockRowParams : CacheRowParams {
+  int32_t warp_rows;           // rows of a block that a warp has
+  int32_t window;              // tokens that one group of warps looks through
+  int32_t num_axes;            // the distinct axes in pair_axis, and those
+  uint8_t axes[64];
 };
 
 // decode_attn_build_tables, tables.cu.
@@ -142,7 +145,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
 
 cudaError_t launch_append(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t append_blocks_prepare();  // sets shared-memory attributes
-cudaError_t launch_append_blocks(CacheRowParams p, bool integers, int num_sms, cudaStream_t stream);
+cudaError_t launch_append_blocks(const CacheRowParams &p, bool integers, int num_sms, cudaStream_t stream);
 cudaError_t launch_gather(CacheRowParams p, int kind, int num_sms, cudaStream_t stream);
 cudaError_t launch_verify(const VerifyParams &p, int num_sms, cudaStream_t stream);
 cudaError_t launch_tables(const TableParams &p, int num_sms, cudaStream_t stream);
