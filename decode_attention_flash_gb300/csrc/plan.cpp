@@ -134,7 +134,8 @@ int64_t stream_head_offset(const da_plan_info &i) {
 // about 45 GB/s. So a call that fewer CTAs would serve with at most four tiles a warp
 // takes no more than leave its longest unit 28 pieces, or 16 of more than 8 rows: one row
 // of 16384 tokens, one head: 17.9 -> 16.3 us; two heads of 16 rows: 31.4 -> 22.7 (28
-// pieces: 28.1). The longest unit's share is that of the planned lengths, or the mean.
+// pieces: 28.1; 8-bit blocks 12: one row of 6000 tokens, 8 heads of 16 rows, 27.5 -> 25.2).
+// The longest unit's share is that of the planned lengths, or the mean.
 void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *seq_lens_host, int32_t num_splits_override,
              int32_t *few_tiles, int32_t *few_ctas) {
   *few_tiles = *few_ctas = 0;
@@ -146,7 +147,7 @@ void stream_few(const da_problem &p, const da_plan_info &info, const int32_t *se
     sum += t * (info.num_units / p.batch);
     longest = std::max(longest, t);
   }
-  const int64_t pieces = info.rows_per_unit <= 8 ? 28 : 16;
+  const int64_t pieces = info.rows_per_unit <= 8 ? 28 : is_block8(p) ? 12 : 16;
   const int64_t most = longest > 0 ? std::max<int64_t>(pieces * sum / longest, 1) : pieces * info.num_units;
   *few_ctas = (int32_t)std::min<int64_t>(most, info.grid_x);
   *few_tiles = (int32_t)std::min<int64_t>(most * 4 * 32 / info.kv_tile * stream_warps(p, info.rows_per_unit), INT32_MAX);
