@@ -363,10 +363,13 @@ cudaError_t launch_append_blocks(const CacheRowParams &rows, bool integers, int 
   p.warp_rows = std::min<int>(p.kv_groups, few ? kFewRows : kRows);
   const int gw = p.kv_groups / p.warp_rows, warps = std::max(kMinWarps, gw);
   // Windows of one token while that makes few warps, else wider ones, up to a block (less a sixteenth): few groups
-  // then find no run.
+  // then find no run. Up to 32 warps an SM, twice what it holds: narrower windows seldom have the ends of two
+  // runs, which one group would take in turn (16: 300 tokens into blocks of 256 25.7 us, now 17.2, 2000 into
+  // blocks of 128 23.3 and 17.6; 300 and 2000 into blocks of 32 10.2 and 17.6, now 10.5 and 18.5; 64: 4096 into
+  // blocks of 32 27.6 -> 28.5).
   const int64_t one = (int64_t)p.num_tokens * p.num_kv_heads * 2 * gw;
   int window = 1;
-  while (!few && window < p.kv_groups * 15 / 16 && one / window > (int64_t)num_sms * 16)
+  while (!few && window < p.kv_groups * 15 / 16 && one / window > (int64_t)num_sms * 32)
     window = window < 16 ? 2 * window : window < kLook ? kLook : 2 * window;
   p.window = window;
   const int64_t items = ((int64_t)p.num_tokens + window - 1) / window * p.num_kv_heads;  // of K, and of V
