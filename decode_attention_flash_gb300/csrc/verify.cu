@@ -6,9 +6,15 @@
 // as the target's own), else from p_n. A draw takes the first token whose running sum of weights passes
 // r times their sum. Running sums meet borders, so they are kept far beyond fp32, as unevaluated pairs of
 // floats: the rounding error of every difference, sum and product is computed exactly (Knuth's two-sum,
-// the product's by a fused multiply) and carried along, which leaves 2^-44 or so of the sum. (Doubles
-// instead: 16 cycles of an SM for a warp's one addition; 82.7, 33.0 and 16.0 us for the three below.)
-// Two such sums side by side take the packed adds.
+// the product's by a fused multiply) and carried along in the second float. That is an fp32 sum itself: weights
+// that each round away beside a great one all land in it, and after hundreds of additions it would be off by
+// 2^-36 of the sum. So it passes what it can on to the first float after the few additions of a segment, and in
+// a lane's sum over its segments a third float has its rounding errors. With u = 2^-24 (a float's rounding) what is
+// left is at most 100 u^2 of a segment's sum (ten additions, the second float at most ten u by then), 3 u^2 for each
+// addition of two such sums, about fifteen in a row, and 40 u^2 inside the segment that is drawn from: 2^-40 of the
+// sum, however the weights lie; of weights that are all alike 2^-46. (Doubles instead, for every token: 16 cycles of
+// an SM for a warp's one addition; 82.7, 33.0 and 16.0 us for the three below; for the sums of segments alone 44.1,
+// 15.2 and 9.9.) Two such sums side by side take the packed adds.
 // A drafted token's product is compared exactly, in 64 bits.
 //
 // What bounds it. One row of p and one of q a batch row, read once: HBM, and latency for few rows.
@@ -61,9 +67,19 @@ struct Two {
     lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(s, b)), __fsub_rn(x, b)));
     hi = s;
   }
-  __device__ __forceinline__ void add(const Two &x) {
+  __device__ __forceinline__ void join(const Two &x) {  // (lo grows by a rounding of the sum)
     add(x.hi);
     lo = __fadd_rn(lo, x.lo);
+  }
+  // lo to at most half a step of hi again (it is less than hi: both are of sums without a negative term)
+  __device__ __forceinline__ void tidy() {
+    const float s = __fadd_rn(hi, lo);
+    lo = __fsub_rn(lo, __fsub_rn(s, hi));
+    hi = s;
+  }
+  __device__ __forceinline__ void add(const Two &x) {
+    join(x);
+    tidy();
   }
   // max(p - q, 0), with its rounding error; NaN counts as 0
   __device__ __forceinline__ void add_rest(float p, float q) {
@@ -110,16 +126,20 @@ __device__ __forceinline__ Two swap(const Two &v, int bit) {
   r.lo = __shfl_xor_sync(0xffffffffu, v.lo, bit);
   return r;
 }
+// 0 in the first `o` lanes: adding that changes nothing (a branch around the additions instead: 0.6 us)
+__device__ __forceinline__ Two shuffle_up(const Two &v, int o, int lane) {
+  Two r;
+  r.hi = __shfl_up_sync(0xffffffffu, v.hi, o);
+  r.lo = __shfl_up_sync(0xffffffffu, v.lo, o);
+  r.hi = lane >= o ? r.hi : 0.f;
+  r.lo = lane >= o ? r.lo : 0.f;
+  return r;
+}
 // Sums up to this lane, itself included, of the first LANES lanes.
 template <int LANES>
 __device__ __forceinline__ Two inclusive(Two v, int lane) {
 #pragma unroll
-  for (int o = 1; o < LANES; o <<= 1) {
-    Two u;
-    u.hi = __shfl_up_sync(0xffffffffu, v.hi, o);
-    u.lo = __shfl_up_sync(0xffffffffu, v.lo, o);
-    if (lane >= o) v.add(u);
-  }
+  for (int o = 1; o < LANES; o <<= 1) v.add(shuffle_up(v, o, lane));
   return v;
 }
 // The first lane whose sum passes `border`, else the last with a weight; -1: none has one.
@@ -150,7 +170,7 @@ struct TwoPairs {
     Two a, b;
     unpack(hi, a.hi, b.hi);
     unpack(lo, a.lo, b.lo);
-    a.add(b);
+    a.join(b);
     return a;
   }
 };
@@ -228,8 +248,8 @@ __device__ __forceinline__ void sum_segments(const Rows &w, int g0, int ng, int 
       const Two u = swap(odd ? s[0] : s[2], 1), v = swap(odd ? s[1] : s[3], 1);
       s[0] = odd ? s[2] : s[0];
       s[1] = odd ? s[3] : s[1];
-      s[0].add(u);
-      s[1].add(v);
+      s[0].join(u);
+      s[1].join(v);
       mine = 2 * (lane & 1);
     }
     constexpr int kHalve = kAt / 2;  // the lane bit that parts the last two sums
@@ -237,11 +257,12 @@ __device__ __forceinline__ void sum_segments(const Rows &w, int g0, int ng, int 
       const bool up = lane & kHalve;
       const Two u = swap(up ? s[0] : s[1], kHalve);
       s[0] = up ? s[1] : s[0];
-      s[0].add(u);
+      s[0].join(u);
       mine += up ? 1 : 0;
     }
 #pragma unroll
-    for (int o = kAt; o < 32; o <<= 1) s[0].add(swap(s[0], o));
+    for (int o = kAt; o < 32; o <<= 1) s[0].join(swap(s[0], o));
+    s[0].tidy();
     if (lane < kAt && g + mine * kWarps < ng) sums[g + mine * kWarps] = make_float2(s[0].hi, s[0].lo);
   }
 }
@@ -274,12 +295,7 @@ __device__ __forceinline__ int pick_token(const Rows &w, int seg, Two border, in
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      Two u;
-      u.hi = __shfl_up_sync(0xffffffffu, sum[g].hi, o);
-      u.lo = __shfl_up_sync(0xffffffffu, sum[g].lo, o);
-      if (lane >= o) sum[g].add(u);
-    }
+    for (int g = 0; g < kGroups; ++g) sum[g].add(shuffle_up(sum[g], o, lane));
   // the group: the last with a weight whose tokens begin at or below the border
   int token = -1;
 #pragma unroll
@@ -447,11 +463,15 @@ __global__ void __launch_bounds__(kThreads, 8) verify_kernel(const __grid_consta
       const int per = (ng + 31) / 32, s0 = min(lane * per, ng), s1 = min(s0 + per, ng);
       Two own, sum;
       if (warp == 0) {
+        Two low;  // own's second float, kept as a sum of its own
         for (int g = s0; g < s1; ++g) {
-          Two x;
-          x.hi = seg_sum[g].x, x.lo = seg_sum[g].y;
-          own.add(x);
+          own.lo = 0.f;
+          own.add(seg_sum[g].x);
+          low.add(own.lo);
+          low.add(seg_sum[g].y);
         }
+        own.lo = __fadd_rn(low.hi, low.lo);
+        own.tidy();
         sum = inclusive<32>(own, lane);
         if (lane == 31) s_total = make_float2(sum.hi, sum.lo);
       }
@@ -466,20 +486,28 @@ __global__ void __launch_bounds__(kThreads, 8) verify_kernel(const __grid_consta
         const int home = some ? pick_lane(upto, part, border) : -1;
         if (home == rank) {
           const Two rest = border.minus(shuffle(upto.minus(part), home));
-          const int l = pick_lane(sum, own, rest);
-          Two at = sum.minus(own), before;
+          const int l = pick_lane(sum, own, rest), a1 = min(l * per + per, ng);
+          Two at = shuffle(sum.minus(own), l), before;
           int seg = -1;
-          for (int g = s0; g < s1; ++g) {
+          for (int a = l * per; a < a1; a += 32) {  // that lane's segments, a lane each
             Two x;
-            x.hi = seg_sum[g].x, x.lo = seg_sum[g].y;
-            if (x.positive() && (seg < 0 || !at.above(rest))) {
-              seg = g;
-              before = at;
+            if (a + lane < a1) x.hi = seg_sum[a + lane].x, x.lo = seg_sum[a + lane].y;
+            Two upto_it = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              if (o >= per) break;
+              upto_it.add(shuffle_up(upto_it, o, lane));
             }
-            at.add(x);
+            upto_it.add(at);
+            const int j = pick_lane(upto_it, x, rest);
+            if (j >= 0) {
+              seg = a + j;
+              before = shuffle(upto_it.minus(x), j);
+              if (shuffle(upto_it, j).above(rest)) break;
+            }
+            at = shuffle(upto_it, 31);
           }
-          seg = __shfl_sync(0xffffffffu, seg, l);
-          const int token = pick_token(w, g0 + seg, rest.minus(shuffle(before, l)), lane);
+          const int token = pick_token(w, g0 + seg, rest.minus(before), lane);
           if (lane == 0) s_token = token;
         }
         if (lane == 0) s_home = home;
