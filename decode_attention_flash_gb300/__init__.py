@@ -113,7 +113,7 @@ class VerifyArgs(ctypes.Structure):
         "target_probs", "draft_probs", "target_tokens", "draft_tokens", "num_draft", "uniforms", "tokens_out",
         "num_accepted", "seq_lens", "seq_lens_out", "block_table", "free_pages", "num_free", "num_free_out")] + [
         ("target_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)] + [
-        (n, ctypes.c_int32) for n in ("q_len", "vocab", "free_capacity")]
+        (n, ctypes.c_int32) for n in ("q_len", "vocab", "free_capacity")] + [("seq_lens_before", ctypes.c_void_p)]
 
 
 class PlanInfo(ctypes.Structure):
@@ -450,7 +450,7 @@ def make_verify_args(tensors: dict, vocab: int = 0) -> VerifyArgs:
     else:
         a.vocab = int(vocab) or 1 << 21
     for name, n in (("target_tokens", b * q), ("draft_tokens", b * (q - 1)), ("num_draft", b), ("tokens_out", b * q),
-                    ("num_accepted", b), ("seq_lens", b), ("seq_lens_out", b), ("block_table", None),
+                    ("num_accepted", b), ("seq_lens", b), ("seq_lens_before", b), ("seq_lens_out", b), ("block_table", None),
                     ("free_pages", None), ("num_free", 1), ("num_free_out", 1)):
         setattr(a, name, _typed_ptr(tensors, name, torch.int32, n))
     a.uniforms = _typed_ptr(tensors, "uniforms", torch.float32, b * q)

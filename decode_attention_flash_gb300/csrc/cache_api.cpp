@@ -248,6 +248,7 @@ da_status decode_attn_verify(da_ctx *ctx, const da_verify_args *a, void *workspa
   if (!greedy && (!a->uniforms || a->target_stride < a->vocab)) return DA_ERR_INVALID_ARG;
   if (a->draft_probs && a->q_len > 1 && a->draft_stride < a->vocab) return DA_ERR_INVALID_ARG;
   if ((a->seq_lens != nullptr) != (a->seq_lens_out != nullptr)) return DA_ERR_INVALID_ARG;
+  if (a->seq_lens_before && !a->seq_lens) return DA_ERR_INVALID_ARG;
   const bool gives = a->free_pages != nullptr;
   if (gives && (!paged || !a->seq_lens || !a->block_table || !a->num_free || !a->num_free_out || a->free_capacity < 0))
     return DA_ERR_INVALID_ARG;
@@ -269,6 +270,7 @@ da_status decode_attn_verify(da_ctx *ctx, const da_verify_args *a, void *workspa
   v.tokens_out = a->tokens_out;
   v.num_accepted = a->num_accepted;
   v.seq_lens = a->seq_lens;
+  v.seq_lens_before = a->seq_lens_before;
   v.seq_lens_out = a->seq_lens_out;
   v.block_table = a->block_table;
   v.free_pages = a->free_pages;

@@ -90,6 +90,7 @@ struct VerifyParams {
   const float *uniforms;               // [B][Q]
   int32_t *tokens_out, *num_accepted;
   const int32_t *seq_lens;             // optional
+  const int32_t *seq_lens_before;      // optional: those before the step's tokens
   int32_t *seq_lens_out;
   const int32_t *block_table;          // with free_pages
   int32_t *free_pages;                 // optional

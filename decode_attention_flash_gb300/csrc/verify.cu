@@ -317,9 +317,25 @@ __device__ __forceinline__ int pick_token(const Rows &w, int seg, Two border, in
   return token;
 }
 
+// A row's drafted tokens, -1 if it takes no part: its caller says so, or it got fewer tokens in this step than its
+// known one and the drafts (those that it got stood where other query tokens' masks apply, or nowhere). That test
+// gives the same again after the row's length has been written over either of the two that it compares.
 __device__ __forceinline__ int drafts_of(const VerifyParams &p, int b) {
-  const int n = p.num_draft ? p.num_draft[b] : p.q_len - 1;
-  return min(n, p.q_len - 1);
+  const int n = min(p.num_draft ? p.num_draft[b] : p.q_len - 1, p.q_len - 1);
+  if (!p.seq_lens_before) return n;
+  const int len = p.seq_lens[b], before = p.seq_lens_before[b];
+  return before < 0 || before > len || len - before <= n ? -1 : n;
+}
+// A row's length after the step, and its length `len` with the step's tokens in; n and kept of its drafts. A row that
+// takes no part because it got fewer tokens goes back to what it had. False: a length out of range, left as it is.
+__device__ __forceinline__ bool length_after(const VerifyParams &p, int b, int n, int kept, int &len, int &after) {
+  int before = len = p.seq_lens[b];
+  const bool asked = !p.num_draft || p.num_draft[b] >= 0;
+  if (p.seq_lens_before && asked) before = p.seq_lens_before[b];
+  after = n >= 0 ? len - (n - kept) : before;
+  const bool ok = before >= 0 && before <= len && after >= 0 && len <= p.capacity;
+  if (!ok) after = len;
+  return ok;
 }
 
 // Rows' lengths without their rejected tokens, and the pages that only those had back on the stack: the
@@ -342,16 +358,14 @@ __device__ __forceinline__ void release(const VerifyParams &p, int *scan) {
       row[j] = j < per && b >= 0 ? b : -1;
       before[j] = after[j] = 0;
       if (row[j] < 0) continue;
-      const int n = drafts_of(p, b), len = p.seq_lens[b];
-      int less = n < 0 ? 0 : n - __ldcg(p.num_accepted + b);
-      if (len < less || len > p.capacity) {
+      int len, left;
+      if (!length_after(p, b, drafts_of(p, b), __ldcg(p.num_accepted + b), len, left)) {
         err |= DA_DEVERR_SEQ_LEN;
-        less = 0;
       } else {
         before[j] = (int)(((int64_t)len + p.page_size - 1) / p.page_size);
-        after[j] = (int)(((int64_t)len - less + p.page_size - 1) / p.page_size);
+        after[j] = (int)(((int64_t)left + p.page_size - 1) / p.page_size);
       }
-      p.seq_lens_out[b] = len - less;
+      p.seq_lens_out[b] = left;
     }
 #pragma unroll
     for (int j = 0; j < kGive; ++j)
@@ -533,11 +547,9 @@ __global__ void __launch_bounds__(kThreads, 8) verify_kernel(const __grid_consta
     if (threadIdx.x == 0) {
       p.num_accepted[b] = a;
       if (p.seq_lens && !p.free_pages) {
-        int len = p.seq_lens[b];
-        const int less = n < 0 ? 0 : n - a;
-        if (len < less || len > p.capacity) err |= DA_DEVERR_SEQ_LEN;
-        else len -= less;
-        p.seq_lens_out[b] = len;
+        int len, left;
+        if (!length_after(p, b, n, a, len, left)) err |= DA_DEVERR_SEQ_LEN;
+        p.seq_lens_out[b] = left;
       }
     }
     if (err && warp == 0) atomicOr(p.err, err);

@@ -602,13 +602,19 @@ da_status decode_attn_gather(da_ctx *ctx, const da_gather_args *args, void *work
  *                  of the token drawn after them. NULL with target_tokens
  *   tokens_out     int32 [B][Q]: the accepted tokens, the one after them, then -1
  *   num_accepted   int32 [B]
- *   seq_lens       int32 [B], lengths with the row's num_draft tokens in (NULL: no lengths)
- *   seq_lens_out   int32 [B], may be seq_lens: less the tokens that were not accepted
+ *   seq_lens       int32 [B], lengths with the row's known token and its num_draft drafted ones in (NULL: no
+ *                  lengths). decode_attn_build_tables leaves a row out that the pool has no pages for, and cuts its
+ *                  tokens short at its capacity or slot_map's end: give seq_lens_before where that may happen
+ *   seq_lens_out   int32 [B], may be seq_lens or seq_lens_before: less the tokens that were not accepted
  *   block_table    int32 [B][max_pages_per_seq], with free_pages: the pages that only those had are put
  *   free_pages     back on the stack int32 [free_capacity] of num_free[0] entries (as
  *                  decode_attn_build_tables takes them): the last row's first, each row's from its end.
  *                  NULL: no pages are given back. The table keeps its entries
  *   num_free, num_free_out  int32 [1], may be the same; NULL without free_pages
+ *   seq_lens_before  int32 [B], optional, with seq_lens: the lengths that the rows had before the step (what
+ *                  decode_attn_build_tables took, where its seq_lens_out is another tensor). A row whose length has
+ *                  not grown by its known token and all its drafts takes no part: it accepts 0, its tokens are -1,
+ *                  its length is the one from before again, and pages past that go back. NULL: every row got them
  */
 typedef struct {
   const float *target_probs;
@@ -630,6 +636,7 @@ typedef struct {
   int32_t q_len;
   int32_t vocab;
   int32_t free_capacity;
+  const int32_t *seq_lens_before;
 } da_verify_args;
 
 /*
@@ -639,7 +646,7 @@ typedef struct {
  * else from the target after the last draft: the first token whose running sum of weights, from token 0 on,
  * passes u_{Q-1} times the sum of all. So tokens are distributed as the target's own. Sums are good to
  * 2^-40 of themselves; weights need not sum to 1; NaN and negative ones count as 0. Lengths out of
- * range stay as they are (DA_DEVERR_SEQ_LEN); ids outside the pool are not given back
+ * range (past the capacity, fewer than the rejected tokens, fewer than before the step) stay as they are (DA_DEVERR_SEQ_LEN); ids outside the pool are not given back
  * (DA_DEVERR_PAGE_INDEX), nor pages that the stack has no room for (DA_DEVERR_NO_PAGES). One kernel; it takes
  * the workspace as the cache calls do, two that give pages back not at once. The context gives batch and the cache's
  * layout. No output may overlap an input except where said. vocab at most 2^21.
