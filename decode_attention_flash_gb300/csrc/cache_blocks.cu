@@ -10,13 +10,15 @@
 // of n calls could add half a step. An e4m3 code keeps its precision under any scale; an integer
 // loses half a bit on average.
 //
-// The layout. The tokens of one block (a run, neighbours in slot_map) are the work of a group of
-// n / 16 warps, for one head and K or V: a warp stages 16 of their rows in shared memory by asynchronous
+// The layout. The tokens of one block (a run, neighbours in slot_map but for tokens without a place) are the work of
+// a group of n / 16 warps, for one head and K or V: a warp stages 16 of their rows in shared memory by asynchronous
 // copies and turns them in place (two rows of 16 lanes at a time, as in cache_rows.cu); the greatest |x| of
 // the group's warps meets in shared memory; then the rows go out as codes. So a row is read once. Only where
 // the scale grew the group reads the block's other rows, 16 a warp, and writes them rounded again. Runs are
 // found by the warps themselves: a group looks through a window of tokens for those whose predecessor is in
-// another block. Queries are the other blocks of the grid, as in cache_rows.cu.
+// another block. Padding and slots outside the cache have no block: both that predecessor and the run's next token are
+// looked for past them, so no two groups have the same block (4096 tokens of padding behind a prefill of 4096: 2 us
+// with blocks of 16, 8 with blocks of 256). Queries are the other blocks of the grid, as in cache_rows.cu.
 //
 // What bounds it. A decode step is latency: 64 tokens of 32 + 16 heads, blocks of 64: 4.7 us (queries alone
 // 2.5); four warps a group there, most with nothing to do, made two waves of blocks: 7.3. A prefill of 4096 such
@@ -35,7 +37,7 @@ namespace {
 
 constexpr int kRows = 16;      // rows of a run, and of a block, that a warp has (of few tokens up to kFewRows)
 constexpr int kFewRows = 64;
-constexpr int kLook = 30;      // tokens that a group looks at together for runs that start there
+constexpr int kLook = 30;      // tokens that a group looks at together for runs that start there (at most)
 constexpr int kMinWarps = 4;   // of a CTA
 constexpr int kMaxWarps = 16;
 constexpr int kPerSm = 4;      // CTAs of kMinWarps an SM
@@ -111,6 +113,39 @@ __device__ __forceinline__ uint32_t again4(uint32_t w, float ratio) {
   return codes4<INT>(x[0] * ratio, x[1] * ratio, x[2] * ratio, x[3] * ratio);
 }
 
+// The slots of a call, and the block of one: -1 for padding, and outside the cache.
+struct Slots {
+  const int64_t *map;
+  int64_t end;
+  int tokens, shift;
+  __device__ __forceinline__ int64_t block_of(int64_t slot) const { return slot < 0 || slot >= end ? -1 : slot >> shift; }
+  __device__ __forceinline__ int64_t at(int64_t t) const { return t >= 0 && t < tokens ? map[t] : -1; }
+};
+// Past tokens without a block, by a warp: the first that has one of t, t + step, .. (step 1 or -1), -1: none has, and
+// its block. 256 tokens a trip to memory. (A function that is called: inlined, its instructions stand in the way of
+// those that every call needs, 0.2 to 0.6 us; of 512 tokens a trip, its registers spill the caller's.)
+constexpr int kFar = 8;
+__device__ __noinline__ int64_t next_block(const int64_t *map, int64_t end, int tokens, int shift, int64_t t, int step, int64_t &blk) {
+  const Slots s = {map, end, tokens, shift};
+  const int lane = threadIdx.x & 31;
+  for (; t >= 0 && t < tokens; t += 32 * kFar * step) {
+    int64_t slot[kFar];
+#pragma unroll
+    for (int k = 0; k < kFar; ++k) slot[k] = s.at(t + (32 * k + lane) * step);
+#pragma unroll
+    for (int k = 0; k < kFar; ++k) {
+      blk = s.block_of(slot[k]);
+      const uint32_t some = __ballot_sync(0xffffffffu, blk >= 0);
+      if (some) {
+        blk = __shfl_sync(0xffffffffu, blk, __ffs(some) - 1);
+        return t + (32 * k + __ffs(some) - 1) * step;
+      }
+    }
+  }
+  blk = -1;
+  return -1;
+}
+
 // Whether every position that turns a pair of token t is in the table.
 __device__ __forceinline__ bool positions_ok(const BlockRowParams &p, int64_t t) {
   bool ok = true;
@@ -128,6 +163,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
                                                                        const int kv_blocks) {
   extern __shared__ uint4 staged_all[];  // [warp][row][16]
   __shared__ uint32_t written_all[kMinWarps][256 / 32];  // rows of the block that the run writes, per group
+  __shared__ int2 place_all[kMaxWarps * kRows];  // a row's token (past the run's first) and position in the block
   __shared__ float amax_all[kMaxWarps];
   __shared__ uint32_t leads_all[kMinWarps][2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -176,22 +212,34 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
   const int partner = lane - kl + (turned && !p.rope_adjacent ? (second ? kl - r : kl + r) : kl);
   const bool norm = NORM && side == 0 && p.k_weight != nullptr;
   uint4 *mine_at = staged_all + (warp * R + sub) * 16 + kl;  // this lane's part of every second row
+  int2 *place = place_all + warp * R;
+  const Slots slots = {p.slot_map, p.num_slots, p.num_tokens, shift};
 
-  auto block_of = [&](int64_t slot) -> int64_t { return slot < 0 || slot >= p.num_slots ? -1 : slot >> shift; };
   uint32_t err = 0;
   const int64_t w1 = min(w0 + p.window, (int64_t)p.num_tokens);
   uint32_t leads = 0, alone = 0;  // of kLook tokens, those whose run starts there, and those whose run is one token
   int64_t from = w0 - kLook;
+  const int ahead = (32 - min(p.window, kLook)) / 2;  // tokens before those, to see whose run they are in
   while (true) {
     while (leads == 0 && (from += kLook) < w1) {
-      // lane i: the slot of token from + i; the last lane that of the token before
-      const int64_t t = lane == 31 ? from - 1 : from + lane;
-      const bool mine = lane < kLook && t < w1;
-      const int64_t slot = t >= 0 && t < p.num_tokens ? p.slot_map[t] : -1, blk = block_of(slot);
+      // lane i: the slot of token from - ahead + i
+      const int64_t t = from - ahead + lane;
+      const bool mine = lane >= ahead && lane < ahead + kLook && t < w1;
+      const int64_t slot = slots.at(t), blk = slots.block_of(slot);
       if (mine && blk < 0 && slot != -1) err |= DA_DEVERR_SLOT;
-      const int64_t before = __shfl_sync(0xffffffffu, blk, (lane + 31) & 31), after = __shfl_sync(0xffffffffu, blk, (lane + 1) & 31);
-      leads = __ballot_sync(0xffffffffu, mine && blk >= 0 && before != blk);
-      alone = __ballot_sync(0xffffffffu, after != blk);
+      // the blocks of the tokens before and after this one that have one
+      const uint32_t some = __ballot_sync(0xffffffffu, blk >= 0);
+      const uint32_t down = some & ((1u << lane) - 1u), up = some & ~((2u << lane) - 1u);
+      int64_t before = __shfl_sync(0xffffffffu, blk, 31 - __clz(down));  // (any lane's, if there is none)
+      const int64_t after = __shfl_sync(0xffffffffu, blk, __ffs(up) - 1);
+      if (!down) before = -1;
+      if (from > ahead && gwarp == 0 && __any_sync(0xffffffffu, mine && blk >= 0 && !down)) {
+        int64_t far;
+        next_block(slots.map, slots.end, slots.tokens, shift, from - ahead - 1, -1, far);
+        if (!down) before = far;
+      }
+      leads = __ballot_sync(0xffffffffu, mine && blk >= 0 && before != blk) >> ahead;
+      alone = __ballot_sync(0xffffffffu, up ? after != blk : from - ahead + 32 >= p.num_tokens) >> ahead;
       if (gw > 1) {  // (the group's warps meet below: what its first one saw holds for all)
         if (gwarp == 0 && lane == 0) leads_all[group][0] = leads, leads_all[group][1] = alone;
         meet();
@@ -203,67 +251,62 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
     if (leads == 0) break;
     const int first = __ffs(leads) - 1;
     leads &= leads - 1;
-    const int64_t t0 = from + first, blk = block_of(p.slot_map[t0]);
-    const int run_most = (alone >> first) & 1u ? 1 : n;  // (a decode step: the tokens after it are not looked at)
+    const int64_t t0 = from + first, blk = slots.block_of(slots.map[t0]);
+    const bool single = (alone >> first) & 1u;  // (a decode step: the tokens after it are not looked at)
     const uint32_t per = (uint32_t)p.rows_per_page >> shift;  // blocks of a page
     const int64_t page = (blk >> 32) == 0 ? (int64_t)((uint32_t)blk / per) : blk / per, j = blk - page * per;
     const int64_t row0 = (page * HK + h) * p.rows_per_page + j * n;
     float *scale = scales + (page * HK + h) * per + j;
     const float was = *scale;
-    // ---- which tokens, and which rows they write
+    // ---- which tokens, and which rows they write; the k-th of them is row k % R of the group's warp k / R
     bool fresh = false;
-    uint64_t mine = 0;            // of the warp's R tokens, those that are written
-    int off_lo = 0, off_hi = 0;   // lane i: the rows of tokens i and 32 + i of those
-    const int in32 = gwarp * R & 31;  // where they begin among 32
-    for (int base = 0; base < n; base += 32) {
-      const int64_t t = t0 + base + lane;
-      const bool in = base + lane < run_most && t < p.num_tokens;
-      const int64_t slot = in ? p.slot_map[t] : -1;
-      const bool same = in && block_of(slot) == blk;
-      const uint32_t run = __ballot_sync(0xffffffffu, same);
-      const int m = run == 0xffffffffu ? 32 : __ffs(~run) - 1;  // up to the first of another block
-      bool use = lane < m;
-      if (use && !positions_ok(p, t)) {
+    int count = 0;
+    if (gwarp == 0 && lane < 8) written[lane] = 0;
+    __syncwarp();
+    for (int64_t t = t0;;) {
+      const int64_t i = t + lane;
+      const int64_t slot = lane == 0 || !single ? slots.at(i) : -1, b = slots.block_of(slot);
+      const uint32_t others = __ballot_sync(0xffffffffu, b >= 0 && b != blk);
+      bool use = b == blk && (others == 0 || lane < __ffs(others) - 1);  // up to the first of another block
+      if (use && !positions_ok(p, i)) {
         err |= DA_DEVERR_POSITION;
         use = false;
       }
-      const int off = use ? (int)(slot & (n - 1)) : -1;
-      fresh = fresh || __any_sync(0xffffffffu, off == 0);
+      const int off = (int)(slot & (n - 1));
+      fresh = fresh || __any_sync(0xffffffffu, use && off == 0);
       const uint32_t used = __ballot_sync(0xffffffffu, use);
-      const int o = __shfl_sync(0xffffffffu, off, (in32 + lane) & 31), at = base - (gwarp * R & ~31);
-      if (at == 0) {
-        mine |= (used >> in32) & (R < 32 ? 0xFFFFu : 0xFFFFFFFFu);
-        off_lo = o;
-      } else if (at == 32 && R == 64) {
-        mine |= (uint64_t)used << 32;
-        off_hi = o;
+      const uint32_t k = count + __popc(used & ((1u << lane) - 1u)) - gwarp * R;
+      if (use && k < (uint32_t)R) place[k] = make_int2((int)(i - t0), off);
+      if (use && gwarp == 0) atomicOr(&written[off >> 5], 1u << (off & 31));
+      count += __popc(used);
+      t += 32;
+      if (others || single || count >= n || t >= p.num_tokens) break;
+      if (__shfl_sync(0xffffffffu, b, 31) < 0) {
+        int64_t found;
+        t = next_block(slots.map, slots.end, slots.tokens, shift, t, 1, found);
+        if (found != blk) break;
       }
-      if (gwarp == 0) {  // (a run of one block: every row once)
-        if (base == 0 && lane < 8) written[lane] = 0;
-        __syncwarp();
-        if (use) atomicOr(&written[off >> 5], 1u << (off & 31));
-      }
-      if (m < 32) break;
     }
+    __syncwarp();
     // ---- the warp's rows: read, normed, turned, in bf16
-    const int64_t t1 = t0 + gwarp * R + sub;
-    const int pairs = (64 - __clzll((long long)mine) + 1) / 2;  // of rows, up to the warp's last
-#pragma unroll 8
+    const int have = min(max(count - gwarp * R, 0), R), pairs = (have + 1) / 2;
+#pragma unroll 4
     for (int i = 0; i < pairs; ++i)
-      if ((mine >> (2 * i + sub)) & 1u) cp_async_16(smem_u32(mine_at + 32 * i), src + (t1 + 2 * i) * stride + kl);
+      if (2 * i + sub < have) cp_async_16(smem_u32(mine_at + 32 * i), src + (t0 + place[2 * i + sub].x) * stride + kl);
     cp_async_commit();
     uint32_t top2 = 0;
     const int pair0 = p.rope_adjacent ? 4 * kl : 8 * (second ? kl - r : kl);
     cp_async_wait_group<0>();  // (a lane reads what it copied itself)
     // (the next rows' angles are in flight while these are turned)
     auto angles = [&](int i, float (&c)[8], float (&s)[8]) {
-      if (!turned || i >= pairs || !((mine >> (2 * i + sub)) & 1u)) return;
-      if (p.rope_adjacent) load_turn<4>(p, t1 + 2 * i, pair0, c, s);
-      else load_turn<8>(p, t1 + 2 * i, pair0, c, s);
+      if (!turned || 2 * i + sub >= have) return;
+      const int64_t t = t0 + place[2 * i + sub].x;
+      if (p.rope_adjacent) load_turn<4>(p, t, pair0, c, s);
+      else load_turn<8>(p, t, pair0, c, s);
     };
     auto turn_rows = [&](int i, float (&c)[8], float (&s)[8]) {
       if (i >= pairs) return;
-      const bool on = (mine >> (2 * i + sub)) & 1u;
+      const bool on = 2 * i + sub < have;
       uint4 x = on ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
       if (r > 0 || norm) {
         if (norm) {
@@ -293,7 +336,7 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
     } else {
 #pragma unroll 2
       for (int i = 0; i < pairs; ++i) {
-        const uint4 x = (mine >> (2 * i + sub)) & 1u ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
+        const uint4 x = 2 * i + sub < have ? mine_at[32 * i] : make_uint4(0u, 0u, 0u, 0u);
         top2 = max_abs2<INT>(max_abs2<INT>(top2, x.x), x.y);
         top2 = max_abs2<INT>(max_abs2<INT>(top2, x.z), x.w);
       }
@@ -311,10 +354,9 @@ __global__ void __launch_bounds__(WARPS * 32, WARPS == kMinWarps ? kPerSm : 1) a
     const bool finite = top < __int_as_float(0x7f800000);
     uint8_t *out = cache + row0 * 128 + kl * 8;
 #pragma unroll 2
-    for (int i = 0; i < pairs; ++i) {
-      const int off = __shfl_sync(0xffffffffu, 2 * i < 32 ? off_lo : off_hi, (2 * i + sub) & 31);
-      if ((mine >> (2 * i + sub)) & 1u) *reinterpret_cast<uint2 *>(out + off * 128) = codes8<INT>(mine_at[32 * i], inv, finite);
-    }
+    for (int i = 0; i < pairs; ++i)
+      if (2 * i + sub < have)
+        *reinterpret_cast<uint2 *>(out + place[2 * i + sub].y * 128) = codes8<INT>(mine_at[32 * i], inv, finite);
     // ---- rows that stay, rounded again
     if (!fresh && now > old) {
       const float ratio = old * inv;

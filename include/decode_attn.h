@@ -526,8 +526,9 @@ typedef struct {
  *                e4m3 codes above the subnormal ones stay exact, integers end within one step).
  *                Infinities saturate; e4m3 keeps a NaN as a NaN code, and integers make the scale,
  *                so the block, NaN until it is started anew. Tokens of a call that belong to one
- *                block of the cache stand next to each other in slot_map, nothing between them (as
- *                decode_attn_build_tables lists them); k_scale and v_scale are written
+ *                block of the cache stand next to each other in slot_map, in any order (as
+ *                decode_attn_build_tables lists them): padding and slots outside the cache may stand
+ *                between them, tokens of other blocks not; k_scale and v_scale are written
  * (rows outside f16's range make an infinite scale or shift). A slot outside the
  * cache (DA_DEVERR_SLOT) or a position outside the table (DA_DEVERR_POSITION) skips
  * its token whole. Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE, NOT_PLANNED, CUDA.
