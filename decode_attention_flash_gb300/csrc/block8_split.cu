@@ -7,9 +7,12 @@
 // with the products on f16 operands with fp32 sums and the scales applied to them in fp32: any
 // fp32 scale serves. With sixteen rows a unit, where the scheduler's issue is what bounds the kernel, the V
 // scale joins the weights instead, over a power of two that O is in units of (but where it is far below
-// that, or not finite), and integers meet Q as u 2^-24, u the code plus 128, the f16 whose bits are u: what
-// the 128 adds is the same for every token and is taken off the score in fp32. (With eight rows, which HBM
-// bounds, both cost more than they save: one row of 131072 tokens, 64 heads, integers: 56.6 -> 59.0 us.)
+// that, or not finite). With eight rows, which HBM bounds, that costs more than it saves. Roundings: the weights
+// meet V as f16 (11 bits, as the codes' products with them need no more for a bf16 output: 2^-11 of a weight; the
+// smallest step is 2^-29 of the greatest weight, or 2^-25 where a V scale is joined that is 2^-4 of its reference),
+// everything else is fp32. (Integers as code plus 128, whose bits are an f16 as they stand, with 128 sum q taken off
+// the score: a subtraction less for two codes, no time, 95.6 us either way, and scores that are differences of two
+// great sums: off by 1.7e-3 where these are by 3e-6.)
 //
 // What bounds it. 16 positions of one kv head are 4096 bytes, 732 cycles of a scheduler at the
 // measured copy bandwidth; their conversions, products and weights take about 250. So HBM does.
@@ -46,11 +49,6 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t 
     hi = e4m3x2_to_f16x2((uint16_t)(w >> 16));
   }
 }
-// The same with the bytes u as f16 of those bits, u 2^-24.
-__device__ __forceinline__ void bits_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-  lo = prmt(w, 0u, 0x4140);
-  hi = prmt(w, 0u, 0x4342);
-}
 template <bool INT>
 __device__ __forceinline__ uint32_t biased(uint32_t w) {
   return INT ? w ^ 0x80808080u : w;
@@ -72,7 +70,6 @@ struct Block8Format {
   static constexpr bool kCareful = true;
   static constexpr bool kBlockScales = true;
   static constexpr bool kFoldsV = ROWS == 2;
-  static constexpr bool kBiased = INT && ROWS == 2;
   static constexpr int kWarps(int nt) { return nt == 1 ? 7 : 11; }
   static constexpr int kStages(int) { return 3; }
   static constexpr bool kQShared(int nt) { return nt == 2; }
@@ -104,35 +101,9 @@ struct Block8Format {
   __device__ static __forceinline__ float v_scale(const uint8_t *scales, int gi) {
     return reinterpret_cast<const float *>(scales)[kH + gi];
   }
-  // 128 times the sum of a query's elements (this lane: a quarter of row r8's), for the lane's score columns.
-  template <int NT>
-  __device__ static __forceinline__ void bias(const uint32_t (&qf)[NT][8][2], const uint4 *qs, int lane, float (&qbias)[NT][2]) {
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      float sum = 0.f;
-#pragma unroll
-      for (int s = 0; s < 8; ++s)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          uint32_t w;
-          if constexpr (kQShared(NT)) {
-            const uint4 q = qs[s * 32];
-            w = nt ? (k ? q.w : q.z) : (k ? q.y : q.x);
-          } else {
-            w = qf[nt][s][k];
-          }
-          const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w));
-          sum += f.x + f.y;
-        }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) qbias[nt][e] = 128.f * __shfl_sync(0xffffffffu, sum, (2 * (lane & 3) + e) * 4);
-    }
-  }
   template <int NT>
   __device__ __forceinline__ void scores(const uint8_t *stage, const uint8_t *scales, const uint32_t (&qf)[NT][8][2],
-                                         const uint4 *qs, const float (&qbias)[NT][2], float (&s)[NT][kH][4]) const {
+                                         const uint4 *qs, float (&s)[NT][kH][4]) const {
     const float *ks = reinterpret_cast<const float *>(scales);
 #pragma unroll
     for (int gi = 0; gi < kH; ++gi) {
@@ -147,13 +118,8 @@ struct Block8Format {
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         uint32_t a0, a1, a2, a3;
-        if (kBiased) {
-          bits_to_f16(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
-          bits_to_f16(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
-        } else {
-          codes_to_f16<INT>(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
-          codes_to_f16<INT>(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
-        }
+        codes_to_f16<INT>(biased<INT>(word(a[c >> 2], c & 3)), a0, a2);
+        codes_to_f16<INT>(biased<INT>(word(b[c >> 2], c & 3)), a1, a3);
         if constexpr (kQShared(NT)) {
           const uint4 q = qs[c * 32];
           mma_f16_16816(s[0][gi], a0, a1, a2, a3, q.x, q.y);
@@ -166,10 +132,7 @@ struct Block8Format {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if (kBiased) s[nt][gi][e] = fmaf(s[nt][gi][e], 0x1p24f, -qbias[nt][e & 1]);
-          s[nt][gi][e] *= ks[gi];
-        }
+        for (int e = 0; e < 4; ++e) s[nt][gi][e] *= ks[gi];
     }
   }
   // Masked tokens weigh 0: their rows must not hold NaN codes, nor a granule that was not copied

@@ -85,7 +85,6 @@ struct Fp4Format {
   static constexpr bool kCareful = false;
   static constexpr bool kBlockScales = false;
   static constexpr bool kFoldsV = false;
-  static constexpr bool kBiased = false;
   static constexpr int kWarps(int nt) { return nt == 1 ? 15 : 11; }  // with the walker four (three) a scheduler
   static constexpr int kStages(int) { return 3; }
   // Q^T fragments: registers for up to eight rows; for sixteen, whose O takes 64
@@ -115,7 +114,7 @@ struct Fp4Format {
   }
   template <int NT>
   __device__ __forceinline__ void scores(const uint8_t *stage, const uint8_t *, const uint32_t (&qf)[NT][8][2],
-                                         const uint4 *qs, const float (&)[NT][2], float (&s)[NT][2][4]) const {
+                                         const uint4 *qs, float (&s)[NT][2][4]) const {
     uint4 ra[2], rb[2];
     uint32_t sa[2], sb[2];
 #pragma unroll

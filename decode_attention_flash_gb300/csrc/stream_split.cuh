@@ -1,5 +1,5 @@
 // stream_split.cuh -- persistent split-KV GQA decode whose warps stream alone, over the formats
-// of a cache in granules of 16 rows (fp4_split.cu, block8_split.cuh).
+// of a cache in granules of 16 rows (fp4_split.cu, block8_split.cu).
 //
 // The mathematics is the online softmax of gqa_split.cuh with the query group as the MMA's N
 // dimension (mma.sync m16n8k16, f16 operands, fp32 sums):
@@ -40,7 +40,7 @@ constexpr float kRaise = 32768.f;    // a sum of weights past this raises the re
 // A format F of the cache is a struct of constants (tokens of a stage, granule bytes, streaming
 // warps, stages of a ring, bytes of scales beside a stage) and of what a lane does: copy a half
 // of a stage, S^T = K Q^T, drop what masked tokens hold, O^T += V^T P^T. kHeadScales: K and V have
-// a scale a head; kBlockScales: a scale a granule, which kFoldsV joins to the weights; kBiased: K codes meet Q with a bias added.
+// a scale a head; kBlockScales: a scale a granule, which kFoldsV joins to the weights.
 template <class F, int NT>
 struct StreamLayout {
   static constexpr int kT = F::kT;                               // tokens per stage
@@ -568,7 +568,6 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
       }
     // (kFoldsV) O is in units of vref, a power of two not below any V scale of the segment so far
     float vref = 0x1p-126f;
-    float qbias[NT][2];       // (kBiased) what the codes' bias adds to a score
     bool from_start = false;  // the segment holds its unit's first tile
     bool fresh = false;       // no reference for the segment's weights yet
     int unit = 0;
@@ -640,7 +639,6 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
             }
           }
         }
-        if constexpr (F::kBiased) F::template bias<NT>(qf, qs, lane, qbias);
         sscale = p.score_scale * (F::kHeadScales ? p.k_scale[h >> fp.kv_shift] : 1.f) * pow2f(-qexp);
         // a zero factor (uniform weights) as 2^-100: a finite score still weighs 1, and
         // an infinite one (a masked token's) 0
@@ -679,7 +677,7 @@ __device__ __forceinline__ void stream_split(const StreamParams &fp) {
         // keep their instructions apart; what a half that was not copied holds is masked below)
         float s[NT][H][4];
         const uint8_t *scales = side + st * F::kSideBytes;
-        fmt.template scores<NT>(stage, scales, qf, qs, qbias, s);
+        fmt.template scores<NT>(stage, scales, qf, qs, s);
         // ---------------- masks and the online softmax (log2 units)
         const bool part = valid != kAll;
         float f = sscale;  // log2 units of a score in s
