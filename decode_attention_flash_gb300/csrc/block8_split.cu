@@ -20,8 +20,8 @@
 // Measured: 32 rows of 1024..8192 tokens, 8 kv heads of 4 rows: 56.3 us (floor 40.4); one row of 131072, 8 heads of 8
 // rows: 56.7 (39.6). While it streams it takes 97 to 106 % of the copy rate (rows of 16384 tokens against rows of 8192);
 // the first tile is there after 5 us, the last block's warps end 5 us after the median one's, pieces and units
-// that blocks share take 7. Sixteen rows a unit: 16 rows of 1000..20000 tokens, 4 query tokens, 95.5 us (51.4);
-// e4m3 streams at 84 % of the copy rate there, integers at 74 % (907 instructions for 32 tokens, issue 46 %).
+// that blocks share take 7. Sixteen rows a unit: 16 rows of 1000..20000 tokens, 4 query tokens, 95.3 us (51.4);
+// e4m3 streams at 84 % of the copy rate there, integers at 74 % (936 instructions for 32 tokens, issue 47 %).
 // Measured and not kept for eight rows: 9, 11, 13 or 15 warps, one or two stages, tiles of 16 tokens (55 to 61 us).
 //
 // The stage. Rows of 128 bytes land with their eight 16-byte chunks turned by the row: chunk c of
@@ -59,7 +59,8 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int c) {
 
 // Up to eight rows a unit: 32 tokens a stage, seven streaming warps, Q in registers. Sixteen, whose O takes
 // 64 registers: 16 tokens a stage, eleven warps in 168 registers, Q in shared memory (16 rows of 1000..20000
-// tokens, 4 query tokens: 95.7 us; as for eight rows, in 255 registers, 102; fifteen warps in 128: 106).
+// tokens, 4 query tokens: 95.3 us, with 8 to 42 bytes of spills a thread; as for eight rows, in 255 registers, 102;
+// fifteen warps in 128: 106).
 template <bool INT, int ROWS>
 struct Block8Format {
   static constexpr int kT = ROWS == 1 ? 32 : 16;

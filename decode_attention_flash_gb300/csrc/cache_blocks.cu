@@ -24,9 +24,12 @@
 // 2.5); four warps a group there, most with nothing to do, made two waves of blocks: 7.3. A prefill of 4096 such
 // tokens into blocks of 32 takes 27 us against a floor of 13.6: keys wait for their angles (5 of the 10 us that a
 // group takes, now loaded a step ahead), rows of one head and one block are little work for the slots,
-// positions and scales that have to be looked up first, and a scheduler has five warps at most. Measured and not
+// positions and scales that have to be looked up first, and a scheduler has four warps at most. Measured and not
 // kept: rows in registers (32 us then); eight rows a warp (the same); more blocks an SM with spills (32 -> 38);
 // the rows' angles copied to shared memory along with them (27.6 -> 29.7, with three axes 48).
+// Past 256 tokens a group takes the runs of its window one after another, which suits a prefill's long ones. A decode
+// step's short ones wait for each other: one token each of 256, 257, 512 and 1024 rows, 8 heads: 10.9, 20.5, 36.1 and
+// 67.6 us in blocks of 64, 31, 73, 134 and 262 in blocks of 256, 8.8, 8.8, 13.0 and 21.0 in blocks of 16.
 #include <algorithm>
 #include <cstring>
 

@@ -32,8 +32,9 @@
 // latent rows with 128 heads: 13.7 us (78 %; the rope key loaded after the latent row is
 // stored: 14.0).
 // Normed first, head by head (the rows' square sum by shuffles, packed fp32 arithmetic, weights from L1): 66 us for
-// the 16381 tokens, 93 % of the copy rate, and 12 for the latent rows; registers allow seven blocks an SM
-// (six: 68, eight, with spills: 70; weights held in registers: 72).
+// the 16381 tokens, 93 % of the copy rate, and 13.8 for the latent rows (9.0 where L2 holds them); seven blocks an SM
+// of 72 registers, which spill 8 bytes a thread for bf16 and latent rows, 8 to 64 for the quantised ones (six: 68,
+// eight, with more spills: 70; weights held in registers: 72).
 // K first and then V, with a head's address worked out for each row: 65.2, 31.4 and
 // 61.3 us, bound by instruction issue; one row in flight of K and of V instead of two:
 // 65.2, 31.0 and 70.7.

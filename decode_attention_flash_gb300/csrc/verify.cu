@@ -12,9 +12,9 @@
 // a lane's sum over its segments a third float has its rounding errors. With u = 2^-24 (a float's rounding) what is
 // left is at most 100 u^2 of a segment's sum (ten additions, the second float at most ten u by then), 3 u^2 for each
 // addition of two such sums, about fifteen in a row, and 40 u^2 inside the segment that is drawn from: 2^-40 of the
-// sum, however the weights lie; of weights that are all alike 2^-46. (Doubles instead, for every token: 16 cycles of
-// an SM for a warp's one addition; 82.7, 33.0 and 16.0 us for the three below; for the sums of segments alone 44.1,
-// 15.2 and 9.9.) Two such sums side by side take the packed adds.
+// sum, however the weights lie; 2^-50 of a softmax. (Doubles instead, for every token: 16 cycles of an SM for a warp's
+// one addition; 82.7, 33.0 and 16.0 us for the three below; for the sums of segments alone 44.1, 15.2 and 9.9.) Two
+// such sums side by side take the packed adds.
 // A drafted token's product is compared exactly, in 64 bits.
 //
 // What bounds it. One row of p and one of q a batch row, read once: HBM, and latency for few rows.
@@ -22,13 +22,13 @@
 // drafted token), sums its share of the vocabulary in segments of 256, and reads the other
 // CTAs' sums through the cluster; the one whose share holds the border finds its segment and looks at
 // that again, from L2.
-// Measured: 256 rows of 128000, four drafts each: 41 us. A row that keeps all its drafts reads no draft's
-// distribution, so 175 MB there, 4.2 TB/s: rows of one distribution and of two lie side by side, and an SM that
-// has more of the second ends later (CTAs of 256 threads, half as many: 43). 64 rows of 151937, no draft's: 14 us
-// from L2 (floor 5.8): 7 us a row has beside its stream (drafts, then their probabilities, then the sums' way
-// through the cluster and back). 4 rows of 32000: 8.9 us, latency, 2.4 of them the pages' return (a count of the
-// rows, then lengths, then table entries). Segments of 512 instead of 256: 9.5, 15.2 and 44.1 us where these took
-// 8.5, 15.3 and 43.4; of 128: 8.2, 15.5 and 51.2. A warp's reduction for each segment's sum alone, not four at
+// Measured: 256 rows of 128000, four drafts each: 42 us. A row that keeps all its drafts reads no draft's
+// distribution, so 175 MB there, 4.2 TB/s (floor 25.8): rows of one distribution and of two lie side by side, and an
+// SM that has more of the second ends later (CTAs of 256 threads, half as many: 43 where these took 41). 64 rows of
+// 151937, no draft's: 14 us from L2 (floor 5.8): 7 us a row has beside its stream (drafts, then their probabilities,
+// then the sums' way through the cluster and back). 4 rows of 32000: 9.2 us, latency, 2.4 of them the pages' return (a
+// count of the rows, then lengths, then table entries). Segments of 512 instead of 256: 9.5, 15.2 and 44.1 us where
+// these took 8.5, 15.3 and 43.4; of 128: 8.2, 15.5 and 51.2. A warp's reduction for each segment's sum alone, not four at
 // once: 16.9 and 45.
 #include <algorithm>
 
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 8) verify_kernel(const __grid_consta
 }  // namespace
 
 // CTAs of a cluster: as many as the SMs hold at once (eight each) and as leave each half a segment a warp.
-// 256 rows of 128000: four CTAs a row 41 us, two 52, eight 44. The sums of a CTA's segments fit 40 KB.
+// 256 rows of 128000: four CTAs a row 42 us; with the sums before these 41, two 52, eight 44. The sums of a CTA's segments fit 40 KB.
 static int verify_ctas(const VerifyParams &p, int num_sms) {
   if (p.target_tokens) return 1;
   int c = kMaxCtas;
