@@ -646,7 +646,8 @@ typedef struct {
  * accepted ones is drawn from max(p_i - q_i, 0) where token i was rejected (from p_i where that is 0 everywhere),
  * else from the target after the last draft: the first token whose running sum of weights, from token 0 on,
  * passes u_{Q-1} times the sum of all. So tokens are distributed as the target's own. Sums are good to
- * 2^-40 of themselves; weights need not sum to 1; NaN and negative ones count as 0. Lengths out of range (past the
+ * 2^-40 of themselves (above 2^-100; one that is not finite counts as no weight at all); weights need not sum to 1;
+ * NaN and negative ones count as 0. Lengths out of range (past the
  * capacity, fewer than the rejected tokens, fewer than before the step) stay as they are (DA_DEVERR_SEQ_LEN); ids
  * outside the pool are not given back (DA_DEVERR_PAGE_INDEX), nor pages that the stack has no room for
  * (DA_DEVERR_NO_PAGES). One kernel; it takes the workspace as the cache calls do, two that give pages back not at
